@@ -25,6 +25,8 @@ __all__ = ["grpo_workspace_size", "grpo_group_adv", "grpo_loss_fwd_bwd", "grpo_l
            "grpo_loss_from_logps", "grpo_count_active", "grpo_loss_finalize", "Shard",
            "totals_buffer", "SEQ_TOTAL_BYTES", "grpo_vocab_chunk", "grpo_vocab_partials",
            "grpo_vocab_loss", "grpo_vocab_grad",
+           "grpo_token_logps", "grpo_token_logps_grad", "grpo_clip_grad_norm",
+           "grpo_clip_workspace_size", "status_buffer", "GRPO_MAX_TOP_K",
            "grpo_read_device_status", "grpo_status_string", "GrpoError", "library_path",
            "GRPO_ADV_EPS_ADD", "GRPO_SKIP_MASKED_GRAD_ROWS"]
 
@@ -35,6 +37,8 @@ GRPO_FLAG_WORKSPACE_CLEAN = 8  # grpo_loss_from_logps: the header is clean, skip
 GRPO_FLAG_OVERLAP_LAUNCH = 16  # grpo_loss_from_logps: dispatch while the previous kernel ends
 GRPO_FLAG_TEST_STALLED_COPY = 0x80000000  # test hook (see include/grpo.h)
 GRPO_FLAG_TEST_STALLED_BARRIER = 0x40000000  # test hook (see include/grpo.h)
+GRPO_MAX_TOP_K = 32  # grpo_token_logps: most alternatives of a token
+GRPO_CLIP_NORM_ONLY = 1  # grpo_clip_grad_norm: read only
 GRPO_ERR_ACTION_RANGE = 16  # device-detected status bits (grpo_read_device_status)
 GRPO_ERR_CSR = 32
 GRPO_ERR_NONFINITE_REWARD = 64
@@ -145,6 +149,17 @@ def lib():
         L.grpo_vocab_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, vp, vp, vp, vp, u32,
                                       vp]
         L.grpo_vocab_grad.restype = ctypes.c_int
+        i32 = ctypes.c_int32
+        L.grpo_token_logps.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, vp, f32, i32,
+                                       vp, vp, vp, vp, vp, vp, vp]
+        L.grpo_token_logps.restype = ctypes.c_int
+        L.grpo_token_logps_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, vp, vp,
+                                            vp, vp, vp, f32, vp, i64, i64, u32, vp, vp]
+        L.grpo_token_logps_grad.restype = ctypes.c_int
+        L.grpo_clip_workspace_size.argtypes = [i64]
+        L.grpo_clip_workspace_size.restype = sz
+        L.grpo_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, f32, f32, f32, u32, vp, vp, sz, vp]
+        L.grpo_clip_grad_norm.restype = ctypes.c_int
         L.grpo_read_device_status.argtypes = [vp, vp]
         L.grpo_read_device_status.restype = ctypes.c_int
         L.grpo_status_string.argtypes = [ctypes.c_int]
@@ -585,6 +600,234 @@ def grpo_vocab_grad(policy_slice: torch.Tensor, action_ids: torch.Tensor,
                                  _ptr(grad), GRPO_SKIP_MASKED_GRAD_ROWS if skip_masked_grad_rows
                                  else 0, _stream(stream)), "grpo_vocab_grad")
     return grad
+
+
+# --------------------------------------------------------------------------
+# log-probs of given tokens, their gradient, and the gradient norm
+def status_buffer(device="cuda") -> torch.Tensor:
+    """A zeroed status word (256 bytes) for ``status=`` of the token entry
+    points; read it with grpo_read_device_status."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _rows(x, name: str):
+    """(B, T, V, stride_b, stride_t) of logits [B, T, V] or [N, V] whose rows
+    hold adjacent elements; any strides between rows."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported {name} dtype {getattr(x, 'dtype', None)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3:
+        B, T, V = shape
+        sb, st, sv = stride
+    elif len(shape) == 2:
+        (B, V), T, st = shape, 1, 0
+        sb, sv = stride
+    else:
+        raise ValueError(f"{name} must be [B, T, V] or [N, V]")
+    if sv != 1 and V > 1:
+        raise ValueError(f"the logits of a row of {name} must be adjacent (stride 1)")
+    return B, T, V, sb, st
+
+
+def _token(t, name: str, lead, dtype, device):
+    """The pointer of a contiguous per-token tensor of shape ``lead`` (None
+    for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != lead or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(lead)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _token_mask(mask, lead, device):
+    if mask is None:
+        return None
+    if mask.dtype != torch.bool and mask.dtype != torch.uint8:
+        raise ValueError("completion_mask must be bool or uint8")
+    return _token(mask, "completion_mask", lead, mask.dtype, device)
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    if status.device != device or not status.is_contiguous() or status.nbytes < 256:
+        raise ValueError("status must be a status_buffer() on the device of the logits")
+    return status.data_ptr()
+
+
+class _AllocateOn:
+    """Outputs of a call on another stream than the current one belong to
+    that stream: memory is taken from its pool, not reused under it."""
+
+    def __init__(self, stream):
+        self.ctx = None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def grpo_token_logps(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
+                     completion_mask: Optional[torch.Tensor] = None, *, temperature: float = 1.0,
+                     top_k: int = 0, want_entropy: bool = False, want_stats: bool = False,
+                     status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Log-probs of given tokens, with entropy and top alternatives.
+
+    ``logits`` [B, T, V] or [N, V] (f32, bf16, f16), rows of adjacent
+    elements at any strides; ``action_ids`` int64 and ``completion_mask``
+    (bool / uint8, None = all active) of the leading shape, contiguous.
+    ``action_ids=None`` leaves the log-probs out.  Returns a dict of device
+    tensors: ``logps`` (f32; 0 on masked tokens), ``entropy`` (f32, with
+    ``want_entropy``), ``stats`` (f32 [2, ...], with ``want_stats``: what
+    grpo_token_logps_grad needs), ``top_ids`` (int64 [..., top_k]; -1 on
+    masked tokens) and ``top_logps`` (f32; equal logits by lowest index
+    first).  ``status``: a ``status_buffer()`` that collects
+    GRPO_ERR_ACTION_RANGE.  See include/grpo.h for rows without a
+    distribution."""
+    B, T, V, sb, st = _rows(logits, "logits")
+    lead, dev = logits.shape[:-1], logits.device
+    ids = _token(action_ids, "action_ids", lead, torch.int64, dev)
+    mask = _token_mask(completion_mask, lead, dev)
+    with _AllocateOn(stream):
+        empty = torch.empty
+        logps = None if ids is None else empty(lead, dtype=torch.float32, device=dev)
+        entropy = empty(lead, dtype=torch.float32, device=dev) if want_entropy else None
+        stats = empty((2, *lead), dtype=torch.float32, device=dev) if want_stats else None
+        top_ids = top_logps = None
+        if top_k:
+            top_ids = empty((*lead, top_k), dtype=torch.int64, device=dev)
+            top_logps = empty((*lead, top_k), dtype=torch.float32, device=dev)
+    rc = lib().grpo_token_logps(logits.data_ptr(), _DTYPES[logits.dtype], B, T, V, sb, st, ids,
+                                mask, temperature, top_k, _ptr(logps), _ptr(entropy), _ptr(stats),
+                                _ptr(top_ids), _ptr(top_logps), _status_ptr(status, dev),
+                                _stream(stream))
+    _check(rc, "grpo_token_logps")
+    return {"logps": logps, "entropy": entropy, "stats": stats, "top_ids": top_ids,
+            "top_logps": top_logps}
+
+
+def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
+                          completion_mask: Optional[torch.Tensor], stats: torch.Tensor, *,
+                          grad_logps: Optional[torch.Tensor] = None,
+                          entropy: Optional[torch.Tensor] = None,
+                          grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                          grad: Optional[torch.Tensor] = None, skip_masked_grad_rows: bool = False,
+                          status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dL/dlogits from dL/dlogps (``grad_logps``, e.g. the ``grad`` of
+    grpo_loss_from_logps) and dL/dentropy (``grad_entropy``, with the
+    forward's ``entropy``); at least one of the two.  ``stats`` is the
+    forward's at the same temperature.  ``grad``: a tensor to write into (any
+    row strides; ``logits`` itself for an in-place gradient), else a new
+    contiguous one of the logits' dtype."""
+    B, T, V, sb, st = _rows(logits, "logits")
+    lead, dev = logits.shape[:-1], logits.device
+    ids = _token(action_ids, "action_ids", lead, torch.int64, dev)
+    mask = _token_mask(completion_mask, lead, dev)
+    f32 = torch.float32
+    stats_p = _token(stats, "stats", torch.Size((2, *lead)), f32, dev)
+    ent = _token(entropy, "entropy", lead, f32, dev)
+    dlogp = _token(grad_logps, "grad_logps", lead, f32, dev)
+    dent = _token(grad_entropy, "grad_entropy", lead, f32, dev)
+    if grad is None:
+        with _AllocateOn(stream):
+            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    elif grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != dev:
+        raise ValueError("grad must have the shape, dtype and device of logits")
+    _, _, _, gsb, gst = _rows(grad, "grad")
+    rc = lib().grpo_token_logps_grad(logits.data_ptr(), _DTYPES[logits.dtype], B, T, V, sb, st,
+                                     ids, mask, stats_p, ent, dlogp, dent, temperature,
+                                     grad.data_ptr(), gsb, gst,
+                                     GRPO_SKIP_MASKED_GRAD_ROWS if skip_masked_grad_rows else 0,
+                                     _status_ptr(status, dev), _stream(stream))
+    _check(rc, "grpo_token_logps_grad")
+    return grad
+
+
+def grpo_clip_workspace_size(num_tensors: int) -> int:
+    return int(lib().grpo_clip_workspace_size(num_tensors))
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one range of memory without gaps (any order:
+    contiguous, transposed, channels-last)."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: float = 1.0,
+                        out=None, norm_only: bool = False,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """The global L2 norm of ``scale`` x ``tensors`` (f32, bf16, f16 in any
+    mixture; each dense in memory) and the tensors scaled by ``scale x min(1,
+    max_norm / (norm + eps))``, in place or into ``out`` (tensors of the same
+    shapes, dtypes and strides).  ``norm_only`` leaves the tensors alone.
+    ``max_norm=math.inf`` applies the scale only.  Returns 0-d device tensors
+    ``norm`` and ``factor``; when the norm is not finite the factor is NaN and
+    nothing is written."""
+    tensors = list(tensors)
+    n = len(tensors)
+    if n == 0:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    else:
+        dev = tensors[0].device
+        if dev.type != "cuda":
+            raise ValueError("tensors must be CUDA tensors")
+    try:
+        dtypes = [_DTYPES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise ValueError(f"unsupported gradient dtype {e.args[0]}") from None
+    ptrs = [t.data_ptr() for t in tensors]
+    numels = [t.numel() for t in tensors]
+    if len({t.device for t in tensors}) > 1:
+        raise ValueError("every tensor must be on one device")
+    if not all([t.is_contiguous() for t in tensors]) and not all([_dense(t) for t in tensors]):
+        raise ValueError("tensors must be dense (no gaps between elements)")
+    if len(set(ptrs)) < n and len({p for p, k in zip(ptrs, numels) if k}) < sum(map(bool, numels)):
+        raise ValueError("a tensor is given twice")
+    out_ptrs = None
+    if out is not None:
+        out = list(out)
+        if norm_only:
+            raise ValueError("norm_only writes nothing: out must be None")
+        if len(out) != n:
+            raise ValueError("out must hold one tensor for each of tensors")
+        if [o.dtype for o in out] != [t.dtype for t in tensors] or \
+                [o.shape for o in out] != [t.shape for t in tensors] or \
+                len({dev, *[o.device for o in out]}) > 1:
+            raise ValueError("out must have the shapes, dtypes and device of tensors")
+        if not all([o.is_contiguous() and t.is_contiguous() or o.stride() == t.stride()
+                    for o, t in zip(out, tensors)]):
+            raise ValueError("out must have the strides of tensors")
+        out_ptrs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    L = lib()
+    with _AllocateOn(stream):
+        out2 = torch.empty(2, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(L.grpo_clip_workspace_size(n), dtype=torch.uint8, device=dev)
+    rc = L.grpo_clip_grad_norm((ctypes.c_void_p * n)(*ptrs), out_ptrs, (ctypes.c_int64 * n)(*numels),
+                               (ctypes.c_int32 * n)(*dtypes), n, max_norm, eps, scale,
+                               GRPO_CLIP_NORM_ONLY if norm_only else 0, out2.data_ptr(),
+                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(rc, "grpo_clip_grad_norm")
+    norm, factor = out2.unbind()
+    return {"norm": norm, "factor": factor, "workspace": workspace}
 
 
 def grpo_read_device_status(workspace: torch.Tensor, stream=None) -> int:

@@ -8,6 +8,8 @@
 //   rows     fused sweep over vocabulary rows            grpo_rows.cu
 //   reduce   fixed-order reduction to the scalars        grpo_reduce.cu
 // or, for the logps-only boundary, prep + the kernel of grpo_logps.cu.
+// The token log-probs, their gradient (grpo_token.cu) and the gradient norm
+// (grpo_clip.cu) are entry points of their own, without header or prep.
 // A shard call (grpo_shard_t) runs the same kernels on its sequences, with
 // the whole batch's groups and counts, and leaves the scalar to
 // grpo_loss_finalize.
@@ -96,6 +98,32 @@ grpo_status_t check_groups(const grpo_groups_t* g, int64_t B, int32_t* spp,
 
 // Slots per sequence: positions and counts within a sequence are 32-bit.
 static constexpr int64_t kMaxT = (int64_t)1 << 30;
+
+// A logits layout of the token entry points: B, T and V in range, strides
+// not negative, and every row's element offset within 63 bits.
+grpo_status_t check_token_shape(int64_t B, int64_t T, int64_t V, int64_t sb, int64_t st) {
+  if (B < 0 || T < 0 || T > kMaxT || B > kMaxT || V < 1 || V > 0x7FFFFFFF) return GRPO_ERR_SHAPE;
+  if (B * T > 0x7FFFFFFF) return GRPO_ERR_SHAPE;  // rows are numbered in 31 bits
+  if (sb < 0 || st < 0) return GRPO_ERR_SHAPE;
+  const double span = (double)B * (double)sb + (double)T * (double)st + (double)V;
+  return span < 4.0e18 ? GRPO_OK : GRPO_ERR_SHAPE;
+}
+
+// Whether no two of the B x T rows of V elements overlap: the rows of the
+// axis with the smaller stride are at least V apart, and the other axis steps
+// over all of them.
+bool rows_disjoint(int64_t B, int64_t T, int64_t V, int64_t sb, int64_t st) {
+  if (B == 0 || T == 0) return true;
+  if (B == 1) return T == 1 || st >= V;
+  if (T == 1) return sb >= V;
+  const bool t_inner = st <= sb;
+  const int64_t inner = t_inner ? st : sb, outer = t_inner ? sb : st, n = t_inner ? T : B;
+  return inner >= V && outer >= inner * (n - 1) + V;
+}
+
+// Limits of grpo_clip_grad_norm: chunks are numbered in 32 bits.
+static constexpr int64_t kMaxClipTensors = 1 << 20;
+static constexpr int64_t kMaxClipNumel = (int64_t)1 << 40;
 
 grpo_status_t check_ws(const void* ws, size_t ws_bytes, int64_t B, int64_t T) {
   if (!ws) return GRPO_ERR_NULL;
@@ -534,6 +562,102 @@ extern "C" grpo_status_t grpo_vocab_grad(const void* policy_slice, grpo_dtype_t 
   ra.flags = flags;
   ra.precise_ok = dt == GRPO_F32;
   return cuda_status(launch_vocab_grad(ra, dt, v_begin, lse_w, (cudaStream_t)stream));
+}
+
+extern "C" grpo_status_t grpo_token_logps(
+    const void* logits, grpo_dtype_t dt, int64_t B, int64_t T, int64_t V, int64_t stride_b,
+    int64_t stride_t, const int64_t* action_ids, const uint8_t* completion_mask,
+    float temperature, int32_t top_k, float* logps, float* entropy, float* stats,
+    int64_t* top_ids, float* top_logps, void* status_ws, void* stream) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
+  grpo_status_t st = check_token_shape(B, T, V, stride_b, stride_t);
+  if (st != GRPO_OK) return st;
+  if (!(isfinite(temperature) && temperature > 0.f) || !isfinite(1.f / temperature))
+    return GRPO_ERR_PARAM;
+  if (top_k < 0 || top_k > GRPO_MAX_TOP_K || top_k > V) return GRPO_ERR_PARAM;
+  if (B * T > 0 && (!logits || (logps && !action_ids) || (top_k > 0 && (!top_ids || !top_logps))))
+    return GRPO_ERR_NULL;
+  if (!aligned(logits, elem_size(dt)) || !aligned(action_ids, 8) || !aligned(logps, 4) ||
+      !aligned(entropy, 4) || !aligned(stats, 4) || !aligned(top_ids, 8) ||
+      !aligned(top_logps, 4) || !aligned(status_ws, 256))
+    return GRPO_ERR_ALIGN;
+  if (B * T == 0) return GRPO_OK;
+  TokenArgs a{logits, B, T, V, stride_b, stride_t, logps ? action_ids : nullptr, completion_mask,
+              (float)(1.0 / (double)temperature),
+              (float)(1.4426950408889634 / (double)temperature), top_k, logps, entropy, stats,
+              top_ids, top_logps, (WsHeader*)status_ws};
+  return cuda_status(launch_token_logps(a, dt, (cudaStream_t)stream));
+}
+
+extern "C" grpo_status_t grpo_token_logps_grad(
+    const void* logits, grpo_dtype_t dt, int64_t B, int64_t T, int64_t V, int64_t stride_b,
+    int64_t stride_t, const int64_t* action_ids, const uint8_t* completion_mask,
+    const float* stats, const float* entropy, const float* grad_logps, const float* grad_entropy,
+    float temperature, void* grad_logits, int64_t grad_stride_b, int64_t grad_stride_t,
+    uint32_t flags, void* status_ws, void* stream) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
+  grpo_status_t st = check_token_shape(B, T, V, stride_b, stride_t);
+  if (st != GRPO_OK) return st;
+  if ((st = check_token_shape(B, T, V, grad_stride_b, grad_stride_t)) != GRPO_OK) return st;
+  if (!rows_disjoint(B, T, V, grad_stride_b, grad_stride_t)) return GRPO_ERR_SHAPE;
+  if (!(isfinite(temperature) && temperature > 0.f) || !isfinite(1.f / temperature))
+    return GRPO_ERR_PARAM;
+  if (flags & ~GRPO_SKIP_MASKED_GRAD_ROWS) return GRPO_ERR_PARAM;
+  if (B * T > 0 && ((!grad_logps && !grad_entropy) || !logits || !stats || !grad_logits ||
+                    (grad_logps && !action_ids) || (grad_entropy && !entropy)))
+    return GRPO_ERR_NULL;
+  // in place: the rows must be the same ones
+  if (logits == grad_logits && B * T > 0 &&
+      ((B > 1 && stride_b != grad_stride_b) || (T > 1 && stride_t != grad_stride_t)))
+    return GRPO_ERR_SHAPE;
+  const size_t es = elem_size(dt);
+  if (!aligned(logits, es) || !aligned(grad_logits, es) || !aligned(action_ids, 8) ||
+      !aligned(stats, 4) || !aligned(entropy, 4) || !aligned(grad_logps, 4) ||
+      !aligned(grad_entropy, 4) || !aligned(status_ws, 256))
+    return GRPO_ERR_ALIGN;
+  if (B * T == 0) return GRPO_OK;
+  TokenGradArgs a{logits, B, T, V, stride_b, stride_t, grad_logps ? action_ids : nullptr,
+                  completion_mask, stats, grad_entropy ? entropy : nullptr, grad_logps,
+                  grad_entropy, (float)(1.0 / (double)temperature),
+                  (float)(1.4426950408889634 / (double)temperature), grad_logits, grad_stride_b,
+                  grad_stride_t, (flags & GRPO_SKIP_MASKED_GRAD_ROWS) ? 1 : 0,
+                  (WsHeader*)status_ws};
+  return cuda_status(launch_token_grad(a, dt, (cudaStream_t)stream));
+}
+
+extern "C" size_t grpo_clip_workspace_size(int64_t num_tensors) {
+  if (num_tensors < 0 || num_tensors > kMaxClipTensors) return 0;
+  return align256(sizeof(double) * clip_partials(num_tensors));
+}
+
+extern "C" grpo_status_t grpo_clip_grad_norm(const void* const* tensors, void* const* outs,
+                                             const int64_t* numels, const int32_t* dtypes,
+                                             int64_t num_tensors, float max_norm, float eps,
+                                             float scale, uint32_t flags, float* out2, void* ws,
+                                             size_t ws_bytes, void* stream) {
+  if (num_tensors < 0 || num_tensors > kMaxClipTensors) return GRPO_ERR_SHAPE;
+  if (!out2 || !ws || (num_tensors > 0 && (!tensors || !numels || !dtypes))) return GRPO_ERR_NULL;
+  if (flags & ~GRPO_CLIP_NORM_ONLY) return GRPO_ERR_PARAM;
+  const bool norm_only = flags & GRPO_CLIP_NORM_ONLY;
+  if (norm_only && outs) return GRPO_ERR_PARAM;
+  if (!(max_norm >= 0.f) || !(isfinite(eps) && eps >= 0.f) || !(isfinite(scale) && scale > 0.f))
+    return GRPO_ERR_PARAM;
+  int64_t sum = 0;
+  for (int64_t i = 0; i < num_tensors; ++i) {
+    if (dtypes[i] != GRPO_F32 && dtypes[i] != GRPO_BF16 && dtypes[i] != GRPO_F16)
+      return GRPO_ERR_DTYPE;
+    if (numels[i] < 0 || numels[i] > kMaxClipNumel) return GRPO_ERR_SHAPE;
+    if ((sum += numels[i]) > kMaxClipNumel) return GRPO_ERR_SHAPE;
+    if (numels[i] == 0) continue;
+    if (!tensors[i] || (outs && !outs[i])) return GRPO_ERR_NULL;
+    const size_t es = elem_size((grpo_dtype_t)dtypes[i]);
+    if (!aligned(tensors[i], es) || (outs && !aligned(outs[i], es))) return GRPO_ERR_ALIGN;
+  }
+  if (!aligned(out2, 4) || !aligned(ws, 256)) return GRPO_ERR_ALIGN;
+  if (ws_bytes < grpo_clip_workspace_size(num_tensors)) return GRPO_ERR_WORKSPACE;
+  ClipArgs a{tensors, outs, numels, dtypes, num_tensors, (double)max_norm, (double)eps,
+             (double)scale, norm_only ? 1 : 0, out2, (double*)ws};
+  return cuda_status(launch_clip(a, (cudaStream_t)stream));
 }
 
 extern "C" grpo_status_t grpo_read_device_status(const void* ws, void* stream) {

@@ -399,6 +399,102 @@ grpo_status_t grpo_vocab_grad(const void *policy_slice, grpo_dtype_t dt, int64_t
                               const uint8_t *completion_mask, const double *lse_w,
                               void *grad_slice, uint32_t flags, void *stream);
 
+/* Log-probs of given tokens, with entropy and top alternatives.  Scores a
+ * rollout (the behaviour policy's old_logps; a serving step is T = 1) and is
+ * the forward pass of a loss formed from log-probs (grpo_loss_from_logps).
+ * For a row x of V logits, s = 1 / temperature:
+ *   m = max_v x_v,  Z = sum_v exp(s (x_v - m)),  log p_v = s (x_v - m) - log Z
+ *   logp = log p_a,  H = -sum_v p_v log p_v      (0 log 0 = 0)
+ *   top alternatives: the top_k largest x_v, equal values by lowest index
+ *   first, with their log p
+ *   logits          : [B,T,V] of dtype `dt`; row (b, t) starts at element
+ *                     b stride_b + t stride_t (strides >= 0, so rows padded
+ *                     beyond V, slices of a longer sequence and [T,B,V]
+ *                     orders need no copy); the V logits of a row are
+ *                     adjacent, 1 <= V < 2^31.
+ *   action_ids      : [B,T] int64; may be NULL with logps NULL.
+ *   completion_mask : [B,T] uint8, NULL = every token active.  A masked
+ *                     token's logits and id are not read; its outputs are 0
+ *                     (top ids -1, stats {0, 1}).
+ *   temperature     : finite, > 0.
+ *   top_k           : 0 .. GRPO_MAX_TOP_K, at most V.
+ *   logps, entropy  : [B,T] f32, each nullable.
+ *   stats           : [2,B,T] f32, nullable: m and Z, what the gradient needs.
+ *   top_ids         : [B,T,top_k] int64, NULL iff top_k == 0.
+ *   top_logps       : [B,T,top_k] f32, NULL iff top_k == 0.
+ *   status_ws       : nullable; 256 bytes of device memory, 256-byte aligned,
+ *                     zeroed by the caller: receives GRPO_ERR_ACTION_RANGE
+ *                     when an active token's id lies outside [0, V) (its logp
+ *                     is NaN with or without status_ws).  Bits stay set until
+ *                     the caller zeroes it; read with grpo_read_device_status.
+ * -inf logits are allowed (p = 0).  A row that holds a NaN or +inf, or only
+ * -inf, has no distribution: logp, entropy, Z and top_logps are NaN, top ids
+ * -1.  Sums are held in fp32; every result is bitwise reproducible. */
+#define GRPO_MAX_TOP_K 32
+grpo_status_t grpo_token_logps(const void *logits, grpo_dtype_t dt, int64_t B, int64_t T,
+                               int64_t V, int64_t stride_b, int64_t stride_t,
+                               const int64_t *action_ids, const uint8_t *completion_mask,
+                               float temperature, int32_t top_k, float *logps, float *entropy,
+                               float *stats, int64_t *top_ids, float *top_logps,
+                               void *status_ws, void *stream);
+
+/* The gradient of grpo_token_logps with respect to the logits, from the
+ * gradients of its logps (dlogp) and entropy (dH):
+ *   dL/dx_v = s (dlogp (1[v = a] - p_v) - dH p_v (log p_v + H))
+ *   stats, entropy         : what grpo_token_logps returned for these logits
+ *                            at this temperature; entropy is needed (and
+ *                            read) only with grad_entropy.
+ *   grad_logps             : [B,T] f32; NULL = 0 (then action_ids may be NULL).
+ *   grad_entropy           : [B,T] f32; NULL = 0.  At least one of the two.
+ *   grad_logits            : [B,T,V] of dtype `dt`, rows at
+ *                            b grad_stride_b + t grad_stride_t, not
+ *                            overlapping; overwritten.  May be `logits`
+ *                            itself with the same strides (in place), and
+ *                            must not overlap it otherwise.
+ *   flags                  : GRPO_SKIP_MASKED_GRAD_ROWS leaves masked rows
+ *                            untouched; otherwise they are set to 0.
+ * A row whose dlogp and dH are both 0 has gradient 0; its logits are not
+ * read.  An id outside [0, V) on an active token with dlogp != 0 makes its
+ * row NaN and sets GRPO_ERR_ACTION_RANGE in status_ws (as above). */
+grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t B, int64_t T,
+                                    int64_t V, int64_t stride_b, int64_t stride_t,
+                                    const int64_t *action_ids, const uint8_t *completion_mask,
+                                    const float *stats, const float *entropy,
+                                    const float *grad_logps, const float *grad_entropy,
+                                    float temperature, void *grad_logits, int64_t grad_stride_b,
+                                    int64_t grad_stride_t, uint32_t flags, void *status_ws,
+                                    void *stream);
+
+/* The global norm of many gradient tensors, and clipping to it:
+ *   norm = scale sqrt(sum_i sum_j g_ij^2)
+ *   c    = scale min(1, max_norm / (norm + eps)),   out_ij = c g_ij
+ * with c rounded to f32 and each product rounded once to the type of out_i.
+ *   tensors, outs, numels, dtypes : HOST arrays of num_tensors entries: the
+ *     device pointers (aligned to their element size; NULL with numel 0), the
+ *     element counts and the grpo_dtype_t of each tensor.  outs NULL, or an
+ *     entry equal to the tensor's: in place.  outs have the tensors' types;
+ *     tensors and outs must not overlap otherwise.  The arrays are read during
+ *     the call only.
+ *   max_norm : >= 0; +infinity: only the scale is applied.
+ *   eps      : finite, >= 0.     scale : finite, > 0 (1 / loss scale, say).
+ *   flags    : GRPO_CLIP_NORM_ONLY: the tensors are only read (outs NULL).
+ *   out2     : device [2] f32: norm and c.
+ * In place with c == 1, nothing is written.  When the norm is not finite, c
+ * is NaN and no output is written, in place or not: the caller skips the
+ * step.  The squares are summed in fp32 over 64 elements and in fp64 beyond
+ * (a thread whose fp32 sum overflows or underflows repeats it in fp64), in an
+ * order that depends on the sizes alone.
+ * ws: grpo_clip_workspace_size(num_tensors) bytes, 256-byte aligned, needs no
+ * initialisation. */
+#define GRPO_CLIP_NORM_ONLY 1u
+size_t grpo_clip_workspace_size(int64_t num_tensors);
+
+grpo_status_t grpo_clip_grad_norm(const void *const *tensors, void *const *outs,
+                                  const int64_t *numels, const int32_t *dtypes,
+                                  int64_t num_tensors, float max_norm, float eps, float scale,
+                                  uint32_t flags, float *out2, void *ws, size_t ws_bytes,
+                                  void *stream);
+
 /* Synchronises `stream` and returns the device status the last call on this
  * workspace left (GRPO_OK or an OR of the device-detected bits), or
  * GRPO_ERR_CUDA.  (grpo_loss_from_logps moves its status bits into a second
