@@ -13,6 +13,7 @@ raises; there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -658,6 +659,14 @@ def _status_ptr(status, device):
     return status.data_ptr()
 
 
+def _stream_on(stream, device) -> int:
+    """The raw handle of the stream, or of the device's current one (by
+    PyTorch's own short cut: making a Stream object costs 3 us)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
+
+
 class _AllocateOn:
     """Outputs of a call on another stream than the current one belong to
     that stream: memory is taken from its pool, not reused under it."""
@@ -711,7 +720,7 @@ def grpo_token_logps(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
     rc = lib().grpo_token_logps(logits.data_ptr(), _DTYPES[logits.dtype], B, T, V, sb, st, ids,
                                 mask, temperature, top_k, _ptr(logps), _ptr(entropy), _ptr(stats),
                                 _ptr(top_ids), _ptr(top_logps), _status_ptr(status, dev),
-                                _stream(stream))
+                                _stream_on(stream, dev))
     _check(rc, "grpo_token_logps")
     return {"logps": logps, "entropy": entropy, "stats": stats, "top_ids": top_ids,
             "top_logps": top_logps}
@@ -749,7 +758,7 @@ def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tenso
                                      ids, mask, stats_p, ent, dlogp, dent, temperature,
                                      grad.data_ptr(), gsb, gst,
                                      GRPO_SKIP_MASKED_GRAD_ROWS if skip_masked_grad_rows else 0,
-                                     _status_ptr(status, dev), _stream(stream))
+                                     _status_ptr(status, dev), _stream_on(stream, dev))
     _check(rc, "grpo_token_logps_grad")
     return grad
 
@@ -777,27 +786,26 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
     """The global L2 norm of ``scale`` x ``tensors`` (f32, bf16, f16 in any
     mixture; each dense in memory) and the tensors scaled by ``scale x min(1,
     max_norm / (norm + eps))``, in place or into ``out`` (tensors of the same
-    shapes, dtypes and strides).  ``norm_only`` leaves the tensors alone.
+    sizes and dtypes, contiguous or with the same shapes and strides).  ``norm_only`` leaves the tensors alone.
     ``max_norm=math.inf`` applies the scale only.  Returns 0-d device tensors
     ``norm`` and ``factor``; when the norm is not finite the factor is NaN and
     nothing is written."""
     tensors = list(tensors)
     n = len(tensors)
-    if n == 0:
-        dev = torch.device("cuda", torch.cuda.current_device())
-    else:
-        dev = tensors[0].device
-        if dev.type != "cuda":
-            raise ValueError("tensors must be CUDA tensors")
+    dev = tensors[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    at = dev.index
     try:
         dtypes = [_DTYPES[t.dtype] for t in tensors]
     except KeyError as e:
         raise ValueError(f"unsupported gradient dtype {e.args[0]}") from None
     ptrs = [t.data_ptr() for t in tensors]
     numels = [t.numel() for t in tensors]
-    if len({t.device for t in tensors}) > 1:
+    if [t.get_device() for t in tensors] != [at] * n:
         raise ValueError("every tensor must be on one device")
-    if not all([t.is_contiguous() for t in tensors]) and not all([_dense(t) for t in tensors]):
+    plain = all([t.is_contiguous() for t in tensors])
+    if not plain and not all([_dense(t) for t in tensors]):
         raise ValueError("tensors must be dense (no gaps between elements)")
     if len(set(ptrs)) < n and len({p for p, k in zip(ptrs, numels) if k}) < sum(map(bool, numels)):
         raise ValueError("a tensor is given twice")
@@ -806,25 +814,27 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
         out = list(out)
         if norm_only:
             raise ValueError("norm_only writes nothing: out must be None")
-        if len(out) != n:
-            raise ValueError("out must hold one tensor for each of tensors")
-        if [o.dtype for o in out] != [t.dtype for t in tensors] or \
-                [o.shape for o in out] != [t.shape for t in tensors] or \
-                len({dev, *[o.device for o in out]}) > 1:
-            raise ValueError("out must have the shapes, dtypes and device of tensors")
-        if not all([o.is_contiguous() and t.is_contiguous() or o.stride() == t.stride()
-                    for o, t in zip(out, tensors)]):
-            raise ValueError("out must have the strides of tensors")
-        out_ptrs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+        if len(out) != n or [o.get_device() for o in out] != [at] * n or \
+                [_DTYPES.get(o.dtype) for o in out] != dtypes or [o.numel() for o in out] != numels:
+            raise ValueError("out must hold a tensor of the same size and dtype, on the same "
+                             "device, for each of tensors")
+        # element i of the memory of one belongs to element i of the other
+        if not (plain and all([o.is_contiguous() for o in out])) and \
+                not all([o.shape == t.shape and o.stride() == t.stride()
+                         for o, t in zip(out, tensors)]):
+            raise ValueError("out must be contiguous as tensors are, or have their strides")
+        out_ptrs = array.array("Q", [o.data_ptr() for o in out])
     L = lib()
     with _AllocateOn(stream):
         out2 = torch.empty(2, dtype=torch.float32, device=dev)
         if workspace is None:
             workspace = torch.empty(L.grpo_clip_workspace_size(n), dtype=torch.uint8, device=dev)
-    rc = L.grpo_clip_grad_norm((ctypes.c_void_p * n)(*ptrs), out_ptrs, (ctypes.c_int64 * n)(*numels),
-                               (ctypes.c_int32 * n)(*dtypes), n, max_norm, eps, scale,
-                               GRPO_CLIP_NORM_ONLY if norm_only else 0, out2.data_ptr(),
-                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    ptrs, numels, dtypes = array.array("Q", ptrs), array.array("q", numels), array.array("i", dtypes)
+    rc = L.grpo_clip_grad_norm(ptrs.buffer_info()[0],
+                               None if out_ptrs is None else out_ptrs.buffer_info()[0],
+                               numels.buffer_info()[0], dtypes.buffer_info()[0], n, max_norm, eps,
+                               scale, GRPO_CLIP_NORM_ONLY if norm_only else 0, out2.data_ptr(),
+                               workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
     _check(rc, "grpo_clip_grad_norm")
     norm, factor = out2.unbind()
     return {"norm": norm, "factor": factor, "workspace": workspace}

@@ -584,8 +584,8 @@ extern "C" grpo_status_t grpo_token_logps(
   if (B * T == 0) return GRPO_OK;
   TokenArgs a{logits, B, T, V, stride_b, stride_t, logps ? action_ids : nullptr, completion_mask,
               (float)(1.0 / (double)temperature),
-              (float)(1.4426950408889634 / (double)temperature), top_k, logps, entropy, stats,
-              top_ids, top_logps, (WsHeader*)status_ws};
+              (float)(1.4426950408889634 / (double)temperature), 0.f, top_k, logps, entropy,
+              stats, top_ids, top_logps, (WsHeader*)status_ws};
   return cuda_status(launch_token_logps(a, dt, (cudaStream_t)stream));
 }
 

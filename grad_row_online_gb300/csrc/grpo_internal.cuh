@@ -830,6 +830,7 @@ struct TokenArgs {
   const uint8_t* mask;      // nullable
   float inv_t;              // s = 1 / temperature
   float s2;                 // s log2(e)
+  float low;                // floor of the logits in the fast sweep; 0: none (set at launch)
   int k;
   float* logps;    // nullable
   float* entropy;  // nullable
