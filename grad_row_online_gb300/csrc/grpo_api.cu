@@ -619,8 +619,8 @@ extern "C" grpo_status_t grpo_token_logps_grad(
   TokenGradArgs a{logits, B, T, V, stride_b, stride_t, grad_logps ? action_ids : nullptr,
                   completion_mask, stats, grad_entropy ? entropy : nullptr, grad_logps,
                   grad_entropy, (float)(1.0 / (double)temperature),
-                  (float)(1.4426950408889634 / (double)temperature), grad_logits, grad_stride_b,
-                  grad_stride_t, (flags & GRPO_SKIP_MASKED_GRAD_ROWS) ? 1 : 0,
+                  (float)(1.4426950408889634 / (double)temperature), 0.f, grad_logits,
+                  grad_stride_b, grad_stride_t, (flags & GRPO_SKIP_MASKED_GRAD_ROWS) ? 1 : 0,
                   (WsHeader*)status_ws};
   return cuda_status(launch_token_grad(a, dt, (cudaStream_t)stream));
 }

@@ -851,6 +851,7 @@ struct TokenGradArgs {
   const float* dlogp;       // nullable
   const float* dent;        // nullable
   float inv_t, s2;
+  float low;                // as in TokenArgs
   void* grad;
   int64_t gsb, gst;
   int skip_masked;

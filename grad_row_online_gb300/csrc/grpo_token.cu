@@ -259,6 +259,15 @@ __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, f
   return all;
 }
 
+// A logits vector, read once: not kept in L1.
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <typename T, int kThreads, bool kEnt>
 __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const Part& p, float low,
                                            float s2, float* mine) {
@@ -269,11 +278,11 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   for (; j + (kUnroll - 1) * kThreads < p.v1; j += kUnroll * kThreads) {
     uint4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(vec + j + u * kThreads);
+    for (int u = 0; u < kUnroll; ++u) v[u] = ld_once(vec + j + u * kThreads);
     f.take(v, low_word, s2);
   }
   for (; j < p.v1; j += kThreads) {
-    uint4 v[1] = {__ldg(vec + j)};
+    uint4 v[1] = {ld_once(vec + j)};
     f.take(v, low_word, s2);
   }
   *mine = f.m > low ? f.m : -INFINITY;
@@ -359,6 +368,7 @@ __device__ void rank_keys(TopSmem<kThreads, kVec>& sm, int n, int k) {
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const unsigned long long mine = sm.key[i];
     int above = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) above += sm.key[j] > mine;
     if (above < k) sm.best[above] = mine;
   }
@@ -377,17 +387,26 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
   if (tid == 0) sm.n = 0;
   __syncthreads();
   if (tid < 32) {
-    // tau: the largest bound, of 20 leading bits, that k maxima reach
+    // tau: the largest bound, of 16 leading bits, that k maxima reach (a lower
+    // bound does as well, at the price of a slice or two more); two bits a
+    // step, the counts of the three candidates in one word
     unsigned o[kThreads / 32];
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) o[i] = sm.ord[tid + 32 * i];
     unsigned t = 0;
-    for (int b = 31; b >= 12; --b) {
-      const unsigned c = t | (1u << b);
-      int cnt = 0;
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) cnt += o[i] >= c;
-      if (__reduce_add_sync(0xFFFFFFFFu, cnt) >= k) t = c;
+    for (int b = 30; b >= 16; b -= 2) {
+      const unsigned step = 1u << b;
+      unsigned cnt = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i)
+        cnt += (o[i] >= t + step ? 1u : 0u) + (o[i] >= t + 2 * step ? 1u << 10 : 0u) +
+               (o[i] >= t + 3 * step ? 1u << 20 : 0u);
+      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+      t += ((cnt >> 20) >= (unsigned)k)              ? 3 * step
+           : (((cnt >> 10) & 1023u) >= (unsigned)k) ? 2 * step
+           : ((cnt & 1023u) >= (unsigned)k)         ? step
+                                                    : 0u;
     }
     // the slices that reach it, in index order
     int at = 0;
@@ -450,19 +469,12 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
   rank_keys(sm, sm.n, k);
 }
 
-// A row's results, by one thread; `act` is its action.
-template <typename T, bool kEnt>
-__device__ __forceinline__ void finish_row(const TokenArgs& a, int64_t r, const T* row, Stat w) {
+// A row's results, by one thread; xa is its action's logit (NaN for an id out
+// of range).
+template <bool kEnt>
+__device__ __forceinline__ void finish_row(const TokenArgs& a, int64_t r, float xa, Stat w) {
   const float lnZ = logf(w.Z);
-  if (a.logps) {
-    const int64_t act = a.actions[r];
-    float lp = NAN;
-    if (act >= 0 && act < a.V)
-      lp = (Storage<T>::load1(row + act) - w.m) * a.inv_t - lnZ;
-    else if (a.hdr)
-      atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
-    a.logps[r] = lp;
-  }
+  if (a.logps) a.logps[r] = (xa - w.m) * a.inv_t - lnZ;
   if (kEnt) a.entropy[r] = lnZ - kLn2f * (w.D / w.Z);
   if (a.stats) {
     a.stats[r] = w.m;
@@ -474,8 +486,7 @@ __device__ __forceinline__ void finish_row(const TokenArgs& a, int64_t r, const 
 static constexpr int kMaxCluster = 8;
 struct Parts {
   Stat st[kMaxCluster];
-  int n[kMaxCluster];  // keys held
-  unsigned long long key[kMaxCluster * GRPO_MAX_TOP_K];
+  unsigned long long key[kMaxCluster][GRPO_MAX_TOP_K];  // largest first, 0 where there is none
 };
 
 // One CTA per row, or with kSplit a cluster of CTAs, each of which takes a
@@ -483,7 +494,7 @@ struct Parts {
 // thread in flight, a tree over the threads, the part's alternatives, and in
 // a cluster the parts joined by its first CTA.
 template <typename T, int kThreads, bool kEnt, bool kTop, bool kSplit>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : 1)
 token_logps_kernel(const TokenArgs a) {
   constexpr int VEC = Storage<T>::kVec;
   __shared__ Stat warp_stat[kThreads / 32];
@@ -512,7 +523,8 @@ token_logps_kernel(const TokenArgs a) {
     }
     return;
   }
-  const T* row = (const T*)a.logits + (r / a.T) * a.sb + (r % a.T) * a.st;
+  const unsigned b = (unsigned)r / (unsigned)a.T, t = (unsigned)r % (unsigned)a.T;
+  const T* row = (const T*)a.logits + b * a.sb + t * a.st;
   const Geom<T> g(row, a.V);
   const uint4* vec = reinterpret_cast<const uint4*>(row + g.head);
   Part p{g.head, g.tail, g.t0, 0, g.nvec};
@@ -521,6 +533,15 @@ token_logps_kernel(const TokenArgs a) {
     p.v0 = min((int64_t)rank * per, g.nvec);
     p.v1 = min(p.v0 + per, g.nvec);
     if (rank != 0) p.head = p.tail = 0;
+  }
+  // the action's logit now, so that the end of the row does not wait for it
+  float xa = NAN;
+  if (tid == 0 && rank == 0 && a.logps) {
+    const int64_t act = a.actions[r];
+    if (act >= 0 && act < a.V)
+      xa = Storage<T>::load1(row + act);
+    else if (a.hdr)
+      atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
   }
   const float s2 = a.s2;
   float mine;
@@ -545,9 +566,8 @@ token_logps_kernel(const TokenArgs a) {
     Parts* first = cluster.map_shared_rank(&parts, 0);
     if (tid == 0) first->st[rank] = st;
     if constexpr (kTop) {
-      const int n = min(a.k, top.n);
-      if (tid == 0) first->n[rank] = n;
-      if (tid < n) first->key[rank * GRPO_MAX_TOP_K + tid] = top.best[tid];
+      if (tid < GRPO_MAX_TOP_K)
+        first->key[rank][tid] = tid < min(a.k, top.n) ? top.best[tid] : 0ull;
     }
     cluster.sync();
     if (rank != 0) return;
@@ -555,7 +575,7 @@ token_logps_kernel(const TokenArgs a) {
     for (unsigned i = 1; i < ctas; ++i) st = merge<kEnt>(st, parts.st[i], s2);
   }
   if (st.m == -INFINITY) st.Z = NAN;  // no finite logit: no distribution
-  if (tid == 0) finish_row<T, kEnt>(a, r, row, st);
+  if (tid == 0) finish_row<kEnt>(a, r, xa, st);
   if constexpr (kTop) {
     if (!(st.Z <= 3.4e38f)) {  // NaN or +inf
       if (tid < a.k) {
@@ -570,15 +590,25 @@ token_logps_kernel(const TokenArgs a) {
       a.top_logps[r * a.k + i] = (x - st.m) * a.inv_t - logf(st.Z);
     };
     if constexpr (kSplit) {
-      // the rank of each part's keys among all of them
+      // a key's place: how many keys of each part lie above it, by bisection
+      // of the parts' ordered lists, all parts at once
       const int part = tid / GRPO_MAX_TOP_K, i = tid % GRPO_MAX_TOP_K;
       static_assert(kThreads >= kMaxCluster * GRPO_MAX_TOP_K, "a thread for each key");
-      if (part < (int)ctas && i < parts.n[part]) {
-        const unsigned long long key = parts.key[tid];
-        int above = 0;
-        for (int q = 0; q < (int)ctas; ++q)
-          for (int n = 0; n < parts.n[q]; ++n) above += parts.key[q * GRPO_MAX_TOP_K + n] > key;
-        if (above < a.k) put(above, key);
+      const unsigned long long key = part < (int)ctas ? parts.key[part][i] : 0ull;
+      if (key != 0ull) {
+        int above[kMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) above[q] = 0;
+#pragma unroll
+        for (int step = GRPO_MAX_TOP_K / 2; step > 0; step /= 2)
+#pragma unroll
+          for (int q = 0; q < kMaxCluster; ++q)
+            if (q < (int)ctas && parts.key[q][above[q] + step - 1] > key) above[q] += step;
+        int place = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < (int)ctas) place += above[q] + (parts.key[q][above[q]] > key);
+        if (place < a.k) put(place, key);
       }
     } else {
       top_alternatives<T, kThreads>(row, vec, p, g.head, mine, a.k, top);
@@ -614,16 +644,19 @@ static cudaError_t launch_logps_t(const TokenArgs& a, unsigned ctas, cudaStream_
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
+// The floor of the fast arithmetic (see Fast): 2^(s2 (low - m)) is 0 for every
+// maximum m > low / 2, and s2 |low| is below 2^30, so that the rounding of a
+// thread's mL is below 2^6.  0: not for this temperature.
+template <typename T>
+static float floor_of(float s2) {
+  if (std::is_same<T, __half>::value) return s2 >= 0.01f && s2 <= 1e4f ? -65504.f : 0.f;
+  const float low = s2 >= 1e-30f && s2 <= 1e30f ? -16384.f / s2 : 0.f;
+  return std::is_same<T, float>::value ? low : __bfloat162float(__float2bfloat16(low));
+}
+
 template <typename T>
 static cudaError_t launch_logps_d(TokenArgs a, cudaStream_t s) {
-  // The floor of the fast sweep (see Fast): 2^(s2 (low - m)) is 0 for every
-  // maximum m > low / 2, and s2 |low| is below 2^30, so that the rounding of
-  // a thread's mL is below 2^6.  0: not for this temperature.
-  if (std::is_same<T, __half>::value)
-    a.low = a.s2 >= 0.01f && a.s2 <= 1e4f ? -65504.f : 0.f;
-  else
-    a.low = a.s2 >= 1e-30f && a.s2 <= 1e30f ? -16384.f / a.s2 : 0.f;
-  if (std::is_same<T, __nv_bfloat16>::value) a.low = __bfloat162float(__float2bfloat16(a.low));
+  a.low = floor_of<T>(a.s2);
   const int64_t bytes = a.V * (int64_t)sizeof(T), rows = a.B * a.T;
   if (bytes <= kWarpRowBytes) return launch_logps_t<T, 32, false>(a, 1, s);
   // few rows: a cluster for each, while the CTAs all run at once
@@ -648,119 +681,188 @@ cudaError_t launch_token_logps(const TokenArgs& a, grpo_dtype_t dt, cudaStream_t
 // With u = s2 (x_v - m):  dL/dx_v = s dlogp 1[v = a] - 2^u (c0 + c1 u),
 //   c0 = s (dlogp + dH (H - ln Z)) / Z,   c1 = s dH ln2 / Z
 // (log p_v = ln2 u - ln Z).  m and Z are the forward pass' own, so 2^u / Z
-// carries no rounding of a logsumexp.
+// carries no rounding of a logsumexp.  Where |m| s2 stays below kFastRange, u
+// is one fused multiply-add, x s2 - mL with mL = fl(m s2); what mL rounds off,
+// r = m s2 - mL, goes into the coefficients (2^u = 2^(u' - r), u = u' - r).
 struct GradRow {
-  float m, c0, c1, ga;  // ga: added at the action
-  int64_t act;
+  float off;      // -mL, or -m
+  float c0, c1;   // negated: the gradient is 2^u (c0 + c1 u)
+  float ga;       // added at the action
+  uint32_t low;   // floor of the logits, as a word (fused)
+  bool fused;
 };
 
-__device__ __forceinline__ float token_grad(float x, const GradRow& q, float s2) {
-  const float u = (x - q.m) * s2;
-  return -ex2_fast(u) * (q.c0 + q.c1 * fmaxf(u, kLowU));
+// The gradient of two logits; fused: the logits are no lower than the floor
+// (Fast), so u is finite.
+template <bool kEnt, bool kFused>
+__device__ __forceinline__ float2 token_grad2(float2 x, const GradRow& q, float s2) {
+  const float2 sc = make_float2(s2, s2), off = make_float2(q.off, q.off);
+  float2 u = kFused ? fma2(x, sc, off) : mul2(add2(x, off), sc);
+  const float2 e = make_float2(ex2_fast(u.x), ex2_fast(u.y));
+  if (!kEnt) return mul2(e, make_float2(q.c0, q.c0));
+  if (!kFused) u = make_float2(fmaxf(u.x, kLowU), fmaxf(u.y, kLowU));
+  return mul2(e, fma2(u, make_float2(q.c1, q.c1), make_float2(q.c0, q.c0)));
 }
 
 static constexpr int kGradThreads = 256;
-
-// A CTA works on chunks of one row, kGradVecs 16-byte vectors a thread each;
-// the row's unaligned ends go to its first CTA.  Plain loads, not the
-// read-only path: in place, the row is written by this kernel.
+// A CTA takes steps of kGradVecs 16-byte vectors a thread along one row, its
+// loads of a step in flight together.  Plain loads, not the read-only path:
+// in place, the row is written by this kernel.
 static constexpr int kGradVecs = 4;
 
 __device__ __forceinline__ float load_plain(const float* p) { return *p; }
 __device__ __forceinline__ float load_plain(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_plain(const __half* p) { return __half2float(*p); }
 
-template <typename T>
-__global__ void __launch_bounds__(kGradThreads)
-token_grad_kernel(const TokenGradArgs a, unsigned chunks, unsigned ctas) {
+// One step: this thread's vectors j0, j0 + kGradThreads, ...; kWhole: all of
+// them inside the row.
+template <typename T, bool kEnt, bool kFused, bool kWhole>
+__device__ __forceinline__ void grad_step(const T* in, T* out, int64_t j0, int64_t nvec,
+                                          int64_t act, const GradRow& q, float s2,
+                                          bool together) {
   constexpr int VEC = Storage<T>::kVec;
-  const int tid = threadIdx.x;
-  const int64_t r = blockIdx.x / ctas, rows = a.B * a.T;
-  const unsigned first = blockIdx.x % ctas;
-  const bool on = !a.mask || a.mask[r];
-  if (!on && a.skip_masked) return;
-  T* grow = (T*)a.grad + (r / a.T) * a.gsb + (r % a.T) * a.gst;
-  const T* row = (const T*)a.logits + (r / a.T) * a.sb + (r % a.T) * a.st;
-  const float w = on && a.dlogp ? a.dlogp[r] : 0.f;
-  const float h = on && a.dent ? a.dent[r] : 0.f;
-  const bool zero = w == 0.f && h == 0.f;
-  GradRow q{0.f, 0.f, 0.f, 0.f, -1};
-  if (!zero) {
-    const float Z = a.stats[rows + r];
-    q.m = a.stats[r];
-    float c0 = w;
-    if (h != 0.f) c0 += h * (a.entropy[r] - logf(Z));
-    q.c0 = a.inv_t * c0 / Z;
-    q.c1 = a.inv_t * kLn2f * h / Z;
-    if (w != 0.f) {
-      q.act = a.actions[r];
-      q.ga = a.inv_t * w;
-      if (q.act < 0 || q.act >= a.V) {
-        q.c0 = NAN;
-        if (a.hdr && first == 0 && tid == 0)
-          atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
-      }
+  uint4 v[kGradVecs];
+#pragma unroll
+  for (int k = 0; k < kGradVecs; ++k) {
+    const int64_t j = j0 + k * kGradThreads;
+    if (!kWhole && j >= nvec) continue;
+    if (together) {
+      v[k] = *(reinterpret_cast<const uint4*>(in) + j);
+    } else {
+      T t[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) t[e] = in[j * VEC + e];
+      v[k] = *reinterpret_cast<const uint4*>(t);
     }
   }
-  const Geom<T> g(grow, a.V);  // by the gradient's alignment: the stores are whole
-  if (first == 0 && tid < g.head + g.tail) {
-    const int64_t v = tid < g.head ? tid : g.t0 + tid - g.head;
-    float d = 0.f;
-    if (!zero) d = token_grad(load_plain(row + v), q, a.s2) + (v == q.act ? q.ga : 0.f);
-    Storage<T>::store1(grow + v, d);
-  }
-  const bool together = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
-  uint4* out = reinterpret_cast<uint4*>(grow + g.head);
-  const T* in = row + g.head;
-  const int64_t act = q.act - g.head;  // among the vectors' elements
-  for (unsigned chunk = first; chunk < chunks; chunk += ctas) {
-    const int64_t j0 = (int64_t)chunk * (kGradVecs * kGradThreads) + tid;
-    if (zero) {
 #pragma unroll
-      for (int k = 0; k < kGradVecs; ++k)
-        if (j0 + k * kGradThreads < g.nvec) out[j0 + k * kGradThreads] = make_uint4(0u, 0u, 0u, 0u);
-      continue;
+  for (int k = 0; k < kGradVecs; ++k) {
+    const int64_t j = j0 + k * kGradThreads;
+    if (!kWhole && j >= nvec) continue;
+    float x[VEC];
+    if (kEnt && kFused) {
+      uint32_t* words = &v[k].x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) words[i] = Words<T>::at_least(words[i], q.low);
     }
-    uint4 v[kGradVecs];
+    Storage<T>::unpack(v[k], x);
 #pragma unroll
-    for (int k = 0; k < kGradVecs; ++k) {
-      const int64_t j = j0 + k * kGradThreads;
-      if (j >= g.nvec) continue;
-      if (together) {
-        v[k] = *(reinterpret_cast<const uint4*>(in) + j);
-      } else {
-        T t[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) t[e] = in[j * VEC + e];
-        v[k] = *reinterpret_cast<const uint4*>(t);
-      }
+    for (int e = 0; e < VEC; e += 2) {
+      const float2 d = token_grad2<kEnt, kFused>(make_float2(x[e], x[e + 1]), q, s2);
+      x[e] = d.x;
+      x[e + 1] = d.y;
     }
+    const uint64_t at = (uint64_t)(act - j * VEC);
+    if (at < VEC) {
 #pragma unroll
-    for (int k = 0; k < kGradVecs; ++k) {
-      const int64_t j = j0 + k * kGradThreads;
-      if (j >= g.nvec) continue;
-      float x[VEC];
-      Storage<T>::unpack(v[k], x);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = token_grad(x[e], q, a.s2);
-      const uint64_t at = (uint64_t)(act - j * VEC);
-      if (at < VEC) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] += at == e ? q.ga : 0.f;
-      }
-      out[j] = Storage<T>::pack(x);
+      for (int e = 0; e < VEC; ++e) x[e] += at == e ? q.ga : 0.f;
     }
+    reinterpret_cast<uint4*>(out)[j] = Storage<T>::pack(x);
   }
 }
 
+template <typename T, bool kEnt, bool kFused>
+__device__ __forceinline__ void grad_steps(const T* in, T* out, int64_t step0, int64_t steps,
+                                           int64_t nvec, int64_t act, const GradRow& q, float s2,
+                                           bool together) {
+  for (int64_t i = step0; i < steps; ++i) {
+    const int64_t j0 = i * (kGradVecs * kGradThreads) + threadIdx.x;
+    if (j0 - threadIdx.x + kGradVecs * kGradThreads <= nvec)
+      grad_step<T, kEnt, kFused, true>(in, out, j0, nvec, act, q, s2, together);
+    else
+      grad_step<T, kEnt, kFused, false>(in, out, j0, nvec, act, q, s2, together);
+  }
+}
+
+// CTA c of a row takes its steps [c per, (c + 1) per); the row's unaligned
+// ends go to its first CTA.
+template <typename T, bool kEnt>
+__global__ void __launch_bounds__(kGradThreads)
+token_grad_kernel(const TokenGradArgs a, unsigned ctas, unsigned per) {
+  const int tid = threadIdx.x;
+  const int64_t r = blockIdx.x / ctas, rows = a.B * a.T;
+  const unsigned cta = blockIdx.x % ctas;
+  // the row's scalars, all asked for at once
+  const bool on = !a.mask || a.mask[r];
+  float w = a.dlogp ? a.dlogp[r] : 0.f;
+  float h = kEnt ? a.dent[r] : 0.f;
+  const float H = kEnt ? a.entropy[r] : 0.f;
+  const float m = a.stats[r], Z = a.stats[rows + r];
+  const int64_t id = a.dlogp ? a.actions[r] : 0;
+  if (!on && a.skip_masked) return;
+  const unsigned b = (unsigned)r / (unsigned)a.T, t = (unsigned)r % (unsigned)a.T;
+  T* grow = (T*)a.grad + b * a.gsb + t * a.gst;
+  const T* row = (const T*)a.logits + b * a.sb + t * a.st;
+  const Geom<T> g(grow, a.V);  // by the gradient's alignment: the stores are whole
+  uint4* out = reinterpret_cast<uint4*>(grow + g.head);
+  const int64_t steps = min((int64_t)(cta + 1) * per,
+                            (g.nvec + kGradVecs * kGradThreads - 1) / (kGradVecs * kGradThreads));
+  const int ev = tid < g.head ? tid : (int)g.t0 + tid - g.head;  // this thread's end element
+  const bool edge = cta == 0 && tid < g.head + g.tail;
+  if (!on || (w == 0.f && h == 0.f)) {
+    if (edge) Storage<T>::store1(grow + ev, 0.f);
+    for (int64_t i = (int64_t)cta * per; i < steps; ++i)
+#pragma unroll
+      for (int k = 0; k < kGradVecs; ++k) {
+        const int64_t j = (i * kGradVecs + k) * kGradThreads + tid;
+        if (j < g.nvec) out[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    return;
+  }
+  GradRow q;
+  const float mL = m * a.s2;
+  q.fused = a.low < 0.f && fabsf(mL) <= kFastRange && m > 0.5f * a.low;
+  q.low = Words<T>::floor_word(a.low);
+  q.off = q.fused ? -mL : -m;
+  const float rest = q.fused ? __fmaf_rn(m, a.s2, -mL) : 0.f;
+  const float f = -a.inv_t * ex2_fast(-rest) / Z;
+  q.c1 = f * kLn2f * h;
+  q.c0 = (kEnt && h != 0.f) ? f * (w + h * (H - logf(Z))) - q.c1 * rest : f * w;
+  q.ga = a.inv_t * w;
+  int64_t act = -1;
+  if (w != 0.f) {
+    act = id;
+    if (id < 0 || id >= a.V) {
+      q.c0 = NAN;
+      if (a.hdr && cta == 0 && tid == 0) atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
+    }
+  }
+  if (edge) {
+    float x = load_plain(row + ev);
+    if (q.fused && x < a.low) x = a.low;
+    const float2 x2 = make_float2(x, x);
+    float d = q.fused ? token_grad2<kEnt, true>(x2, q, a.s2).x
+                      : token_grad2<kEnt, false>(x2, q, a.s2).x;
+    if (ev == act) d += q.ga;
+    Storage<T>::store1(grow + ev, d);
+  }
+  const bool together = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
+  const T* in = row + g.head;
+  T* o = grow + g.head;
+  act -= g.head;  // among the vectors' elements
+  if (q.fused)
+    grad_steps<T, kEnt, true>(in, o, (int64_t)cta * per, steps, g.nvec, act, q, a.s2, together);
+  else
+    grad_steps<T, kEnt, false>(in, o, (int64_t)cta * per, steps, g.nvec, act, q, a.s2, together);
+}
+
 template <typename T>
-static cudaError_t launch_grad_t(const TokenGradArgs& a, cudaStream_t s) {
-  const int64_t per = (int64_t)kGradThreads * kGradVecs * Storage<T>::kVec;
-  const int64_t chunks = (a.V + per - 1) / per, rows = a.B * a.T;
-  // one CTA per chunk, fewer where the grid would pass 2^31 - 1 CTAs
-  const int64_t most = 0x7FFFFFFF / rows, ctas = chunks < most ? chunks : most;
-  token_grad_kernel<T><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(a, (unsigned)chunks,
-                                                                        (unsigned)ctas);
+static cudaError_t launch_grad_t(TokenGradArgs a, cudaStream_t s) {
+  a.low = floor_of<T>(a.s2);
+  const int64_t step = (int64_t)kGradThreads * kGradVecs * Storage<T>::kVec;
+  const int64_t steps = (a.V + step - 1) / step, rows = a.B * a.T;
+  // steps a CTA: up to 4, one where the rows alone are too few to fill the
+  // GPU several times over, and enough to keep the grid below 2^31 CTAs
+  int64_t per = 1;
+  while (per < 4 && per < steps && rows * ((steps + 2 * per - 1) / (2 * per)) >= 152 * 32) per *= 2;
+  while (rows * ((steps + per - 1) / per) > 0x7FFFFFFF) per *= 2;
+  const int64_t ctas = (steps + per - 1) / per;
+  if (a.dent)
+    token_grad_kernel<T, true><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(
+        a, (unsigned)ctas, (unsigned)per);
+  else
+    token_grad_kernel<T, false><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(
+        a, (unsigned)ctas, (unsigned)per);
   return cudaGetLastError();
 }
 
