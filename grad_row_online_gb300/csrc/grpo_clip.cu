@@ -18,8 +18,15 @@
 namespace grpo {
 
 static constexpr int kClipThreads = 256;
-static constexpr int kClipCtasPerSm = 4;
-static constexpr int kClipMaxGrid = 1024;
+// CTAs an SM in each kernel, vectors a thread in flight and chunks a piece,
+// chosen on 3.6 GB and 0.45 GB of gradients (us of both kernels): 4 / 6 / 4 /
+// 2 1561 and 235; 4 / 4 / 8 / 8 1584 and 260; 4 / 16 / 4 / 2 1595 and 236;
+// 4 / 32 / 4 / 4 1557 and 249, but 586 instead of 520 when nothing is clipped.
+static constexpr int kNormCtasPerSm = 4;
+static constexpr int kScaleCtasPerSm = 6;
+static constexpr int kClipAhead = 4;
+static constexpr unsigned kPiece = 2;
+static constexpr int kClipMaxGrid = 2048;
 // elements of a chunk: 64 a thread, which one fp32 sum of squares covers
 static constexpr int64_t kClipChunk = 64 * kClipThreads;
 
@@ -41,16 +48,36 @@ static constexpr int kClipFew = 64;
 static constexpr int kClipMany = 1000;
 static_assert(sizeof(ClipTable<kClipMany>) + 64 <= 32764, "kernel parameters end at 32,764 bytes");
 
-// The entry that holds chunk c, at or after entry i.
+// A CTA takes pieces of kPiece consecutive chunks; the entry of a piece's
+// first chunk is searched for (each probe of the table is a constant-cache
+// miss when it is long), the others follow it.
+
+// The last entry whose chunk0 is at most c.
 template <int kCap>
-__device__ __forceinline__ int find_entry(const ClipTable<kCap>& t, unsigned c, int i) {
-  int lo = i, hi = t.count;  // e[lo].chunk0 <= c < e[hi].chunk0
+__device__ __forceinline__ int find_entry(const ClipTable<kCap>& t, unsigned c) {
+  int lo = 0, hi = t.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (t.e[mid].chunk0 <= c) lo = mid;
     else hi = mid;
   }
   return lo;
+}
+
+// fn(entry, chunk) for each chunk of piece p.
+template <int kCap, typename F>
+__device__ __forceinline__ void each_chunk(const ClipTable<kCap>& t, unsigned p, F fn) {
+  unsigned c = p * kPiece;
+  const unsigned end = min(c + kPiece, t.chunks);
+  int i = find_entry(t, c);
+  unsigned next = i + 1 < t.count ? t.e[i + 1].chunk0 : t.chunks;
+  for (; c < end; ++c) {
+    if (c >= next) {
+      ++i;
+      next = i + 1 < t.count ? t.e[i + 1].chunk0 : t.chunks;
+    }
+    fn(t.e[i], c);
+  }
 }
 
 template <typename T>
@@ -75,6 +102,16 @@ __device__ __forceinline__ float clip_load(const float* p) { return *p; }
 __device__ __forceinline__ float clip_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float clip_load(const __half* p) { return __half2float(*p); }
 
+// The gradients of a chunk; not kept in L1.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // This thread's part of a chunk's sum of squares.  The fp32 sum is taken
 // where it lies well inside the range (or the elements are all zero); a sum
 // that overflowed, or so small that squares were lost below the range, is
@@ -94,16 +131,35 @@ __device__ double chunk_squares(const ClipChunk<T>& k) {
     any = x != 0.f;
     s = x * x;
   }
-#pragma unroll 4
-  for (int i = 0; i < kVecs; ++i) {
-    const int j = tid + i * kClipThreads;
-    if (j >= k.nvec) break;
-    const uint4 v = vec[j];
+  auto take = [&](const uint4& v) {
     float x[VEC];
     Storage<T>::unpack(v, x);
     any |= v.x | v.y | v.z | v.w;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
+  };
+  // the loads of kClipAhead vectors in flight together
+  if (k.nvec == kVecs * kClipThreads) {
+#pragma unroll
+    for (int i = 0; i < kVecs; i += kClipAhead) {
+      uint4 v[kClipAhead];
+#pragma unroll
+      for (int u = 0; u < kClipAhead; ++u) v[u] = ld_stream(vec + tid + (i + u) * kClipThreads);
+#pragma unroll
+      for (int u = 0; u < kClipAhead; ++u) take(v[u]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVecs; i += kClipAhead) {
+      uint4 v[kClipAhead];
+#pragma unroll
+      for (int u = 0; u < kClipAhead; ++u) {
+        const int j = tid + (i + u) * kClipThreads;
+        v[u] = j < k.nvec ? ld_stream(vec + j) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < kClipAhead; ++u) take(v[u]);
+    }
   }
   if (s > 0x1p-100f && s < 0x1p126f) return (double)s;
   if (any == 0u) return 0.0;
@@ -137,16 +193,16 @@ __global__ void __launch_bounds__(kClipThreads)
 clip_norm_kernel(const __grid_constant__ ClipTable<kCap> t, double* partials) {
   __shared__ double sm[kClipThreads / 32];
   double sum = 0.0;
-  int i = 0;
-  for (unsigned c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    i = find_entry(t, c, i);
-    const ClipEntry& e = t.e[i];
-    switch (e.n >> 62) {
-      case GRPO_F32: sum += chunk_squares(ClipChunk<float>(e, c)); break;
-      case GRPO_BF16: sum += chunk_squares(ClipChunk<__nv_bfloat16>(e, c)); break;
-      default: sum += chunk_squares(ClipChunk<__half>(e, c)); break;
-    }
-  }
+  const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
+  for (unsigned p = blockIdx.x; p < pieces; p += gridDim.x)
+    each_chunk(t, p, [&](const ClipEntry& e, unsigned c) {
+      switch (e.n >> 62) {
+        case GRPO_F32: sum += chunk_squares(ClipChunk<float>(e, c)); break;
+        case GRPO_BF16: sum += chunk_squares(ClipChunk<__nv_bfloat16>(e, c)); break;
+        default: sum += chunk_squares(ClipChunk<__half>(e, c)); break;
+      }
+    });
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   sum = cta_sum(sum, sm);
   if (threadIdx.x == 0) partials[blockIdx.x] = sum;
 }
@@ -156,7 +212,8 @@ struct ClipScale {
   int count;
   double max_norm, eps, scale;
   float* out2;
-  int first;  // this launch writes out2
+  int first;     // this launch writes out2
+  int in_place;  // no tensor has an output of its own
 };
 
 // norm and c from the partial sums, the same in every thread of every CTA.
@@ -187,19 +244,32 @@ __device__ __forceinline__ void scale_chunk(const ClipChunk<T>& k, float f) {
   }
   const uint4* vec = reinterpret_cast<const uint4*>(k.in + k.head);
   const bool together = (((uintptr_t)k.in ^ (uintptr_t)k.out) & 15) == 0;
-#pragma unroll 4
-  for (int i = 0; i < kVecs; ++i) {
-    const int j = tid + i * kClipThreads;
-    if (j >= k.nvec) break;
+  const uint64_t pol = l2_evict_first();
+  auto put = [&](int j, const uint4& v) {
     float x[VEC];
-    Storage<T>::unpack(vec[j], x);
+    Storage<T>::unpack(v, x);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) x[e] *= f;
     if (together) {
-      reinterpret_cast<uint4*>(k.out + k.head)[j] = Storage<T>::pack(x);
+      // first to leave L2: what is still to be read stays
+      st_hint(reinterpret_cast<uint4*>(k.out + k.head) + j, Storage<T>::pack(x), pol);
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) Storage<T>::store1(k.out + k.head + j * VEC + e, x[e]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kVecs; i += kClipAhead) {
+    uint4 v[kClipAhead];
+#pragma unroll
+    for (int u = 0; u < kClipAhead; ++u) {
+      const int j = tid + (i + u) * kClipThreads;
+      if (j < k.nvec) v[u] = ld_stream(vec + j);
+    }
+#pragma unroll
+    for (int u = 0; u < kClipAhead; ++u) {
+      const int j = tid + (i + u) * kClipThreads;
+      if (j < k.nvec) put(j, v[u]);
     }
   }
 }
@@ -208,18 +278,20 @@ template <int kCap>
 __global__ void __launch_bounds__(kClipThreads)
 clip_scale_kernel(const __grid_constant__ ClipTable<kCap> t, const ClipScale k) {
   __shared__ double sm[kClipThreads / 32];
+  // launched while the norm's last CTAs run; their sums are complete from here
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float f = clip_factor(k, sm);
-  if (f != f) return;
-  int i = 0;
-  for (unsigned c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    i = find_entry(t, c, i);
-    const ClipEntry& e = t.e[i];
-    switch (e.n >> 62) {
-      case GRPO_F32: scale_chunk(ClipChunk<float>(e, c), f); break;
-      case GRPO_BF16: scale_chunk(ClipChunk<__nv_bfloat16>(e, c), f); break;
-      default: scale_chunk(ClipChunk<__half>(e, c), f); break;
-    }
-  }
+  if (f != f || (f == 1.f && k.in_place)) return;
+  // from the end: what the norm read last is in L2 still
+  const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
+  for (unsigned q = blockIdx.x; q < pieces; q += gridDim.x)
+    each_chunk(t, pieces - 1 - q, [&](const ClipEntry& e, unsigned c) {
+      switch (e.n >> 62) {
+        case GRPO_F32: scale_chunk(ClipChunk<float>(e, c), f); break;
+        case GRPO_BF16: scale_chunk(ClipChunk<__nv_bfloat16>(e, c), f); break;
+        default: scale_chunk(ClipChunk<__half>(e, c), f); break;
+      }
+    });
 }
 
 size_t clip_partials(int64_t num_tensors) {
@@ -247,14 +319,15 @@ static void fill_table(const ClipArgs& a, int64_t* i, ClipTable<kCap>* t) {
 
 template <int kCap>
 static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
-  const unsigned most = (unsigned)(sms * kClipCtasPerSm < kClipMaxGrid ? sms * kClipCtasPerSm
-                                                                       : kClipMaxGrid);
+  const unsigned most = (unsigned)min(sms * kNormCtasPerSm, kClipMaxGrid);
+  const unsigned most_scale = (unsigned)(sms * kScaleCtasPerSm);
   ClipTable<kCap> t;
-  ClipScale k{a.partials, 0, a.max_norm, a.eps, a.scale, a.out2, 1};
+  ClipScale k{a.partials, 0, a.max_norm, a.eps, a.scale, a.out2, 1, a.outs == nullptr};
   int64_t i = 0;
   do {
     fill_table(a, &i, &t);
-    const unsigned grid = t.chunks < most ? (t.chunks ? t.chunks : 1) : most;
+    const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
+    const unsigned grid = max(1u, min(pieces, most));
     clip_norm_kernel<kCap><<<grid, kClipThreads, 0, s>>>(t, a.partials + k.count);
     k.count += (int)grid;
   } while (i < a.count);
@@ -267,8 +340,21 @@ static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
     } else {
       fill_table(a, &i, &t);
     }
-    const unsigned grid = t.chunks < most ? (t.chunks ? t.chunks : 1) : most;
-    clip_scale_kernel<kCap><<<grid, kClipThreads, 0, s>>>(t, k);
+    const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
+    const unsigned grid = max(1u, min(pieces, most_scale));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kClipThreads);
+    cfg.stream = s;
+    // the first one may be dispatched while the norm kernel ends (it waits
+    // for it); a later one follows it in full
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = k.first ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel<kCap>, t, k);
+    if (e != cudaSuccess) return e;
     k.first = 0;
   } while (i < a.count);
   return cudaGetLastError();
