@@ -145,8 +145,9 @@ struct Fast {
   static constexpr int kPairs = Words<T>::kPairs;
   float m, mL;
   float2 Z, D;
+  float cur;  // the largest logit since it was last cleared
   __device__ void init(float low, float s2) {
-    m = low;
+    m = cur = low;
     mL = low * s2;
     Z = D = make_float2(0.f, 0.f);
   }
@@ -175,6 +176,7 @@ struct Fast {
       top = n == 0 ? t : Words<T>::larger(top, t);
     }
     const float vmax = Words<T>::value(top);
+    cur = fmaxf(cur, vmax);
     if (vmax > m) raise(vmax, s2);
     const float2 sc = make_float2(s2, s2), off = make_float2(-mL, -mL);
 #pragma unroll
@@ -220,12 +222,31 @@ struct Part {
   int64_t t0, v0, v1;
 };
 
+// A thread's share of a part, its slice: the vectors v0 + tid, v0 + tid +
+// kThreads, ...; one of them is a round.  For the alternatives the sweep leaves
+// the maximum of every slice's segments of `rounds` rounds (kMaxSegs of them at
+// most, whole groups of kUnroll rounds).
+static constexpr int kMaxSegs = 8;
+template <int kThreads>
+struct Segments {
+  int rounds, count;
+  __device__ explicit Segments(const Part& p) {
+    const int all = (int)((p.v1 - p.v0 + kThreads - 1) / kThreads);
+    rounds = (all + kMaxSegs * kUnroll - 1) / (kMaxSegs * kUnroll) * kUnroll;
+    count = all > 0 ? (all + rounds - 1) / rounds : 0;
+  }
+  __device__ int64_t end(const Part& p, int seg) const {
+    const int64_t e = p.v0 + (int64_t)(seg + 1) * rounds * kThreads;
+    return e < p.v1 ? e : p.v1;
+  }
+};
+
 // The sweep for any values: x - m is formed first, exactly near the maximum
 // and without overflow to +inf, so that rows of the type's lowest value come
 // out uniform.  Out of line: few rows come here.
 template <typename T, int kThreads, bool kEnt>
 __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, float s2,
-                                       float* mine) {
+                                       float* seg_max) {
   constexpr int VEC = Storage<T>::kVec;
   Stat st{-INFINITY, 0.f, 0.f};
   auto one = [&](float x) {
@@ -242,14 +263,20 @@ __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, f
   };
   // sums of a few vectors apart, so that no long chain of additions forms
   Stat all{-INFINITY, 0.f, 0.f};
-  for (int64_t j = p.v0 + threadIdx.x; j < p.v1; j += kThreads) {
-    float x[VEC];
-    Storage<T>::unpack(__ldg(vec + j), x);
-    st = Stat{-INFINITY, 0.f, 0.f};
-    for (int e = 0; e < VEC; ++e) one(x[e]);
-    all = merge<kEnt>(all, st, s2);
+  const Segments<kThreads> segs(p);
+  int64_t j = p.v0 + threadIdx.x;
+  for (int seg = 0; seg < segs.count; ++seg) {
+    float cur = -INFINITY;
+    for (; j < segs.end(p, seg); j += kThreads) {
+      float x[VEC];
+      Storage<T>::unpack(__ldg(vec + j), x);
+      st = Stat{-INFINITY, 0.f, 0.f};
+      for (int e = 0; e < VEC; ++e) one(x[e]);
+      cur = fmaxf(cur, st.m);
+      all = merge<kEnt>(all, st, s2);
+    }
+    if (seg_max) seg_max[seg * kThreads + threadIdx.x] = cur;
   }
-  *mine = all.m;
   if ((int)threadIdx.x < p.head + p.tail) {
     const int i = threadIdx.x;
     st = Stat{-INFINITY, 0.f, 0.f};
@@ -268,24 +295,40 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   return v;
 }
 
-template <typename T, int kThreads, bool kEnt>
+template <typename T, int kThreads, bool kEnt, bool kTop>
 __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const Part& p, float low,
-                                           float s2, float* mine) {
+                                           float s2, float* seg_max) {
   Fast<T, kEnt> f;
   f.init(low, s2);
   const uint32_t low_word = Words<T>::floor_word(low);
   int64_t j = p.v0 + threadIdx.x;
-  for (; j + (kUnroll - 1) * kThreads < p.v1; j += kUnroll * kThreads) {
-    uint4 v[kUnroll];
+  auto run = [&](int64_t end) {
+    for (; j + (kUnroll - 1) * kThreads < end; j += kUnroll * kThreads) {
+      uint4 v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = ld_once(vec + j + u * kThreads);
-    f.take(v, low_word, s2);
+      for (int u = 0; u < kUnroll; ++u) v[u] = ld_once(vec + j + u * kThreads);
+      f.take(v, low_word, s2);
+    }
+    if (j < end) {  // the rest in one group too, filled up with the floor
+      uint4 v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        v[u] = j + u * kThreads < end ? ld_once(vec + j + u * kThreads)
+                                      : make_uint4(low_word, low_word, low_word, low_word);
+      f.take(v, low_word, s2);
+      j += kUnroll * kThreads;
+    }
+  };
+  if (kTop) {
+    const Segments<kThreads> segs(p);
+    for (int seg = 0; seg < segs.count; ++seg) {
+      f.cur = low;
+      run(segs.end(p, seg));
+      seg_max[seg * kThreads + threadIdx.x] = f.cur > low ? f.cur : -INFINITY;
+    }
+  } else {
+    run(p.v1);
   }
-  for (; j < p.v1; j += kThreads) {
-    uint4 v[1] = {ld_once(vec + j)};
-    f.take(v, low_word, s2);
-  }
-  *mine = f.m > low ? f.m : -INFINITY;
   if ((int)threadIdx.x < p.head + p.tail) {
     const int i = threadIdx.x;
     f.take1(Storage<T>::load1(row + (i < p.head ? i : p.t0 + i - p.head)), low, s2);
@@ -339,24 +382,23 @@ __device__ __forceinline__ unsigned long long key_of(float x, unsigned v) {
   return ((unsigned long long)order_of(x) << 32) | (0xFFFFFFFFu - v);
 }
 
-// Top-k.  A thread's slice is the 16-byte vectors tid, tid + kThreads, ... of
-// the row.  The sweep leaves every thread's maximum; the k-th largest of them
-// is a lower bound tau of the k-th largest logit, because k distinct logits
-// reach it, and only slices whose maximum reaches tau can hold one of the top
-// k.  So only those slices -- k of them, and those that tie -- are read
-// again (from L2), and their logits at or above tau collected; each collected
-// key's rank among them is its place in the answer.  The sweep itself pays
-// nothing for the alternatives.
+// Top-k.  The k-th largest of the slices' maxima is a lower bound tau of the
+// k-th largest logit, because k distinct logits reach it; and only segments
+// whose maximum reaches tau can hold one of the top k.  So only those segments
+// -- little more than k of them -- are read again (from L2), and their logits at
+// or above tau collected; each collected key's rank among them is its place in
+// the answer.  The sweep itself pays one maximum in kUnroll vectors for the
+// alternatives.
 template <int kThreads, int kVec>
 struct TopSmem {
-  // a batch of kBatch vectors a thread may pass the bound whole
-  static constexpr int kBatch = 1;
+  static constexpr int kBatch = 4;  // vectors a thread in flight
+  static constexpr int kCap = 4 * kThreads;
   static constexpr int kCompactAt = 2 * kThreads;
-  static constexpr int kCap = kCompactAt + kThreads * kVec * kBatch;
+  float seg_max[kMaxSegs * kThreads];
   unsigned long long key[kCap];
   unsigned long long best[GRPO_MAX_TOP_K];
-  unsigned ord[kThreads];        // each thread's maximum
-  unsigned short sel[kThreads];  // slices to read again, in index order
+  unsigned ord[kThreads];                   // each slice's maximum
+  unsigned short sel[kMaxSegs * kThreads];  // segments to read again: seg kThreads + tid
   int nsel, n;
   unsigned tau;
 };
@@ -368,7 +410,7 @@ __device__ void rank_keys(TopSmem<kThreads, kVec>& sm, int n, int k) {
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const unsigned long long mine = sm.key[i];
     int above = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int j = 0; j < n; ++j) above += sm.key[j] > mine;
     if (above < k) sm.best[above] = mine;
   }
@@ -376,30 +418,38 @@ __device__ void rank_keys(TopSmem<kThreads, kVec>& sm, int n, int k) {
 }
 
 template <typename T, int kThreads>
-__device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, int head,
-                                 float mine, int k,
+__device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, int head, int k,
                                  TopSmem<kThreads, Storage<T>::kVec>& sm) {
   constexpr int VEC = Storage<T>::kVec;
   using Smem = TopSmem<kThreads, VEC>;
   const int tid = threadIdx.x;
-  const bool has = p.v0 + tid < p.v1;
-  sm.ord[tid] = has ? order_of(mine) : 0u;
-  if (tid == 0) sm.n = 0;
+  const Segments<kThreads> segs(p);
+  unsigned mine = 0u;  // an empty slice is below every logit
+  if (p.v0 + tid < p.v1)
+    for (int i = 0; i < segs.count; ++i)
+      mine = max(mine, order_of(sm.seg_max[i * kThreads + tid]));
+  sm.ord[tid] = mine;
+  if (tid == 0) sm.n = sm.nsel = 0;
   __syncthreads();
   if (tid < 32) {
-    // tau: the largest bound, of 16 leading bits, that k maxima reach (a lower
-    // bound does as well, at the price of a slice or two more); two bits a
-    // step, the counts of the three candidates in one word
-    unsigned o[kThreads / 32];
+    // tau: the largest bound, of 16 leading bits, that the maxima of k out of
+    // at most 64 groups of slices reach (a lower bound than the slices' own
+    // does as well, at the price of a few segments more); two bits a step, the
+    // counts of the three candidates in one word
+    constexpr int kGroups = kThreads >= 64 ? 2 : 1;  // a lane
+    unsigned o[kGroups];
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) o[i] = sm.ord[tid + 32 * i];
+    for (int i = 0; i < kGroups; ++i) o[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i)
+      o[i % kGroups] = max(o[i % kGroups], sm.ord[tid + 32 * i]);
     unsigned t = 0;
-#pragma unroll
+#pragma unroll 1
     for (int b = 30; b >= 16; b -= 2) {
       const unsigned step = 1u << b;
       unsigned cnt = 0;
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i)
+      for (int i = 0; i < kGroups; ++i)
         cnt += (o[i] >= t + step ? 1u : 0u) + (o[i] >= t + 2 * step ? 1u << 10 : 0u) +
                (o[i] >= t + 3 * step ? 1u << 20 : 0u);
       cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
@@ -408,62 +458,95 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
            : ((cnt & 1023u) >= (unsigned)k)         ? step
                                                     : 0u;
     }
-    // the slices that reach it, in index order
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      const bool in = o[i] >= t && o[i] != 0u;
-      const unsigned b = __ballot_sync(0xFFFFFFFFu, in);
-      if (in) sm.sel[at + __popc(b & ((1u << tid) - 1u))] = (unsigned short)(tid + 32 * i);
-      at += __popc(b);
-    }
-    if (tid == 0) {
-      sm.nsel = at;
-      sm.tau = t;
-    }
+    if (tid == 0) sm.tau = t;
   }
   __syncthreads();
-  unsigned long long bound = (unsigned long long)sm.tau << 32;
-  const int nsel = sm.nsel;
+  const unsigned tau = sm.tau;
+  if (mine >= tau && mine != 0u)
+    for (int i = 0; i < segs.count; ++i)
+      if (order_of(sm.seg_max[i * kThreads + tid]) >= tau)
+        sm.sel[atomicAdd(&sm.nsel, 1)] = (unsigned short)(i * kThreads + tid);
+  unsigned long long bound = (unsigned long long)tau << 32;
   auto push = [&](float x, int64_t v) {
     const unsigned long long key = key_of(x, (unsigned)v);
-    if (key >= bound) sm.key[atomicAdd(&sm.n, 1)] = key;
+    if (key >= bound) {
+      const int i = atomicAdd(&sm.n, 1);
+      if (i < Smem::kCap) sm.key[i] = key;
+    }
   };
   // row ends outside the vectors (fewer than kVec on either side)
   if (tid < p.head) push(Storage<T>::load1(row + tid), tid);
   if (tid < p.tail) push(Storage<T>::load1(row + p.t0 + tid), p.t0 + tid);
-  // vectors in index order: j steps over the slices' length, i over the slices
-  const unsigned total = (unsigned)nsel * (unsigned)((p.v1 - p.v0 + kThreads - 1) / kThreads);
+  __syncthreads();
+  const unsigned nsel = (unsigned)sm.nsel, total = nsel * (unsigned)segs.rounds;
+  // keeps the k best keys so far, which raises the bound; at least k are held
+  auto compact = [&](int n) {
+    rank_keys(sm, n, k);
+    if (tid < k) sm.key[tid] = sm.best[tid];
+    if (tid == 0) sm.n = k;
+    bound = sm.best[k - 1] + 1;  // the k-th itself is held
+    __syncthreads();
+  };
   for (unsigned q0 = 0; q0 < total; q0 += Smem::kBatch * kThreads) {
     uint4 v[Smem::kBatch];
-    int64_t at[Smem::kBatch];
+    unsigned at[Smem::kBatch];  // vector of the part
+    const unsigned nvec = (unsigned)(p.v1 - p.v0);
+    const int held = sm.n;
 #pragma unroll
     for (int u = 0; u < Smem::kBatch; ++u) {
       const unsigned q = q0 + tid + u * kThreads;
-      at[u] = p.v1;
-      if (q < total) at[u] = p.v0 + sm.sel[q % nsel] + (q / nsel) * kThreads;
-      if (at[u] < p.v1) v[u] = __ldg(vec + at[u]);
+      at[u] = nvec;
+      if (q < total) {
+        const unsigned seg = sm.sel[q % nsel];
+        at[u] = (seg / kThreads * segs.rounds + q / nsel) * kThreads + seg % kThreads;
+        if (at[u] < nvec) v[u] = __ldg(vec + p.v0 + at[u]);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < Smem::kBatch; ++u) {
-      if (at[u] >= p.v1) continue;
+    // the keys of a vector that pass, with one reservation
+    auto push_vec = [&](const uint4& w, unsigned i) {
       float x[VEC];
-      Storage<T>::unpack(v[u], x);
+      Storage<T>::unpack(w, x);
+      const unsigned e0 = (unsigned)(head + (p.v0 + i) * VEC);
+      unsigned pass = 0;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) push(x[e], head + at[u] * VEC + e);
-    }
+      for (int e = 0; e < VEC; ++e) pass |= (key_of(x[e], e0 + e) >= bound ? 1u : 0u) << e;
+      if (pass == 0) return;
+      int to = atomicAdd(&sm.n, __popc(pass));
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (pass >> e & 1u) {
+          if (to < Smem::kCap) sm.key[to] = key_of(x[e], e0 + e);
+          ++to;
+        }
+    };
+    __syncthreads();  // every thread has read sm.n
+#pragma unroll
+    for (int u = 0; u < Smem::kBatch; ++u)
+      if (at[u] < nvec) push_vec(v[u], at[u]);
     __syncthreads();
-    // many ties: keep the k best so far, which raises the bound
     const int n = sm.n;
-    if (n > Smem::kCompactAt) {
-      rank_keys(sm, n, k);
-      if (tid < k) sm.key[tid] = sm.best[tid];
-      if (tid == 0) sm.n = k;
-      bound = sm.best[k - 1];
-      // the k-th key itself is held already
-      bound += 1;
+    if (n > Smem::kCap) {
+      // ties: again, in steps that fit, from the keys that were held before
+      __syncthreads();
+      if (tid == 0) sm.n = held;
+      __syncthreads();
+      constexpr int kStep = (Smem::kCap - Smem::kCompactAt) / VEC;  // threads a step
+#pragma unroll 1
+      for (int u = 0; u < Smem::kBatch; ++u)
+#pragma unroll 1
+        for (int t0 = 0; t0 < kThreads; t0 += kStep) {
+          if (tid >= t0 && tid < t0 + kStep) {
+            const unsigned i = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
+            if (i < nvec) push_vec(__ldg(vec + p.v0 + i), i);
+          }
+          __syncthreads();
+          const int m = sm.n;
+          __syncthreads();
+          if (m > Smem::kCompactAt) compact(m);
+        }
+    } else if (n > Smem::kCompactAt) {
+      compact(n);
     }
-    __syncthreads();
   }
   __syncthreads();
   rank_keys(sm, sm.n, k);
@@ -482,6 +565,41 @@ __device__ __forceinline__ void finish_row(const TokenArgs& a, int64_t r, float 
   }
 }
 
+// The outputs of a masked row, by the first threads of a warp or more.
+template <bool kEnt, bool kTop>
+__device__ __forceinline__ void masked_row(const TokenArgs& a, int64_t r, int lane) {
+  if (lane == 0) {
+    if (a.logps) a.logps[r] = 0.f;
+    if (kEnt) a.entropy[r] = 0.f;
+    if (a.stats) {
+      a.stats[r] = 0.f;
+      a.stats[a.B * a.T + r] = 1.f;
+    }
+  }
+  if (kTop && lane < a.k) {
+    a.top_ids[r * a.k + lane] = -1;
+    a.top_logps[r * a.k + lane] = 0.f;
+  }
+}
+
+// Alternative i of row r.
+__device__ __forceinline__ void put_top(const TokenArgs& a, int64_t r, int i,
+                                        unsigned long long key, const Stat& st) {
+  const float x = order_value((unsigned)(key >> 32));
+  a.top_ids[r * a.k + i] = (int64_t)(0xFFFFFFFFu - (unsigned)key);
+  a.top_logps[r * a.k + i] = (x - st.m) * a.inv_t - logf(st.Z);
+}
+
+// Whether row r has a distribution; if not, its alternatives are marked so.
+__device__ __forceinline__ bool has_top(const TokenArgs& a, int64_t r, const Stat& st) {
+  if (st.Z <= 3.4e38f) return true;  // not NaN, not +inf
+  if ((int)threadIdx.x < a.k) {
+    a.top_ids[r * a.k + threadIdx.x] = -1;
+    a.top_logps[r * a.k + threadIdx.x] = NAN;
+  }
+  return false;
+}
+
 // What the CTAs of a cluster leave in its first CTA's shared memory.
 static constexpr int kMaxCluster = 8;
 struct Parts {
@@ -494,7 +612,7 @@ struct Parts {
 // thread in flight, a tree over the threads, the part's alternatives, and in
 // a cluster the parts joined by its first CTA.
 template <typename T, int kThreads, bool kEnt, bool kTop, bool kSplit>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : 1)
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 11 : kThreads == 256 && !kSplit ? 6 : 1024 / kThreads)
 token_logps_kernel(const TokenArgs a) {
   constexpr int VEC = Storage<T>::kVec;
   __shared__ Stat warp_stat[kThreads / 32];
@@ -506,21 +624,9 @@ token_logps_kernel(const TokenArgs a) {
     rank = cg::this_cluster().block_rank();
     ctas = cg::this_cluster().num_blocks();
   }
-  const int64_t r = blockIdx.x / ctas, rows = a.B * a.T;
+  const int64_t r = blockIdx.x / ctas;
   if (a.mask && !a.mask[r]) {  // the whole cluster
-    if (rank != 0) return;
-    if (tid == 0) {
-      if (a.logps) a.logps[r] = 0.f;
-      if (kEnt) a.entropy[r] = 0.f;
-      if (a.stats) {
-        a.stats[r] = 0.f;
-        a.stats[rows + r] = 1.f;
-      }
-    }
-    if (kTop && tid < a.k) {
-      a.top_ids[r * a.k + tid] = -1;
-      a.top_logps[r * a.k + tid] = 0.f;
-    }
+    if (rank == 0) masked_row<kEnt, kTop>(a, r, tid);
     return;
   }
   const unsigned b = (unsigned)r / (unsigned)a.T, t = (unsigned)r % (unsigned)a.T;
@@ -544,23 +650,24 @@ token_logps_kernel(const TokenArgs a) {
       atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
   }
   const float s2 = a.s2;
-  float mine;
+  float* seg_max = nullptr;
+  if constexpr (kTop) seg_max = top.seg_max;
   Stat st;
   bool fast = a.low < 0.f;
   if (fast) {
     st = cta_stat<kThreads, kEnt>(
-        sweep_fast<T, kThreads, kEnt>(row, vec, p, a.low, s2, &mine), s2, warp_stat);
+        sweep_fast<T, kThreads, kEnt, kTop>(row, vec, p, a.low, s2, seg_max), s2, warp_stat);
     fast = fabsf(st.m) * s2 <= kFastRange && st.m > 0.5f * a.low;
   }
   if (!fast)
-    st = cta_stat<kThreads, kEnt>(sweep_any<T, kThreads, kEnt>(row, vec, p, s2, &mine), s2,
+    st = cta_stat<kThreads, kEnt>(sweep_any<T, kThreads, kEnt>(row, vec, p, s2, seg_max), s2,
                                   warp_stat);
   if constexpr (kSplit) {
     // every CTA of the cluster runs before its shared memory is written
     cg::cluster_group cluster = cg::this_cluster();
     if constexpr (kTop) {
       // a part may hold fewer than k logits
-      top_alternatives<T, kThreads>(row, vec, p, g.head, mine, a.k, top);
+      top_alternatives<T, kThreads>(row, vec, p, g.head, a.k, top);
     }
     cluster.sync();
     Parts* first = cluster.map_shared_rank(&parts, 0);
@@ -577,18 +684,7 @@ token_logps_kernel(const TokenArgs a) {
   if (st.m == -INFINITY) st.Z = NAN;  // no finite logit: no distribution
   if (tid == 0) finish_row<kEnt>(a, r, xa, st);
   if constexpr (kTop) {
-    if (!(st.Z <= 3.4e38f)) {  // NaN or +inf
-      if (tid < a.k) {
-        a.top_ids[r * a.k + tid] = -1;
-        a.top_logps[r * a.k + tid] = NAN;
-      }
-      return;
-    }
-    auto put = [&](int i, unsigned long long key) {
-      const float x = order_value((unsigned)(key >> 32));
-      a.top_ids[r * a.k + i] = (int64_t)(0xFFFFFFFFu - (unsigned)key);
-      a.top_logps[r * a.k + i] = (x - st.m) * a.inv_t - logf(st.Z);
-    };
+    if (!has_top(a, r, st)) return;
     if constexpr (kSplit) {
       // a key's place: how many keys of each part lie above it, by bisection
       // of the parts' ordered lists, all parts at once
@@ -599,7 +695,7 @@ token_logps_kernel(const TokenArgs a) {
         int above[kMaxCluster];
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q) above[q] = 0;
-#pragma unroll
+#pragma unroll 1
         for (int step = GRPO_MAX_TOP_K / 2; step > 0; step /= 2)
 #pragma unroll
           for (int q = 0; q < kMaxCluster; ++q)
@@ -608,19 +704,24 @@ token_logps_kernel(const TokenArgs a) {
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q)
           if (q < (int)ctas) place += above[q] + (parts.key[q][above[q]] > key);
-        if (place < a.k) put(place, key);
+        if (place < a.k) put_top(a, r, place, key, st);
       }
     } else {
-      top_alternatives<T, kThreads>(row, vec, p, g.head, mine, a.k, top);
-      if (tid < a.k) put(tid, top.best[tid]);
+      top_alternatives<T, kThreads>(row, vec, p, g.head, a.k, top);
+      if (tid < a.k) put_top(a, r, tid, top.best[tid], st);
     }
   }
 }
 
-// Rows of at most this many bytes go to one warp, longer ones to 256 threads.
-static constexpr int64_t kWarpRowBytes = 4096;
-// A cluster's CTA gets at least this much of a row.
-static constexpr int64_t kPartBytes = 8192;
+// Rows of at most kWarpRowBytes go to one warp, rows from kLongRowBytes on (and
+// few rows) to 256 threads, those between to 128: more and smaller CTAs hide the ends of
+// short rows better, and on long rows too few CTAs are left at the end (us at
+// 128 / 256 threads: 64 KB rows, ragged 64 x 1024, 337 / 371; 8192 of them with
+// 8 alternatives 109 / 136; 304 KB rows, 2048, 117 / 107).
+static constexpr int64_t kWarpRowBytes = 4096, kLongRowBytes = 128 * 1024;
+// A cluster's CTA gets at least this much of a row (40 rows of 64 KB: 4 parts
+// 3.7 us, 8 parts 4.6 us; 152 rows: 2 parts 4.3, 4 parts 6.8).
+static constexpr int64_t kPartBytes = 16384;
 
 template <typename T, int kThreads, bool kSplit>
 static cudaError_t launch_logps_t(const TokenArgs& a, unsigned ctas, cudaStream_t s) {
@@ -659,12 +760,15 @@ static cudaError_t launch_logps_d(TokenArgs a, cudaStream_t s) {
   a.low = floor_of<T>(a.s2);
   const int64_t bytes = a.V * (int64_t)sizeof(T), rows = a.B * a.T;
   if (bytes <= kWarpRowBytes) return launch_logps_t<T, 32, false>(a, 1, s);
-  // few rows: a cluster for each, while the CTAs all run at once
+  // few rows: a cluster for each, while its CTAs are at most two an SM (four
+  // for two halves of a long row)
   unsigned ctas = 1;
-  while (ctas < kMaxCluster && rows * (2 * ctas) <= 152 * 4 && bytes / (2 * ctas) >= kPartBytes)
+  while (ctas < kMaxCluster && rows * (2 * ctas) <= 2 * 152 && bytes / (2 * ctas) >= kPartBytes)
     ctas *= 2;
-  return ctas == 1 ? launch_logps_t<T, 256, false>(a, 1, s)
-                   : launch_logps_t<T, 256, true>(a, ctas, s);
+  if (ctas == 1 && rows <= 2 * 152 && bytes >= kLongRowBytes) ctas = 2;
+  if (ctas > 1) return launch_logps_t<T, 256, true>(a, ctas, s);
+  return rows > 2 * 152 && bytes < kLongRowBytes ? launch_logps_t<T, 128, false>(a, 1, s)
+                                                 : launch_logps_t<T, 256, false>(a, 1, s);
 }
 
 cudaError_t launch_token_logps(const TokenArgs& a, grpo_dtype_t dt, cudaStream_t s) {

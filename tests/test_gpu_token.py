@@ -361,3 +361,35 @@ def test_python_refusals():
     with pytest.raises(g.GrpoError):  # rows of the gradient overlap
         g.grpo_token_logps_grad(x, ids, mask, f["stats"], grad_logps=w,
                                 grad=torch.empty((1, 1, 50), device="cuda").expand(2, 3, 50))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("B,T,V,pad,k", [(40, 30, 8192, 0, 0), (31, 37, 8219, 0, 7),
+                                         (25, 40, 16411, 5, 32), (1100, 1, 50001, 0, 3)])
+def test_many_rows(dtype, B, T, V, pad, k):
+    """Enough rows for CTAs to take several: ragged masks, rows of special
+    values between ordinary ones, ids out of range."""
+    x, ids, mask = make(B, T, V, dtype, pad, seed=V, p_mask=0.4)
+    if T > 1:
+        mask &= torch.arange(T, device="cuda")[None] < torch.randint(0, T + 1, (B, 1), device="cuda")
+    low = torch.finfo(DT[dtype]).min
+    rows = x.reshape(B * T, -1)[:, :V] if pad == 0 else x.flatten(0, 1)
+    for i, v in enumerate((-math.inf, low, math.nan, math.inf, 0.0)):
+        rows[5 + 7 * i] = v
+        rows[300 + 11 * i, 3:] = v
+    x = rows.reshape(B, T, V)
+    flat = ids.flatten()
+    flat[600:640:5] = V
+    st = g.status_buffer()
+    got = g.grpo_token_logps(x, ids, mask, top_k=k, want_entropy=True, want_stats=True, status=st)
+    ref = forward(x, ids, mask, 1.0, k)
+    del got["stats"]
+    check_forward(got, ref, x)
+    seen = bool((mask.flatten() & (flat == V)).any())
+    assert g.grpo_read_device_status(st) == (g.GRPO_ERR_ACTION_RANGE if seen else 0)
+    again = g.grpo_token_logps(x, ids, mask, top_k=k, want_entropy=True)
+    for n in ("logps", "entropy", "top_ids", "top_logps"):
+        if got[n] is not None:
+            assert torch.equal(got[n].nan_to_num(), again[n].nan_to_num())
+    alone = g.grpo_token_logps(x, ids, mask)
+    assert torch.equal(alone["logps"].nan_to_num(), got["logps"].nan_to_num())
