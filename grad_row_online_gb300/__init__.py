@@ -825,19 +825,25 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
             raise ValueError("out must be contiguous as tensors are, or have their strides")
         out_ptrs = array.array("Q", [o.data_ptr() for o in out])
     L = lib()
-    with _AllocateOn(stream):
-        out2 = torch.empty(2, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(L.grpo_clip_workspace_size(n), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        need = 0
+    else:
+        need = L.grpo_clip_workspace_size(n)
+    with _AllocateOn(stream):  # norm, factor and 256 bytes further on the workspace
+        out2 = torch.empty(64 + need // 4 if need else 2, dtype=torch.float32, device=dev)
+    out2_p, size = out2.data_ptr(), need
+    ws = out2_p + 256
+    if workspace is not None:
+        ws, size = workspace.data_ptr(), workspace.nbytes
     ptrs, numels, dtypes = array.array("Q", ptrs), array.array("q", numels), array.array("i", dtypes)
     rc = L.grpo_clip_grad_norm(ptrs.buffer_info()[0],
                                None if out_ptrs is None else out_ptrs.buffer_info()[0],
                                numels.buffer_info()[0], dtypes.buffer_info()[0], n, max_norm, eps,
-                               scale, GRPO_CLIP_NORM_ONLY if norm_only else 0, out2.data_ptr(),
-                               workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
+                               scale, GRPO_CLIP_NORM_ONLY if norm_only else 0, out2_p, ws, size,
+                               _stream_on(stream, dev))
     _check(rc, "grpo_clip_grad_norm")
-    norm, factor = out2.unbind()
-    return {"norm": norm, "factor": factor, "workspace": workspace}
+    return {"norm": out2[0], "factor": out2[1]}
 
 
 def grpo_read_device_status(workspace: torch.Tensor, stream=None) -> int:

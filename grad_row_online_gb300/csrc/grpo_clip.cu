@@ -86,11 +86,15 @@ struct ClipChunk {
   T* out;
   int n, head, nvec, t0;
   __device__ ClipChunk(const ClipEntry& e, unsigned c) {
-    const int64_t at = (int64_t)(c - e.chunk0) * kClipChunk;
+    // chunks are cut at 16-byte boundaries of the input: all but a tensor's
+    // first and last are whole vectors
+    const int64_t skew = ((uintptr_t)e.in & 15) / sizeof(T);
     const int64_t size = (int64_t)(e.n & ((1ull << 62) - 1));
+    const int64_t end = (int64_t)(c - e.chunk0 + 1) * kClipChunk - skew;
+    const int64_t at = c == e.chunk0 ? 0 : end - kClipChunk;
     in = (const T*)e.in + at;
     out = (T*)e.out + at;
-    n = (int)(size - at < kClipChunk ? size - at : kClipChunk);
+    n = (int)((size < end ? size : end) - at);
     head = (int)(((16 - ((uintptr_t)in & 15)) & 15) / sizeof(T));
     if (head > n) head = n;
     nvec = (n - head) / Storage<T>::kVec;
@@ -313,7 +317,8 @@ static void fill_table(const ClipArgs& a, int64_t* i, ClipTable<kCap>* t) {
     e.out = a.outs ? a.outs[*i] : const_cast<void*>(a.tensors[*i]);
     e.n = (unsigned long long)n | (unsigned long long)a.dtypes[*i] << 62;
     e.chunk0 = t->chunks;
-    t->chunks += (unsigned)((n + kClipChunk - 1) / kClipChunk);
+    const int64_t skew = ((uintptr_t)e.in & 15) / (a.dtypes[*i] == GRPO_F32 ? 4 : 2);
+    t->chunks += (unsigned)((n + skew + kClipChunk - 1) / kClipChunk);
   }
 }
 
