@@ -109,6 +109,11 @@ grpo_status_t check_token_shape(int64_t B, int64_t T, int64_t V, int64_t sb, int
   return span < 4.0e18 ? GRPO_OK : GRPO_ERR_SHAPE;
 }
 
+// 1 / temperature and log2(e) / temperature are fp32 numbers.
+bool temperature_ok(float t) {
+  return isfinite(t) && t > 0.f && isfinite((float)(1.4426950408889634 / (double)t));
+}
+
 // Whether no two of the B x T rows of V elements overlap: the rows of the
 // axis with the smaller stride are at least V apart, and the other axis steps
 // over all of them.
@@ -572,8 +577,7 @@ extern "C" grpo_status_t grpo_token_logps(
   if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
   grpo_status_t st = check_token_shape(B, T, V, stride_b, stride_t);
   if (st != GRPO_OK) return st;
-  if (!(isfinite(temperature) && temperature > 0.f) || !isfinite(1.f / temperature))
-    return GRPO_ERR_PARAM;
+  if (!temperature_ok(temperature)) return GRPO_ERR_PARAM;
   if (top_k < 0 || top_k > GRPO_MAX_TOP_K || top_k > V) return GRPO_ERR_PARAM;
   if (B * T > 0 && (!logits || (logps && !action_ids) || (top_k > 0 && (!top_ids || !top_logps))))
     return GRPO_ERR_NULL;
@@ -600,8 +604,7 @@ extern "C" grpo_status_t grpo_token_logps_grad(
   if (st != GRPO_OK) return st;
   if ((st = check_token_shape(B, T, V, grad_stride_b, grad_stride_t)) != GRPO_OK) return st;
   if (!rows_disjoint(B, T, V, grad_stride_b, grad_stride_t)) return GRPO_ERR_SHAPE;
-  if (!(isfinite(temperature) && temperature > 0.f) || !isfinite(1.f / temperature))
-    return GRPO_ERR_PARAM;
+  if (!temperature_ok(temperature)) return GRPO_ERR_PARAM;
   if (flags & ~GRPO_SKIP_MASKED_GRAD_ROWS) return GRPO_ERR_PARAM;
   if (B * T > 0 && ((!grad_logps && !grad_entropy) || !logits || !stats || !grad_logits ||
                     (grad_logps && !action_ids) || (grad_entropy && !entropy)))

@@ -222,17 +222,28 @@ struct Part {
   int64_t t0, v0, v1;
 };
 
+// 16-byte loads a thread of the sweep has in flight, and the CTAs an SM that
+// leaves registers for (us for 2048 rows of 304 KB at 256 threads: 6 CTAs x 4
+// loads 107, 5 x 5 100.5, 5 x 6 100.6, 4 x 8 101.4, 5 x 8 134; ragged 64 x 1024
+// rows of 64 KB at 128 threads: 11 x 4 342, 12 x 3 354, 10 x 5 353, 9 x 6 359).
+template <int kThreads>
+__host__ __device__ constexpr int in_flight() { return kThreads == 256 ? 5 : 4; }
+template <int kThreads, bool kSplit>
+__host__ __device__ constexpr int ctas_per_sm() {
+  return kThreads == 128 ? 11 : kThreads == 256 && !kSplit ? 5 : 1024 / kThreads;
+}
+
 // A thread's share of a part, its slice: the vectors v0 + tid, v0 + tid +
 // kThreads, ...; one of them is a round.  For the alternatives the sweep leaves
 // the maximum of every slice's segments of `rounds` rounds (kMaxSegs of them at
-// most, whole groups of kUnroll rounds).
+// most, whole groups of loads in flight).
 static constexpr int kMaxSegs = 8;
 template <int kThreads>
 struct Segments {
   int rounds, count;
   __device__ explicit Segments(const Part& p) {
     const int all = (int)((p.v1 - p.v0 + kThreads - 1) / kThreads);
-    rounds = (all + kMaxSegs * kUnroll - 1) / (kMaxSegs * kUnroll) * kUnroll;
+    rounds = (all + kMaxSegs * in_flight<kThreads>() - 1) / (kMaxSegs * in_flight<kThreads>()) * in_flight<kThreads>();
     count = all > 0 ? (all + rounds - 1) / rounds : 0;
   }
   __device__ int64_t end(const Part& p, int seg) const {
@@ -303,20 +314,20 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   const uint32_t low_word = Words<T>::floor_word(low);
   int64_t j = p.v0 + threadIdx.x;
   auto run = [&](int64_t end) {
-    for (; j + (kUnroll - 1) * kThreads < end; j += kUnroll * kThreads) {
-      uint4 v[kUnroll];
+    for (; j + (in_flight<kThreads>() - 1) * kThreads < end; j += in_flight<kThreads>() * kThreads) {
+      uint4 v[in_flight<kThreads>()];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) v[u] = ld_once(vec + j + u * kThreads);
+      for (int u = 0; u < in_flight<kThreads>(); ++u) v[u] = ld_once(vec + j + u * kThreads);
       f.take(v, low_word, s2);
     }
     if (j < end) {  // the rest in one group too, filled up with the floor
-      uint4 v[kUnroll];
+      uint4 v[in_flight<kThreads>()];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
+      for (int u = 0; u < in_flight<kThreads>(); ++u)
         v[u] = j + u * kThreads < end ? ld_once(vec + j + u * kThreads)
                                       : make_uint4(low_word, low_word, low_word, low_word);
       f.take(v, low_word, s2);
-      j += kUnroll * kThreads;
+      j += in_flight<kThreads>() * kThreads;
     }
   };
   if (kTop) {
@@ -387,7 +398,7 @@ __device__ __forceinline__ unsigned long long key_of(float x, unsigned v) {
 // whose maximum reaches tau can hold one of the top k.  So only those segments
 // -- little more than k of them -- are read again (from L2), and their logits at
 // or above tau collected; each collected key's rank among them is its place in
-// the answer.  The sweep itself pays one maximum in kUnroll vectors for the
+// the answer.  The sweep itself pays one maximum in four vectors for the
 // alternatives.
 template <int kThreads, int kVec>
 struct TopSmem {
@@ -608,11 +619,10 @@ struct Parts {
 };
 
 // One CTA per row, or with kSplit a cluster of CTAs, each of which takes a
-// contiguous part of the row's vectors: a sweep with kUnroll 16-byte loads a
-// thread in flight, a tree over the threads, the part's alternatives, and in
-// a cluster the parts joined by its first CTA.
+// contiguous part of the row's vectors: a sweep, a tree over the threads, the
+// part's alternatives, and in a cluster the parts joined by its first CTA.
 template <typename T, int kThreads, bool kEnt, bool kTop, bool kSplit>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 11 : kThreads == 256 && !kSplit ? 6 : 1024 / kThreads)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<kThreads, kSplit>())
 token_logps_kernel(const TokenArgs a) {
   constexpr int VEC = Storage<T>::kVec;
   __shared__ Stat warp_stat[kThreads / 32];

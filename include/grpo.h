@@ -416,7 +416,8 @@ grpo_status_t grpo_vocab_grad(const void *policy_slice, grpo_dtype_t dt, int64_t
  *   completion_mask : [B,T] uint8, NULL = every token active.  A masked
  *                     token's logits and id are not read; its outputs are 0
  *                     (top ids -1, stats {0, 1}).
- *   temperature     : finite, > 0.
+ *   temperature     : finite, > 0, and not so small (4.3e-39) that
+ *                     log2(e) / temperature overflows.
  *   top_k           : 0 .. GRPO_MAX_TOP_K, at most V.
  *   logps, entropy  : [B,T] f32, each nullable.
  *   stats           : [2,B,T] f32, nullable: m and Z, what the gradient needs.

@@ -393,3 +393,51 @@ def test_many_rows(dtype, B, T, V, pad, k):
             assert torch.equal(got[n].nan_to_num(), again[n].nan_to_num())
     alone = g.grpo_token_logps(x, ids, mask)
     assert torch.equal(alone["logps"].nan_to_num(), got["logps"].nan_to_num())
+
+
+@pytest.mark.parametrize("rows", [3, 400])
+@pytest.mark.parametrize("offset", [3e3, 1e5, -1e5, 1e20, -1e20])
+def test_offsets(rows, offset):
+    """Logits far from zero: rows that the fast arithmetic does not take."""
+    V, k = 20000, 6
+    x, ids, _ = make(rows, 1, V, "f32", seed=7)
+    x = x + offset
+    x[rows // 2] -= offset  # one row that it does take
+    got = scores(x, ids, None, k)
+    check_forward(got, forward(x, ids, None, 1.0, k), x)
+    w = torch.linspace(-1, 1, rows, device="cuda")[:, None].contiguous()
+    h = torch.full_like(w, 0.5)
+    d = g.grpo_token_logps_grad(x, ids, None, got["stats"], grad_logps=w, entropy=got["entropy"],
+                                grad_entropy=h)
+    check_gradient(d, *gradient(x, ids, None, w, h), x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("temperature", [1e-35, 1e-4, 0.02, 40.0, 1e4, 1e36])
+def test_temperatures(dtype, temperature):
+    x, ids, mask = make(3, 5, 5001, dtype, seed=11)
+    ids[0] = x[0].argmax(-1)
+    k = 5
+    got = scores(x, ids, mask, k, temperature)
+    s = torch.tensor(1.0 / temperature, dtype=torch.float64).to(torch.float32).double().item()
+    ref = forward(x, ids, mask, 1.0 / s, k)  # the fp32 scale itself
+    V, n = 5001, 5001 / 256 / 4 + 20
+    top = ref["top_logps"].abs()
+    # a log-prob of |s t| carries three roundings of its own size; sums as in check_forward
+    lnV = math.log(V)
+    z_err = 2.0 ** -24 * (n + 4 * lnV + 16)
+    tol = lambda v: 2.0 ** -24 * (6 * v.abs().nan_to_num(0, 0, 0) + 4 * lnV + 4) + z_err
+    assert_close(got["logps"], ref["logps"], tol(ref["logps"]), "logps")
+    assert torch.equal(got["top_ids"], ref["top_ids"])
+    assert_close(got["top_logps"], ref["top_logps"], tol(ref["top_logps"]), "top_logps")
+    assert_close(got["entropy"], ref["entropy"], 2.0 ** -24 * (6 * lnV + 8) + z_err * (1 + 2 * lnV),
+                 "entropy")
+
+
+def test_null_stream():
+    x, ids, mask = make(2, 3, 9000, "bf16")
+    want = scores(x, ids, mask, 2)
+    torch.cuda.synchronize()
+    got = g.grpo_token_logps(x, ids, mask, top_k=2, want_entropy=True, want_stats=True, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[n], want[n]) for n in want)

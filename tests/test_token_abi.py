@@ -21,7 +21,7 @@ def test_token_logps_rejects_bad_arguments(lib):  # noqa: F811
     for kw in (dict(B=-1), dict(T=-1), dict(V=0), dict(V=1 << 31), dict(T=(1 << 30) + 1),
                dict(B=1 << 20, T=1 << 20), dict(sb=-1), dict(st=-1), dict(sb=1 << 62)):
         assert _fwd(lib, **kw) == 2, kw
-    for t in (0.0, -1.0, math.nan, math.inf, 1e-45):
+    for t in (0.0, -1.0, math.nan, math.inf, 1e-45, 4.1e-39):
         assert _fwd(lib, temp=t) == 6, t
     assert _fwd(lib, k=-1) == 6
     assert _fwd(lib, k=33, ti=FAKE, tl=FAKE) == 6
