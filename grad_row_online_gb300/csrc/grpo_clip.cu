@@ -11,8 +11,14 @@
 //                      double of the workspace
 //   clip_scale_kernel  every CTA adds all those doubles in one fixed order,
 //                      which gives it c, and scales its chunks
-// Both read at memory speed: a chunk is cut from one tensor, its elements
-// taken as 16-byte vectors where the tensor's alignment allows.
+// A chunk is cut from one tensor, its elements taken as 16-byte vectors where
+// the tensor's alignment allows.
+//
+// Bound by memory: the tensors are read once for the norm and, where they are
+// larger than L2, again to be scaled.  291 bf16 tensors of 3.6 GB: norm 506 us
+// (7.0 TB/s), both 1563 us for 10.7 GB (6.8 TB/s, the rate of a copy); 111
+// packed tensors of mixed types, 0.45 GB: 91 and 233 us.  Unclipped in place
+// 517 us: the second kernel returns.  21 small tensors: 11.7 us on the GPU.
 #include "grpo_internal.cuh"
 
 namespace grpo {

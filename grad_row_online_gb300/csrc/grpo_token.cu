@@ -10,7 +10,13 @@
 // Z' = 2^d Z, D' = 2^d (D + d Z)).
 //
 //   token_logps_kernel  one CTA, or a cluster of CTAs, per row
-//   token_grad_kernel   one CTA per row and chunk of the row
+//   token_grad_kernel   one CTA per row and up to 64 KB of it
+//
+// Both are bound by memory: 2 or 4 bytes a logit read once, against about five
+// issued instructions a bf16 logit of the ten that memory speed leaves room
+// for; the gradient also writes as much.  Sums are fp32 (a thread adds 1/128
+// or less of a row, in groups of eight, then a tree), so ln Z is good to a few
+// 1e-7, as log-probs in fp32 are.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -621,6 +627,14 @@ struct Parts {
 // One CTA per row, or with kSplit a cluster of CTAs, each of which takes a
 // contiguous part of the row's vectors: a sweep, a tree over the threads, the
 // part's alternatives, and in a cluster the parts joined by its first CTA.
+// Many independent CTAs an SM keep memory busy over the ends of rows: 36,836 of
+// 65,536 rows of 32768 bf16 logits take 339 us (7.1 TB/s; 38 % of the ALU pipe,
+// 37 % of the exponential unit, 52 % of issue), 4,601 of 8,192 rows of 151936
+// with 8 alternatives 235 us (6.0 TB/s), 4,337 rows of 128256 fp32 304 us (7.3
+// TB/s).  One row of 32768 with 5 alternatives 7.1 us, 64 of 151936 with 20
+// 11.1 us.  (A persistent form -- a producer warp streaming rows through a ring
+// of bulk copies -- measured 387 us and 322 us on the first two when they took
+// 368 and 265: its three CTAs an SM hide a row's end worse.)
 template <typename T, int kThreads, bool kEnt, bool kTop, bool kSplit>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<kThreads, kSplit>())
 token_logps_kernel(const TokenArgs a) {
@@ -889,7 +903,11 @@ __device__ __forceinline__ void grad_steps(const T* in, T* out, int64_t step0, i
 }
 
 // CTA c of a row takes its steps [c per, (c + 1) per); the row's unaligned
-// ends go to its first CTA.
+// ends go to its first CTA.  Bound by memory: 64 x 512 rows of 32768 bf16 logits
+// (18,404 active) with an entropy term 490 us, 6.85 TB/s; 16 x 256 rows of
+// 128256 fp32 435 us, 6.9 TB/s: the rate of a copy.  Four steps a CTA against
+// one: 182 and 213 us on 8,192 rows of 32768; more CTAs an SM with fewer
+// registers (6 x 4 vectors, 8 x 2) 234 and 202 us.
 template <typename T, bool kEnt>
 __global__ void __launch_bounds__(kGradThreads)
 token_grad_kernel(const TokenGradArgs a, unsigned ctas, unsigned per) {
