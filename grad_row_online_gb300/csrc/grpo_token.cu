@@ -54,6 +54,21 @@ __device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float s2) {
   return r;
 }
 
+// A row's kThreads threads: a whole CTA, or one warp of a CTA of
+// kWarpRows rows.
+static constexpr int kWarpRows = 8;
+template <int kThreads>
+__device__ __forceinline__ int row_tid() {
+  return kThreads == 32 ? (int)threadIdx.x % 32 : (int)threadIdx.x;
+}
+template <int kThreads>
+__device__ __forceinline__ void row_sync() {
+  if (kThreads == 32) __syncwarp();
+  else __syncthreads();
+}
+template <int kThreads>
+__host__ __device__ constexpr int rows_per_cta() { return kThreads == 32 ? kWarpRows : 1; }
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -236,7 +251,7 @@ template <int kThreads>
 __host__ __device__ constexpr int in_flight() { return kThreads == 256 ? 5 : 4; }
 template <int kThreads, bool kSplit>
 __host__ __device__ constexpr int ctas_per_sm() {
-  return kThreads == 128 ? 11 : kThreads == 256 && !kSplit ? 5 : 1024 / kThreads;
+  return kThreads == 32 ? 6 : kThreads == 128 ? 11 : kThreads == 256 && !kSplit ? 5 : 4;
 }
 
 // A thread's share of a part, its slice: the vectors v0 + tid, v0 + tid +
@@ -281,7 +296,8 @@ __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, f
   // sums of a few vectors apart, so that no long chain of additions forms
   Stat all{-INFINITY, 0.f, 0.f};
   const Segments<kThreads> segs(p);
-  int64_t j = p.v0 + threadIdx.x;
+  const int tid = row_tid<kThreads>();
+  int64_t j = p.v0 + tid;
   for (int seg = 0; seg < segs.count; ++seg) {
     float cur = -INFINITY;
     for (; j < segs.end(p, seg); j += kThreads) {
@@ -292,12 +308,11 @@ __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, f
       cur = fmaxf(cur, st.m);
       all = merge<kEnt>(all, st, s2);
     }
-    if (seg_max) seg_max[seg * kThreads + threadIdx.x] = cur;
+    if (seg_max) seg_max[seg * kThreads + tid] = cur;
   }
-  if ((int)threadIdx.x < p.head + p.tail) {
-    const int i = threadIdx.x;
+  if (tid < p.head + p.tail) {
     st = Stat{-INFINITY, 0.f, 0.f};
-    one(Storage<T>::load1(row + (i < p.head ? i : p.t0 + i - p.head)));
+    one(Storage<T>::load1(row + (tid < p.head ? tid : p.t0 + tid - p.head)));
     all = merge<kEnt>(all, st, s2);
   }
   return all;
@@ -318,7 +333,8 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   Fast<T, kEnt> f;
   f.init(low, s2);
   const uint32_t low_word = Words<T>::floor_word(low);
-  int64_t j = p.v0 + threadIdx.x;
+  const int tid = row_tid<kThreads>();
+  int64_t j = p.v0 + tid;
   auto run = [&](int64_t end) {
     for (; j + (in_flight<kThreads>() - 1) * kThreads < end; j += in_flight<kThreads>() * kThreads) {
       uint4 v[in_flight<kThreads>()];
@@ -341,14 +357,13 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
     for (int seg = 0; seg < segs.count; ++seg) {
       f.cur = low;
       run(segs.end(p, seg));
-      seg_max[seg * kThreads + threadIdx.x] = f.cur > low ? f.cur : -INFINITY;
+      seg_max[seg * kThreads + tid] = f.cur > low ? f.cur : -INFINITY;
     }
   } else {
     run(p.v1);
   }
-  if ((int)threadIdx.x < p.head + p.tail) {
-    const int i = threadIdx.x;
-    f.take1(Storage<T>::load1(row + (i < p.head ? i : p.t0 + i - p.head)), low, s2);
+  if (tid < p.head + p.tail) {
+    f.take1(Storage<T>::load1(row + (tid < p.head ? tid : p.t0 + tid - p.head)), low, s2);
   }
   return f.stat(s2);
 }
@@ -366,12 +381,13 @@ __device__ __forceinline__ Stat cta_stat(Stat st, float s2, Stat* sm) {
     st = merge<kEnt>(st, other, s2);
   }
   constexpr int kWarps = kThreads / 32;
-  if (kWarps == 1) return st;
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = st;
-  __syncthreads();
-  const int lane = threadIdx.x % 32;
-  st = lane < kWarps ? sm[lane] : Stat{-INFINITY, 0.f, 0.f};
+  if (kWarps > 1) {
+    row_sync<kThreads>();
+    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = st;
+    row_sync<kThreads>();
+    const int lane = threadIdx.x % 32;
+    st = lane < kWarps ? sm[lane] : Stat{-INFINITY, 0.f, 0.f};
+  }
 #pragma unroll
   for (int o = kWarps / 2; o > 0; o >>= 1) {
     Stat other;
@@ -380,6 +396,7 @@ __device__ __forceinline__ Stat cta_stat(Stat st, float s2, Stat* sm) {
     other.D = kEnt ? __shfl_xor_sync(0xFFFFFFFFu, st.D, o) : 0.f;
     st = merge<kEnt>(st, other, s2);
   }
+  // (the lanes' roundings may differ: a row has one value)
   st.m = __shfl_sync(0xFFFFFFFFu, st.m, 0);
   st.Z = __shfl_sync(0xFFFFFFFFu, st.Z, 0);
   st.D = __shfl_sync(0xFFFFFFFFu, st.D, 0);
@@ -424,14 +441,14 @@ struct TopSmem {
 // distinct).  Called by the whole CTA; ends with a barrier.
 template <int kThreads, int kVec>
 __device__ void rank_keys(TopSmem<kThreads, kVec>& sm, int n, int k) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = row_tid<kThreads>(); i < n; i += kThreads) {
     const unsigned long long mine = sm.key[i];
     int above = 0;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) above += sm.key[j] > mine;
     if (above < k) sm.best[above] = mine;
   }
-  __syncthreads();
+  row_sync<kThreads>();
 }
 
 template <typename T, int kThreads>
@@ -439,7 +456,7 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
                                  TopSmem<kThreads, Storage<T>::kVec>& sm) {
   constexpr int VEC = Storage<T>::kVec;
   using Smem = TopSmem<kThreads, VEC>;
-  const int tid = threadIdx.x;
+  const int tid = row_tid<kThreads>();
   const Segments<kThreads> segs(p);
   unsigned mine = 0u;  // an empty slice is below every logit
   if (p.v0 + tid < p.v1)
@@ -447,7 +464,7 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
       mine = max(mine, order_of(sm.seg_max[i * kThreads + tid]));
   sm.ord[tid] = mine;
   if (tid == 0) sm.n = sm.nsel = 0;
-  __syncthreads();
+  row_sync<kThreads>();
   if (tid < 32) {
     // tau: the largest bound, of 16 leading bits, that the maxima of k out of
     // at most 64 groups of slices reach (a lower bound than the slices' own
@@ -477,7 +494,7 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
     }
     if (tid == 0) sm.tau = t;
   }
-  __syncthreads();
+  row_sync<kThreads>();
   const unsigned tau = sm.tau;
   if (mine >= tau && mine != 0u)
     for (int i = 0; i < segs.count; ++i)
@@ -494,7 +511,7 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
   // row ends outside the vectors (fewer than kVec on either side)
   if (tid < p.head) push(Storage<T>::load1(row + tid), tid);
   if (tid < p.tail) push(Storage<T>::load1(row + p.t0 + tid), p.t0 + tid);
-  __syncthreads();
+  row_sync<kThreads>();
   const unsigned nsel = (unsigned)sm.nsel, total = nsel * (unsigned)segs.rounds;
   // keeps the k best keys so far, which raises the bound; at least k are held
   auto compact = [&](int n) {
@@ -502,7 +519,7 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
     if (tid < k) sm.key[tid] = sm.best[tid];
     if (tid == 0) sm.n = k;
     bound = sm.best[k - 1] + 1;  // the k-th itself is held
-    __syncthreads();
+    row_sync<kThreads>();
   };
   for (unsigned q0 = 0; q0 < total; q0 += Smem::kBatch * kThreads) {
     uint4 v[Smem::kBatch];
@@ -536,17 +553,17 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
           ++to;
         }
     };
-    __syncthreads();  // every thread has read sm.n
+    row_sync<kThreads>();  // every thread has read sm.n
 #pragma unroll
     for (int u = 0; u < Smem::kBatch; ++u)
       if (at[u] < nvec) push_vec(v[u], at[u]);
-    __syncthreads();
+    row_sync<kThreads>();
     const int n = sm.n;
     if (n > Smem::kCap) {
       // ties: again, in steps that fit, from the keys that were held before
-      __syncthreads();
+      row_sync<kThreads>();
       if (tid == 0) sm.n = held;
-      __syncthreads();
+      row_sync<kThreads>();
       constexpr int kStep = (Smem::kCap - Smem::kCompactAt) / VEC;  // threads a step
 #pragma unroll 1
       for (int u = 0; u < Smem::kBatch; ++u)
@@ -556,16 +573,16 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
             const unsigned i = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
             if (i < nvec) push_vec(__ldg(vec + p.v0 + i), i);
           }
-          __syncthreads();
+          row_sync<kThreads>();
           const int m = sm.n;
-          __syncthreads();
+          row_sync<kThreads>();
           if (m > Smem::kCompactAt) compact(m);
         }
     } else if (n > Smem::kCompactAt) {
       compact(n);
     }
   }
-  __syncthreads();
+  row_sync<kThreads>();
   rank_keys(sm, sm.n, k);
 }
 
@@ -608,11 +625,11 @@ __device__ __forceinline__ void put_top(const TokenArgs& a, int64_t r, int i,
 }
 
 // Whether row r has a distribution; if not, its alternatives are marked so.
-__device__ __forceinline__ bool has_top(const TokenArgs& a, int64_t r, const Stat& st) {
+__device__ __forceinline__ bool has_top(const TokenArgs& a, int64_t r, int tid, const Stat& st) {
   if (st.Z <= 3.4e38f) return true;  // not NaN, not +inf
-  if ((int)threadIdx.x < a.k) {
-    a.top_ids[r * a.k + threadIdx.x] = -1;
-    a.top_logps[r * a.k + threadIdx.x] = NAN;
+  if (tid < a.k) {
+    a.top_ids[r * a.k + tid] = -1;
+    a.top_logps[r * a.k + tid] = NAN;
   }
   return false;
 }
@@ -636,19 +653,22 @@ struct Parts {
 // of bulk copies -- measured 387 us and 322 us on the first two when they took
 // 368 and 265: its three CTAs an SM hide a row's end worse.)
 template <typename T, int kThreads, bool kEnt, bool kTop, bool kSplit>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<kThreads, kSplit>())
+__global__ void __launch_bounds__(kThreads* rows_per_cta<kThreads>(),
+                                  ctas_per_sm<kThreads, kSplit>())
 token_logps_kernel(const TokenArgs a) {
-  constexpr int VEC = Storage<T>::kVec;
+  constexpr int VEC = Storage<T>::kVec, kRows = rows_per_cta<kThreads>();
   __shared__ Stat warp_stat[kThreads / 32];
-  __shared__ typename std::conditional<kTop, TopSmem<kThreads, VEC>, int>::type top;
+  __shared__ typename std::conditional<kTop, TopSmem<kThreads, VEC>, int>::type tops[kRows];
   __shared__ typename std::conditional<kSplit, Parts, int>::type parts;
-  const int tid = threadIdx.x;
+  const int tid = row_tid<kThreads>(), mine = kRows == 1 ? 0 : (int)threadIdx.x / 32;
+  auto& top = tops[mine];
   unsigned rank = 0, ctas = 1;
   if constexpr (kSplit) {
     rank = cg::this_cluster().block_rank();
     ctas = cg::this_cluster().num_blocks();
   }
-  const int64_t r = blockIdx.x / ctas;
+  const int64_t r = kRows == 1 ? blockIdx.x / ctas : (int64_t)blockIdx.x * kRows + mine;
+  if (kRows > 1 && r >= a.B * a.T) return;
   if (a.mask && !a.mask[r]) {  // the whole cluster
     if (rank == 0) masked_row<kEnt, kTop>(a, r, tid);
     return;
@@ -708,7 +728,7 @@ token_logps_kernel(const TokenArgs a) {
   if (st.m == -INFINITY) st.Z = NAN;  // no finite logit: no distribution
   if (tid == 0) finish_row<kEnt>(a, r, xa, st);
   if constexpr (kTop) {
-    if (!has_top(a, r, st)) return;
+    if (!has_top(a, r, tid, st)) return;
     if constexpr (kSplit) {
       // a key's place: how many keys of each part lie above it, by bisection
       // of the parts' ordered lists, all parts at once
@@ -737,12 +757,20 @@ token_logps_kernel(const TokenArgs a) {
   }
 }
 
-// Rows of at most kWarpRowBytes go to one warp, rows from kLongRowBytes on (and
-// few rows) to 256 threads, those between to 128: more and smaller CTAs hide the ends of
-// short rows better, and on long rows too few CTAs are left at the end (us at
-// 128 / 256 threads: 64 KB rows, ragged 64 x 1024, 337 / 371; 8192 of them with
-// 8 alternatives 109 / 136; 304 KB rows, 2048, 117 / 107).
-static constexpr int64_t kWarpRowBytes = 4096, kLongRowBytes = 128 * 1024;
+// Which threads a row gets.  A warp: up to kWarpRowBytes, and up to
+// kManyWarpRowBytes where there are kManyRows of them (20,000 rows of 8000
+// bf16 logits, us by a warp / 128 threads: 60 / 62, with 8 alternatives 99 /
+// 115, the gradient, against 256 threads, 107 / 121; 1,000 rows: 7.1 / 5.0, 12.3
+// / 9.0, 9.3 / 6.5).  128 threads below kLongRowBytes, 256 from there on and for
+// few rows: more and smaller CTAs hide the ends of short rows better, and on
+// long rows too few CTAs are left at the end (128 / 256 threads: ragged 64 x
+// 1024 rows of 64 KB 337 / 371, 8,192 of them with 8 alternatives 109 / 136;
+// 2,048 rows of 304 KB 117 / 107).
+static constexpr int64_t kWarpRowBytes = 4096, kManyWarpRowBytes = 24 * 1024, kManyRows = 2000;
+static constexpr int64_t kLongRowBytes = 128 * 1024;
+static bool to_warps(int64_t bytes, int64_t rows) {
+  return bytes <= (rows >= kManyRows ? kManyWarpRowBytes : kWarpRowBytes);
+}
 // A cluster's CTA gets at least this much of a row (40 rows of 64 KB: 4 parts
 // 3.7 us, 8 parts 4.6 us; 152 rows: 2 parts 4.3, 4 parts 6.8).
 static constexpr int64_t kPartBytes = 16384;
@@ -755,8 +783,9 @@ static cudaError_t launch_logps_t(const TokenArgs& a, unsigned ctas, cudaStream_
               : (a.entropy ? token_logps_kernel<T, kThreads, true, false, kSplit>
                            : token_logps_kernel<T, kThreads, false, false, kSplit>);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.B * a.T) * ctas);
-  cfg.blockDim = dim3(kThreads);
+  constexpr int kRows = rows_per_cta<kThreads>();
+  cfg.gridDim = dim3((unsigned)((a.B * a.T + kRows - 1) / kRows) * ctas);
+  cfg.blockDim = dim3(kThreads * kRows);
   cfg.stream = s;
   cudaLaunchAttribute attr;
   if (kSplit) {
@@ -783,7 +812,7 @@ template <typename T>
 static cudaError_t launch_logps_d(TokenArgs a, cudaStream_t s) {
   a.low = floor_of<T>(a.s2);
   const int64_t bytes = a.V * (int64_t)sizeof(T), rows = a.B * a.T;
-  if (bytes <= kWarpRowBytes) return launch_logps_t<T, 32, false>(a, 1, s);
+  if (to_warps(bytes, rows)) return launch_logps_t<T, 32, false>(a, 1, s);
   // few rows: a cluster for each, while its CTAs are at most two an SM (four
   // for two halves of a long row)
   unsigned ctas = 1;
@@ -832,7 +861,6 @@ __device__ __forceinline__ float2 token_grad2(float2 x, const GradRow& q, float 
   return mul2(e, fma2(u, make_float2(q.c1, q.c1), make_float2(q.c0, q.c0)));
 }
 
-static constexpr int kGradThreads = 256;
 // A CTA takes steps of kGradVecs 16-byte vectors a thread along one row, its
 // loads of a step in flight together.  Plain loads, not the read-only path:
 // in place, the row is written by this kernel.
@@ -842,9 +870,9 @@ __device__ __forceinline__ float load_plain(const float* p) { return *p; }
 __device__ __forceinline__ float load_plain(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_plain(const __half* p) { return __half2float(*p); }
 
-// One step: this thread's vectors j0, j0 + kGradThreads, ...; kWhole: all of
+// One step: this thread's vectors j0, j0 + kThreads, ...; kWhole: all of
 // them inside the row.
-template <typename T, bool kEnt, bool kFused, bool kWhole>
+template <typename T, int kThreads, bool kEnt, bool kFused, bool kWhole>
 __device__ __forceinline__ void grad_step(const T* in, T* out, int64_t j0, int64_t nvec,
                                           int64_t act, const GradRow& q, float s2,
                                           bool together) {
@@ -852,7 +880,7 @@ __device__ __forceinline__ void grad_step(const T* in, T* out, int64_t j0, int64
   uint4 v[kGradVecs];
 #pragma unroll
   for (int k = 0; k < kGradVecs; ++k) {
-    const int64_t j = j0 + k * kGradThreads;
+    const int64_t j = j0 + k * kThreads;
     if (!kWhole && j >= nvec) continue;
     if (together) {
       v[k] = *(reinterpret_cast<const uint4*>(in) + j);
@@ -865,7 +893,7 @@ __device__ __forceinline__ void grad_step(const T* in, T* out, int64_t j0, int64
   }
 #pragma unroll
   for (int k = 0; k < kGradVecs; ++k) {
-    const int64_t j = j0 + k * kGradThreads;
+    const int64_t j = j0 + k * kThreads;
     if (!kWhole && j >= nvec) continue;
     float x[VEC];
     if (kEnt && kFused) {
@@ -889,16 +917,16 @@ __device__ __forceinline__ void grad_step(const T* in, T* out, int64_t j0, int64
   }
 }
 
-template <typename T, bool kEnt, bool kFused>
+template <typename T, int kThreads, bool kEnt, bool kFused>
 __device__ __forceinline__ void grad_steps(const T* in, T* out, int64_t step0, int64_t steps,
                                            int64_t nvec, int64_t act, const GradRow& q, float s2,
                                            bool together) {
   for (int64_t i = step0; i < steps; ++i) {
-    const int64_t j0 = i * (kGradVecs * kGradThreads) + threadIdx.x;
-    if (j0 - threadIdx.x + kGradVecs * kGradThreads <= nvec)
-      grad_step<T, kEnt, kFused, true>(in, out, j0, nvec, act, q, s2, together);
+    const int64_t j0 = i * (kGradVecs * kThreads) + row_tid<kThreads>();
+    if ((i + 1) * (kGradVecs * kThreads) <= nvec)
+      grad_step<T, kThreads, kEnt, kFused, true>(in, out, j0, nvec, act, q, s2, together);
     else
-      grad_step<T, kEnt, kFused, false>(in, out, j0, nvec, act, q, s2, together);
+      grad_step<T, kThreads, kEnt, kFused, false>(in, out, j0, nvec, act, q, s2, together);
   }
 }
 
@@ -907,13 +935,18 @@ __device__ __forceinline__ void grad_steps(const T* in, T* out, int64_t step0, i
 // (18,404 active) with an entropy term 490 us, 6.85 TB/s; 16 x 256 rows of
 // 128256 fp32 435 us, 6.9 TB/s: the rate of a copy.  Four steps a CTA against
 // one: 182 and 213 us on 8,192 rows of 32768; more CTAs an SM with fewer
-// registers (6 x 4 vectors, 8 x 2) 234 and 202 us.
-template <typename T, bool kEnt>
-__global__ void __launch_bounds__(kGradThreads)
+// registers (6 x 4 vectors, 8 x 2) 234 and 202 us.  Short rows go to warps (see
+// to_warps).
+template <typename T, int kThreads, bool kEnt>
+__global__ void __launch_bounds__(kThreads* rows_per_cta<kThreads>(), 4)
 token_grad_kernel(const TokenGradArgs a, unsigned ctas, unsigned per) {
-  const int tid = threadIdx.x;
-  const int64_t r = blockIdx.x / ctas, rows = a.B * a.T;
-  const unsigned cta = blockIdx.x % ctas;
+  constexpr int kRows = rows_per_cta<kThreads>();
+  const int tid = row_tid<kThreads>();
+  const int64_t rows = a.B * a.T;
+  const int64_t r = kRows == 1 ? blockIdx.x / ctas
+                               : (int64_t)blockIdx.x * kRows + threadIdx.x / 32;
+  const unsigned cta = kRows == 1 ? blockIdx.x % ctas : 0;
+  if (kRows > 1 && r >= rows) return;
   // the row's scalars, all asked for at once
   const bool on = !a.mask || a.mask[r];
   float w = a.dlogp ? a.dlogp[r] : 0.f;
@@ -928,7 +961,7 @@ token_grad_kernel(const TokenGradArgs a, unsigned ctas, unsigned per) {
   const Geom<T> g(grow, a.V);  // by the gradient's alignment: the stores are whole
   uint4* out = reinterpret_cast<uint4*>(grow + g.head);
   const int64_t steps = min((int64_t)(cta + 1) * per,
-                            (g.nvec + kGradVecs * kGradThreads - 1) / (kGradVecs * kGradThreads));
+                            (g.nvec + kGradVecs * kThreads - 1) / (kGradVecs * kThreads));
   const int ev = tid < g.head ? tid : (int)g.t0 + tid - g.head;  // this thread's end element
   const bool edge = cta == 0 && tid < g.head + g.tail;
   if (!on || (w == 0.f && h == 0.f)) {
@@ -936,7 +969,7 @@ token_grad_kernel(const TokenGradArgs a, unsigned ctas, unsigned per) {
     for (int64_t i = (int64_t)cta * per; i < steps; ++i)
 #pragma unroll
       for (int k = 0; k < kGradVecs; ++k) {
-        const int64_t j = (i * kGradVecs + k) * kGradThreads + tid;
+        const int64_t j = (i * kGradVecs + k) * kThreads + tid;
         if (j < g.nvec) out[j] = make_uint4(0u, 0u, 0u, 0u);
       }
     return;
@@ -973,36 +1006,41 @@ token_grad_kernel(const TokenGradArgs a, unsigned ctas, unsigned per) {
   T* o = grow + g.head;
   act -= g.head;  // among the vectors' elements
   if (q.fused)
-    grad_steps<T, kEnt, true>(in, o, (int64_t)cta * per, steps, g.nvec, act, q, a.s2, together);
+    grad_steps<T, kThreads, kEnt, true>(in, o, (int64_t)cta * per, steps, g.nvec, act, q, a.s2, together);
   else
-    grad_steps<T, kEnt, false>(in, o, (int64_t)cta * per, steps, g.nvec, act, q, a.s2, together);
+    grad_steps<T, kThreads, kEnt, false>(in, o, (int64_t)cta * per, steps, g.nvec, act, q, a.s2, together);
 }
 
-template <typename T>
-static cudaError_t launch_grad_t(TokenGradArgs a, cudaStream_t s) {
-  a.low = floor_of<T>(a.s2);
-  const int64_t step = (int64_t)kGradThreads * kGradVecs * Storage<T>::kVec;
+template <typename T, int kThreads>
+static cudaError_t launch_grad_t(const TokenGradArgs& a, cudaStream_t s) {
+  const int64_t step = (int64_t)kThreads * kGradVecs * Storage<T>::kVec;
   const int64_t steps = (a.V + step - 1) / step, rows = a.B * a.T;
-  // steps a CTA: up to 4, one where the rows alone are too few to fill the
-  // GPU several times over, and enough to keep the grid below 2^31 CTAs
-  int64_t per = 1;
+  constexpr int kRows = rows_per_cta<kThreads>();
+  // steps a CTA: all of a warp's row; up to 4, one where the rows alone are too
+  // few to fill the GPU several times over, and enough to keep the grid below
+  // 2^31 CTAs
+  int64_t per = kRows > 1 ? steps : 1;
   while (per < 4 && per < steps && rows * ((steps + 2 * per - 1) / (2 * per)) >= 152 * 32) per *= 2;
   while (rows * ((steps + per - 1) / per) > 0x7FFFFFFF) per *= 2;
   const int64_t ctas = (steps + per - 1) / per;
-  if (a.dent)
-    token_grad_kernel<T, true><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(
-        a, (unsigned)ctas, (unsigned)per);
-  else
-    token_grad_kernel<T, false><<<(unsigned)(rows * ctas), kGradThreads, 0, s>>>(
-        a, (unsigned)ctas, (unsigned)per);
+  const unsigned grid = (unsigned)(kRows > 1 ? (rows + kRows - 1) / kRows : rows * ctas);
+  auto fn = a.dent ? token_grad_kernel<T, kThreads, true> : token_grad_kernel<T, kThreads, false>;
+  fn<<<grid, kThreads * kRows, 0, s>>>(a, (unsigned)ctas, (unsigned)per);
   return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t launch_grad_d(TokenGradArgs a, cudaStream_t s) {
+  a.low = floor_of<T>(a.s2);
+  const int64_t bytes = a.V * (int64_t)sizeof(T);
+  return to_warps(bytes, a.B * a.T) ? launch_grad_t<T, 32>(a, s) : launch_grad_t<T, 256>(a, s);
 }
 
 cudaError_t launch_token_grad(const TokenGradArgs& a, grpo_dtype_t dt, cudaStream_t s) {
   switch (dt) {
-    case GRPO_F32: return launch_grad_t<float>(a, s);
-    case GRPO_BF16: return launch_grad_t<__nv_bfloat16>(a, s);
-    default: return launch_grad_t<__half>(a, s);
+    case GRPO_F32: return launch_grad_d<float>(a, s);
+    case GRPO_BF16: return launch_grad_d<__nv_bfloat16>(a, s);
+    default: return launch_grad_d<__half>(a, s);
   }
 }
 

@@ -441,3 +441,23 @@ def test_null_stream():
     got = g.grpo_token_logps(x, ids, mask, top_k=2, want_entropy=True, want_stats=True, stream=0)
     torch.cuda.synchronize()
     assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("B,T,V,k", [(1, 2003, 5003, 9), (67, 61, 2500, 4), (3000, 1, 1025, 32),
+                                     (1, 20001, 64, 3)])
+def test_many_short_rows(dtype, B, T, V, k):
+    """Rows that share a CTA, in a number that does not fill the last one."""
+    x, ids, mask = make(B, T, V, dtype, seed=B + T)
+    got = scores(x, ids, mask, k)
+    check_forward(got, forward(x, ids, mask, 1.0, k), x)
+    w = torch.randn((B, T), device="cuda")
+    h = torch.randn((B, T), device="cuda")
+    w[:, ::3] = 0.0
+    for dl, dh in ((w, None), (w, h)):
+        d = g.grpo_token_logps_grad(x, ids, mask, got["stats"], grad_logps=dl, grad_entropy=dh,
+                                    entropy=got["entropy"] if dh is not None else None)
+        check_gradient(d, *gradient(x, ids, mask, dl, dh), x)
+    y = x.clone()
+    assert torch.equal(g.grpo_token_logps_grad(y, ids, mask, got["stats"], grad_logps=w, grad=y),
+                       g.grpo_token_logps_grad(x, ids, mask, got["stats"], grad_logps=w))
