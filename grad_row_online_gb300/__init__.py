@@ -13,7 +13,6 @@ raises; there is no fallback.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import os
 from typing import Optional
@@ -39,7 +38,6 @@ GRPO_FLAG_OVERLAP_LAUNCH = 16  # grpo_loss_from_logps: dispatch while the previo
 GRPO_FLAG_TEST_STALLED_COPY = 0x80000000  # test hook (see include/grpo.h)
 GRPO_FLAG_TEST_STALLED_BARRIER = 0x40000000  # test hook (see include/grpo.h)
 GRPO_MAX_TOP_K = 32  # grpo_token_logps: most alternatives of a token
-GRPO_CLIP_NORM_ONLY = 1  # grpo_clip_grad_norm: read only
 GRPO_ERR_ACTION_RANGE = 16  # device-detected status bits (grpo_read_device_status)
 GRPO_ERR_CSR = 32
 GRPO_ERR_NONFINITE_REWARD = 64
@@ -611,80 +609,33 @@ def status_buffer(device="cuda") -> torch.Tensor:
     return torch.zeros(256, dtype=torch.uint8, device=device)
 
 
-def _rows(x, name: str):
-    """(B, T, V, stride_b, stride_t) of logits [B, T, V] or [N, V] whose rows
-    hold adjacent elements; any strides between rows."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
-        raise ValueError(f"unsupported {name} dtype {getattr(x, 'dtype', None)}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    shape, stride = x.shape, x.stride()
-    if len(shape) == 3:
-        B, T, V = shape
-        sb, st, sv = stride
-    elif len(shape) == 2:
-        (B, V), T, st = shape, 1, 0
-        sb, sv = stride
-    else:
-        raise ValueError(f"{name} must be [B, T, V] or [N, V]")
-    if sv != 1 and V > 1:
-        raise ValueError(f"the logits of a row of {name} must be adjacent (stride 1)")
-    return B, T, V, sb, st
+_calls = None
 
 
-def _token(t, name: str, lead, dtype, device):
-    """The pointer of a contiguous per-token tensor of shape ``lead`` (None
-    for None)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != lead or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(lead)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+def native():
+    """The native calls (_native.so; raises if it was not built)."""
+    global _calls
+    if _calls is None:
+        if not os.path.exists(_build.NATIVE):
+            raise RuntimeError(f"{_build.NATIVE} is missing: build it with __graft_entry__.build()")
+        from . import _native
+        _calls = _native
+    return _calls
 
 
-def _token_mask(mask, lead, device):
-    if mask is None:
-        return None
-    if mask.dtype != torch.bool and mask.dtype != torch.uint8:
-        raise ValueError("completion_mask must be bool or uint8")
-    return _token(mask, "completion_mask", lead, mask.dtype, device)
-
-
-def _status_ptr(status, device):
-    if status is None:
-        return None
-    if status.device != device or not status.is_contiguous() or status.nbytes < 256:
-        raise ValueError("status must be a status_buffer() on the device of the logits")
-    return status.data_ptr()
-
-
-def _stream_on(stream, device) -> int:
-    """The raw handle of the stream, or of the device's current one (by
-    PyTorch's own short cut: making a Stream object costs 3 us)."""
+def _native_call(what: str, call, stream, args):
+    """A native call on ``stream`` (None: the current one); its outputs come
+    from that stream's memory pool, so they are not reused under it."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return _stream(stream)
-
-
-class _AllocateOn:
-    """Outputs of a call on another stream than the current one belong to
-    that stream: memory is taken from its pool, not reused under it."""
-
-    def __init__(self, stream):
-        self.ctx = None
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
-            self.ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        r = call(*args)
+    else:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream))
+        with torch.cuda.stream(stream):
+            r = call(*args)
+    if type(r) is int:
+        raise GrpoError(r, what)
+    return r
 
 
 def grpo_token_logps(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
@@ -704,26 +655,9 @@ def grpo_token_logps(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
     first).  ``status``: a ``status_buffer()`` that collects
     GRPO_ERR_ACTION_RANGE.  See include/grpo.h for rows without a
     distribution."""
-    B, T, V, sb, st = _rows(logits, "logits")
-    lead, dev = logits.shape[:-1], logits.device
-    ids = _token(action_ids, "action_ids", lead, torch.int64, dev)
-    mask = _token_mask(completion_mask, lead, dev)
-    with _AllocateOn(stream):
-        empty = torch.empty
-        logps = None if ids is None else empty(lead, dtype=torch.float32, device=dev)
-        entropy = empty(lead, dtype=torch.float32, device=dev) if want_entropy else None
-        stats = empty((2, *lead), dtype=torch.float32, device=dev) if want_stats else None
-        top_ids = top_logps = None
-        if top_k:
-            top_ids = empty((*lead, top_k), dtype=torch.int64, device=dev)
-            top_logps = empty((*lead, top_k), dtype=torch.float32, device=dev)
-    rc = lib().grpo_token_logps(logits.data_ptr(), _DTYPES[logits.dtype], B, T, V, sb, st, ids,
-                                mask, temperature, top_k, _ptr(logps), _ptr(entropy), _ptr(stats),
-                                _ptr(top_ids), _ptr(top_logps), _status_ptr(status, dev),
-                                _stream_on(stream, dev))
-    _check(rc, "grpo_token_logps")
-    return {"logps": logps, "entropy": entropy, "stats": stats, "top_ids": top_ids,
-            "top_logps": top_logps}
+    return _native_call("grpo_token_logps", (_calls or native()).token_logps, stream,
+                        (logits, action_ids, completion_mask, temperature, top_k, want_entropy,
+                         want_stats, status))
 
 
 def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
@@ -739,45 +673,13 @@ def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tenso
     forward's at the same temperature.  ``grad``: a tensor to write into (any
     row strides; ``logits`` itself for an in-place gradient), else a new
     contiguous one of the logits' dtype."""
-    B, T, V, sb, st = _rows(logits, "logits")
-    lead, dev = logits.shape[:-1], logits.device
-    ids = _token(action_ids, "action_ids", lead, torch.int64, dev)
-    mask = _token_mask(completion_mask, lead, dev)
-    f32 = torch.float32
-    stats_p = _token(stats, "stats", torch.Size((2, *lead)), f32, dev)
-    ent = _token(entropy, "entropy", lead, f32, dev)
-    dlogp = _token(grad_logps, "grad_logps", lead, f32, dev)
-    dent = _token(grad_entropy, "grad_entropy", lead, f32, dev)
-    if grad is None:
-        with _AllocateOn(stream):
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    elif grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != dev:
-        raise ValueError("grad must have the shape, dtype and device of logits")
-    _, _, _, gsb, gst = _rows(grad, "grad")
-    rc = lib().grpo_token_logps_grad(logits.data_ptr(), _DTYPES[logits.dtype], B, T, V, sb, st,
-                                     ids, mask, stats_p, ent, dlogp, dent, temperature,
-                                     grad.data_ptr(), gsb, gst,
-                                     GRPO_SKIP_MASKED_GRAD_ROWS if skip_masked_grad_rows else 0,
-                                     _status_ptr(status, dev), _stream_on(stream, dev))
-    _check(rc, "grpo_token_logps_grad")
-    return grad
+    return _native_call("grpo_token_logps_grad", (_calls or native()).token_logps_grad, stream,
+                        (logits, action_ids, completion_mask, stats, grad_logps, entropy,
+                         grad_entropy, temperature, grad, skip_masked_grad_rows, status))
 
 
 def grpo_clip_workspace_size(num_tensors: int) -> int:
     return int(lib().grpo_clip_workspace_size(num_tensors))
-
-
-def _dense(t: torch.Tensor) -> bool:
-    """Whether t's elements fill one range of memory without gaps (any order:
-    contiguous, transposed, channels-last)."""
-    if t.is_contiguous():
-        return True
-    want = 1
-    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
-        if stride != want:
-            return False
-        want *= size
-    return True
 
 
 def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: float = 1.0,
@@ -790,60 +692,12 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
     ``max_norm=math.inf`` applies the scale only.  Returns 0-d device tensors
     ``norm`` and ``factor``; when the norm is not finite the factor is NaN and
     nothing is written."""
-    tensors = list(tensors)
-    n = len(tensors)
-    dev = tensors[0].device if n else torch.device("cuda", torch.cuda.current_device())
-    if dev.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    at = dev.index
-    try:
-        dtypes = [_DTYPES[t.dtype] for t in tensors]
-    except KeyError as e:
-        raise ValueError(f"unsupported gradient dtype {e.args[0]}") from None
-    ptrs = [t.data_ptr() for t in tensors]
-    numels = [t.numel() for t in tensors]
-    if [t.get_device() for t in tensors] != [at] * n:
-        raise ValueError("every tensor must be on one device")
-    plain = all([t.is_contiguous() for t in tensors])
-    if not plain and not all([_dense(t) for t in tensors]):
-        raise ValueError("tensors must be dense (no gaps between elements)")
-    if len(set(ptrs)) < n and len({p for p, k in zip(ptrs, numels) if k}) < sum(map(bool, numels)):
-        raise ValueError("a tensor is given twice")
-    out_ptrs = None
-    if out is not None:
+    if type(tensors) is not list:
+        tensors = list(tensors)
+    if out is not None and type(out) is not list:
         out = list(out)
-        if norm_only:
-            raise ValueError("norm_only writes nothing: out must be None")
-        if len(out) != n or [o.get_device() for o in out] != [at] * n or \
-                [_DTYPES.get(o.dtype) for o in out] != dtypes or [o.numel() for o in out] != numels:
-            raise ValueError("out must hold a tensor of the same size and dtype, on the same "
-                             "device, for each of tensors")
-        # element i of the memory of one belongs to element i of the other
-        if not (plain and all([o.is_contiguous() for o in out])) and \
-                not all([o.shape == t.shape and o.stride() == t.stride()
-                         for o, t in zip(out, tensors)]):
-            raise ValueError("out must be contiguous as tensors are, or have their strides")
-        out_ptrs = array.array("Q", [o.data_ptr() for o in out])
-    L = lib()
-    if workspace is not None:
-        _dev(workspace, "workspace")
-        need = 0
-    else:
-        need = L.grpo_clip_workspace_size(n)
-    with _AllocateOn(stream):  # norm, factor and 256 bytes further on the workspace
-        out2 = torch.empty(64 + need // 4 if need else 2, dtype=torch.float32, device=dev)
-    out2_p, size = out2.data_ptr(), need
-    ws = out2_p + 256
-    if workspace is not None:
-        ws, size = workspace.data_ptr(), workspace.nbytes
-    ptrs, numels, dtypes = array.array("Q", ptrs), array.array("q", numels), array.array("i", dtypes)
-    rc = L.grpo_clip_grad_norm(ptrs.buffer_info()[0],
-                               None if out_ptrs is None else out_ptrs.buffer_info()[0],
-                               numels.buffer_info()[0], dtypes.buffer_info()[0], n, max_norm, eps,
-                               scale, GRPO_CLIP_NORM_ONLY if norm_only else 0, out2_p, ws, size,
-                               _stream_on(stream, dev))
-    _check(rc, "grpo_clip_grad_norm")
-    return {"norm": out2[0], "factor": out2[1]}
+    return _native_call("grpo_clip_grad_norm", (_calls or native()).clip_grad_norm, stream,
+                        (tensors, max_norm, eps, scale, out, norm_only, workspace))
 
 
 def grpo_read_device_status(workspace: torch.Tensor, stream=None) -> int:
