@@ -15,26 +15,31 @@
 // the tensor's alignment allows.
 //
 // Bound by memory: the tensors are read once for the norm and, where they are
-// larger than L2, again to be scaled.  291 bf16 tensors of 3.6 GB: norm 506 us
-// (7.0 TB/s), both 1563 us for 10.7 GB (6.8 TB/s, the rate of a copy); 111
-// packed tensors of mixed types, 0.45 GB: 91 and 233 us.  Unclipped in place
-// 517 us: the second kernel returns.  21 small tensors: 11.7 us on the GPU.
+// larger than L2, again to be scaled.  291 bf16 tensors of 3.6 GB: norm 516 us
+// (6.9 TB/s), both 1560 us for 10.7 GB (6.8 TB/s, the rate of a copy); 111
+// packed tensors of mixed types, 0.45 GB: 84 and 225 us.  Unclipped in place
+// 518 us: the second kernel returns.  Small sets cost latency: one tensor of 1000
+// elements 4.5 us, 21 of 7.5 MB in all 10 us.
 #include "grpo_internal.cuh"
 
 namespace grpo {
 
 static constexpr int kClipThreads = 256;
-// CTAs an SM in each kernel, vectors a thread in flight and chunks a piece,
-// chosen on 3.6 GB and 0.45 GB of gradients (us of both kernels): 4 / 6 / 4 /
-// 2 1561 and 235; 4 / 4 / 8 / 8 1584 and 260; 4 / 16 / 4 / 2 1595 and 236;
-// 4 / 32 / 4 / 4 1557 and 249, but 586 instead of 520 when nothing is clipped.
-static constexpr int kNormCtasPerSm = 4;
-static constexpr int kScaleCtasPerSm = 6;
-static constexpr int kClipAhead = 4;
-static constexpr unsigned kPiece = 2;
+// CTAs an SM and vectors a thread in flight in each kernel.  Norm of 3.6 GB,
+// us: 4 CTAs x 8 vectors 508, 5 x 8 498 (but 89 instead of 84 on 0.45 GB), 4 x 4
+// 559, 6 x 4 511, 8 x 4 622.  Scaling: 6 CTAs x 4, chosen with pieces of two
+// chunks on both sets; 32 CTAs an SM cost 70 us where nothing is clipped.
+static constexpr int kNormCtasPerSm = 4, kNormAhead = 8;
+static constexpr int kScaleCtasPerSm = 6, kScaleAhead = 4;
 static constexpr int kClipMaxGrid = 2048;
-// elements of a chunk: 64 a thread, which one fp32 sum of squares covers
-static constexpr int64_t kClipChunk = 64 * kClipThreads;
+// A chunk holds kPer elements a thread, whose squares one fp32 sum covers: 64,
+// or 16 up to kSmallTotal elements, where chunks of 64 leave SMs idle (us at 16
+// / 64: one tensor of 100,000 5.7 / 10.4, 200 of them 41 / 52, 400 80 / 91;
+// 113 M elements 242 / 230).
+static constexpr int64_t kSmallTotal = 64 << 20;
+static constexpr unsigned kPiece = 2;  // chunks a CTA takes at a time
+template <int kPer>
+__host__ __device__ constexpr int64_t clip_chunk() { return (int64_t)kPer * kClipThreads; }
 
 struct ClipEntry {
   const void* in;
@@ -86,7 +91,7 @@ __device__ __forceinline__ void each_chunk(const ClipTable<kCap>& t, unsigned p,
   }
 }
 
-template <typename T>
+template <typename T, int kPer>
 struct ClipChunk {
   const T* in;
   T* out;
@@ -96,8 +101,8 @@ struct ClipChunk {
     // first and last are whole vectors
     const int64_t skew = ((uintptr_t)e.in & 15) / sizeof(T);
     const int64_t size = (int64_t)(e.n & ((1ull << 62) - 1));
-    const int64_t end = (int64_t)(c - e.chunk0 + 1) * kClipChunk - skew;
-    const int64_t at = c == e.chunk0 ? 0 : end - kClipChunk;
+    const int64_t end = (int64_t)(c - e.chunk0 + 1) * clip_chunk<kPer>() - skew;
+    const int64_t at = c == e.chunk0 ? 0 : end - clip_chunk<kPer>();
     in = (const T*)e.in + at;
     out = (T*)e.out + at;
     n = (int)((size < end ? size : end) - at);
@@ -122,14 +127,24 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   return v;
 }
 
+// A thread's sum of squares: a float pair (fp32 operations: double ones run at
+// a 64th of their rate on this GPU) and, for what lies outside its range, a
+// double.
+struct ClipSum {
+  float hi = 0.f, lo = 0.f;
+  double wide = 0.0;
+  int used = 0;  // whether wide holds anything
+};
+
 // This thread's part of a chunk's sum of squares.  The fp32 sum is taken
 // where it lies well inside the range (or the elements are all zero); a sum
 // that overflowed, or so small that squares were lost below the range, is
 // formed again in double.
-template <typename T>
-__device__ double chunk_squares(const ClipChunk<T>& k) {
+template <typename T, int kPer>
+__device__ __forceinline__ void add_squares(const ClipChunk<T, kPer>& k, ClipSum& sum) {
   constexpr int VEC = Storage<T>::kVec;
-  constexpr int kVecs = (int)(kClipChunk / kClipThreads) / VEC;  // vectors a thread at most
+  constexpr int kVecs = kPer / VEC;  // vectors a thread at most
+  constexpr int kAhead = kNormAhead < kVecs ? kNormAhead : kVecs;
   const int tid = threadIdx.x;
   const uint4* vec = reinterpret_cast<const uint4*>(k.in + k.head);
   float s = 0.f;
@@ -151,28 +166,33 @@ __device__ double chunk_squares(const ClipChunk<T>& k) {
   // the loads of kClipAhead vectors in flight together
   if (k.nvec == kVecs * kClipThreads) {
 #pragma unroll
-    for (int i = 0; i < kVecs; i += kClipAhead) {
-      uint4 v[kClipAhead];
+    for (int i = 0; i < kVecs; i += kAhead) {
+      uint4 v[kAhead];
 #pragma unroll
-      for (int u = 0; u < kClipAhead; ++u) v[u] = ld_stream(vec + tid + (i + u) * kClipThreads);
+      for (int u = 0; u < kAhead; ++u) v[u] = ld_stream(vec + tid + (i + u) * kClipThreads);
 #pragma unroll
-      for (int u = 0; u < kClipAhead; ++u) take(v[u]);
+      for (int u = 0; u < kAhead; ++u) take(v[u]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kVecs; i += kClipAhead) {
-      uint4 v[kClipAhead];
+    for (int i = 0; i < kVecs; i += kAhead) {
+      uint4 v[kAhead];
 #pragma unroll
-      for (int u = 0; u < kClipAhead; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         const int j = tid + (i + u) * kClipThreads;
         v[u] = j < k.nvec ? ld_stream(vec + j) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
-      for (int u = 0; u < kClipAhead; ++u) take(v[u]);
+      for (int u = 0; u < kAhead; ++u) take(v[u]);
     }
   }
-  if (s > 0x1p-100f && s < 0x1p126f) return (double)s;
-  if (any == 0u) return 0.0;
+  if (s > 0x1p-100f && s < 0x1p100f) {
+    const FF t = two_sum(sum.hi, s);
+    sum.hi = t.hi;
+    sum.lo = __fadd_rn(sum.lo, t.lo);
+    return;
+  }
+  if (any == 0u) return;
   double d = 0.0;
   if (edge) {
     const double x = clip_load(k.in + ev);
@@ -183,38 +203,58 @@ __device__ double chunk_squares(const ClipChunk<T>& k) {
       const double x = clip_load(k.in + k.head + j * VEC + e);
       d += x * x;
     }
-  return d;
+  sum.wide += d;
+  sum.used = 1;
 }
 
-// Sum over the CTA in a fixed order; the result in every thread.
-__device__ __forceinline__ double cta_sum(double v, double* sm) {
-  v = warp_sum(v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = v;
-  __syncthreads();
-  double t = sm[0];
+struct ClipSmem {
+  FF pair[kClipThreads / 32];
+  double wide[kClipThreads / 32];
+  float factor;
+};
+
+// The CTA's sum in a fixed order, in thread 0.
+__device__ __forceinline__ double cta_squares(const ClipSum& v, ClipSmem& sm) {
+  constexpr int kWarps = kClipThreads / 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const FF w = warp_sum_ff2(FF{v.hi, v.lo});
+  if (lane == 0) sm.pair[warp] = w;
+  const bool wide = __syncthreads_or(v.used);
+  if (wide) {  // rare
+    const double d = warp_sum(v.wide);
+    if (lane == 0) sm.wide[warp] = d;
+    __syncthreads();
+  }
+  double t = 0.0;
+  if (threadIdx.x == 0) {
+    FF f = sm.pair[0];
 #pragma unroll
-  for (int i = 1; i < kClipThreads / 32; ++i) t += sm[i];
+    for (int i = 1; i < kWarps; ++i) f = ff_add(f, sm.pair[i]);
+    t = (double)f.hi + (double)f.lo;
+    if (wide)
+      for (int i = 0; i < kWarps; ++i) t += sm.wide[i];
+  }
   return t;
 }
 
-template <int kCap>
+template <int kCap, int kPer>
 __global__ void __launch_bounds__(kClipThreads)
 clip_norm_kernel(const __grid_constant__ ClipTable<kCap> t, double* partials) {
-  __shared__ double sm[kClipThreads / 32];
-  double sum = 0.0;
+  __shared__ ClipSmem sm;
+  // the scaling CTAs may take their places beside these, and wait
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  ClipSum sum;
   const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
   for (unsigned p = blockIdx.x; p < pieces; p += gridDim.x)
     each_chunk(t, p, [&](const ClipEntry& e, unsigned c) {
       switch (e.n >> 62) {
-        case GRPO_F32: sum += chunk_squares(ClipChunk<float>(e, c)); break;
-        case GRPO_BF16: sum += chunk_squares(ClipChunk<__nv_bfloat16>(e, c)); break;
-        default: sum += chunk_squares(ClipChunk<__half>(e, c)); break;
+        case GRPO_F32: add_squares(ClipChunk<float, kPer>(e, c), sum); break;
+        case GRPO_BF16: add_squares(ClipChunk<__nv_bfloat16, kPer>(e, c), sum); break;
+        default: add_squares(ClipChunk<__half, kPer>(e, c), sum); break;
       }
     });
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  sum = cta_sum(sum, sm);
-  if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+  const double total = cta_squares(sum, sm);
+  if (threadIdx.x == 0) partials[blockIdx.x] = total;
 }
 
 struct ClipScale {
@@ -226,26 +266,37 @@ struct ClipScale {
   int in_place;  // no tensor has an output of its own
 };
 
-// norm and c from the partial sums, the same in every thread of every CTA.
-__device__ __forceinline__ float clip_factor(const ClipScale& k, double* sm) {
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < k.count; i += kClipThreads) sum += k.partials[i];
-  const double norm = k.scale * sqrt(cta_sum(sum, sm));
-  double c = 1.0;
-  if (!(k.max_norm >= norm + k.eps)) c = k.max_norm / (norm + k.eps);
-  float f = (float)(c * k.scale);
-  if (!(norm < INFINITY)) f = NAN;  // NaN too
-  if (k.first && blockIdx.x == 0 && threadIdx.x == 0) {
-    k.out2[0] = (float)norm;
-    k.out2[1] = f;
+// norm and c from the partial sums, the same in every CTA; by one warp of it,
+// because the double operations of eight would take microseconds.
+__device__ __forceinline__ float clip_factor(const ClipScale& k, ClipSmem& sm) {
+  const int lane = threadIdx.x;
+  if (lane < 32) {
+    double sum = 0.0;
+#pragma unroll 8
+    for (int i = lane; i < k.count; i += 32) sum += k.partials[i];
+    sum = warp_sum(sum);
+    const double norm = k.scale * sqrt(sum);
+    double c = 1.0;
+    if (!(k.max_norm >= norm + k.eps)) c = k.max_norm / (norm + k.eps);
+    float f = (float)(c * k.scale);
+    if (!(norm < INFINITY)) f = NAN;  // NaN too
+    if (lane == 0) {
+      sm.factor = f;
+      if (k.first && blockIdx.x == 0) {
+        k.out2[0] = (float)norm;
+        k.out2[1] = f;
+      }
+    }
   }
-  return f;
+  __syncthreads();
+  return sm.factor;
 }
 
-template <typename T>
-__device__ __forceinline__ void scale_chunk(const ClipChunk<T>& k, float f) {
+template <typename T, int kPer>
+__device__ __forceinline__ void scale_chunk(const ClipChunk<T, kPer>& k, float f) {
   constexpr int VEC = Storage<T>::kVec;
-  constexpr int kVecs = (int)(kClipChunk / kClipThreads) / VEC;
+  constexpr int kVecs = kPer / VEC;
+  constexpr int kAhead = kScaleAhead < kVecs ? kScaleAhead : kVecs;
   const int tid = threadIdx.x;
   if (f == 1.f && k.in == k.out) return;
   if (tid < k.head + (k.n - k.t0)) {
@@ -269,25 +320,25 @@ __device__ __forceinline__ void scale_chunk(const ClipChunk<T>& k, float f) {
     }
   };
 #pragma unroll
-  for (int i = 0; i < kVecs; i += kClipAhead) {
-    uint4 v[kClipAhead];
+  for (int i = 0; i < kVecs; i += kAhead) {
+    uint4 v[kAhead];
 #pragma unroll
-    for (int u = 0; u < kClipAhead; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       const int j = tid + (i + u) * kClipThreads;
       if (j < k.nvec) v[u] = ld_stream(vec + j);
     }
 #pragma unroll
-    for (int u = 0; u < kClipAhead; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       const int j = tid + (i + u) * kClipThreads;
       if (j < k.nvec) put(j, v[u]);
     }
   }
 }
 
-template <int kCap>
+template <int kCap, int kPer>
 __global__ void __launch_bounds__(kClipThreads)
 clip_scale_kernel(const __grid_constant__ ClipTable<kCap> t, const ClipScale k) {
-  __shared__ double sm[kClipThreads / 32];
+  __shared__ ClipSmem sm;
   // launched while the norm's last CTAs run; their sums are complete from here
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float f = clip_factor(k, sm);
@@ -297,9 +348,9 @@ clip_scale_kernel(const __grid_constant__ ClipTable<kCap> t, const ClipScale k) 
   for (unsigned q = blockIdx.x; q < pieces; q += gridDim.x)
     each_chunk(t, pieces - 1 - q, [&](const ClipEntry& e, unsigned c) {
       switch (e.n >> 62) {
-        case GRPO_F32: scale_chunk(ClipChunk<float>(e, c), f); break;
-        case GRPO_BF16: scale_chunk(ClipChunk<__nv_bfloat16>(e, c), f); break;
-        default: scale_chunk(ClipChunk<__half>(e, c), f); break;
+        case GRPO_F32: scale_chunk(ClipChunk<float, kPer>(e, c), f); break;
+        case GRPO_BF16: scale_chunk(ClipChunk<__nv_bfloat16, kPer>(e, c), f); break;
+        default: scale_chunk(ClipChunk<__half, kPer>(e, c), f); break;
       }
     });
 }
@@ -311,7 +362,7 @@ size_t clip_partials(int64_t num_tensors) {
 }
 
 // Fills a table from tensor *i on; returns its chunks and moves *i past it.
-template <int kCap>
+template <int kCap, int kPer>
 static void fill_table(const ClipArgs& a, int64_t* i, ClipTable<kCap>* t) {
   t->count = 0;
   t->chunks = 0;
@@ -324,11 +375,11 @@ static void fill_table(const ClipArgs& a, int64_t* i, ClipTable<kCap>* t) {
     e.n = (unsigned long long)n | (unsigned long long)a.dtypes[*i] << 62;
     e.chunk0 = t->chunks;
     const int64_t skew = ((uintptr_t)e.in & 15) / (a.dtypes[*i] == GRPO_F32 ? 4 : 2);
-    t->chunks += (unsigned)((n + skew + kClipChunk - 1) / kClipChunk);
+    t->chunks += (unsigned)((n + skew + clip_chunk<kPer>() - 1) / clip_chunk<kPer>());
   }
 }
 
-template <int kCap>
+template <int kCap, int kPer>
 static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
   const unsigned most = (unsigned)min(sms * kNormCtasPerSm, kClipMaxGrid);
   const unsigned most_scale = (unsigned)(sms * kScaleCtasPerSm);
@@ -336,10 +387,10 @@ static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
   ClipScale k{a.partials, 0, a.max_norm, a.eps, a.scale, a.out2, 1, a.outs == nullptr};
   int64_t i = 0;
   do {
-    fill_table(a, &i, &t);
+    fill_table<kCap, kPer>(a, &i, &t);
     const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
     const unsigned grid = max(1u, min(pieces, most));
-    clip_norm_kernel<kCap><<<grid, kClipThreads, 0, s>>>(t, a.partials + k.count);
+    clip_norm_kernel<kCap, kPer><<<grid, kClipThreads, 0, s>>>(t, a.partials + k.count);
     k.count += (int)grid;
   } while (i < a.count);
   i = 0;
@@ -349,7 +400,7 @@ static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
       t.chunks = 0;
       i = a.count;
     } else {
-      fill_table(a, &i, &t);
+      fill_table<kCap, kPer>(a, &i, &t);
     }
     const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
     const unsigned grid = max(1u, min(pieces, most_scale));
@@ -364,7 +415,7 @@ static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = k.first ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel<kCap>, t, k);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, clip_scale_kernel<kCap, kPer>, t, k);
     if (e != cudaSuccess) return e;
     k.first = 0;
   } while (i < a.count);
@@ -376,8 +427,12 @@ cudaError_t launch_clip(const ClipArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return a.count <= kClipFew ? launch_clip_t<kClipFew>(a, sms, s)
-                             : launch_clip_t<kClipMany>(a, sms, s);
+  int64_t total = 0;
+  for (int64_t i = 0; i < a.count; ++i) total += a.numels[i];
+  const bool few = a.count <= kClipFew;
+  if (total <= kSmallTotal)
+    return few ? launch_clip_t<kClipFew, 16>(a, sms, s) : launch_clip_t<kClipMany, 16>(a, sms, s);
+  return few ? launch_clip_t<kClipFew, 64>(a, sms, s) : launch_clip_t<kClipMany, 64>(a, sms, s);
 }
 
 }  // namespace grpo

@@ -482,9 +482,10 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
  *   out2     : device [2] f32: norm and c.
  * In place with c == 1, nothing is written.  When the norm is not finite, c
  * is NaN and no output is written, in place or not: the caller skips the
- * step.  The squares are summed in fp32 over 64 elements and in fp64 beyond
- * (a thread whose fp32 sum overflows or underflows repeats it in fp64), in an
- * order that depends on the sizes alone.
+ * step.  The squares are summed in fp32 over at most 64 elements, then in
+ * pairs of fp32 numbers and over the CTAs in fp64 (a thread whose fp32 sum
+ * overflows or underflows repeats it in fp64), in an order that depends on the
+ * sizes and addresses alone.
  * ws: grpo_clip_workspace_size(num_tensors) bytes, 256-byte aligned, needs no
  * initialisation. */
 #define GRPO_CLIP_NORM_ONLY 1u
