@@ -368,9 +368,10 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   return f.stat(s2);
 }
 
-// The CTA's Stat from its threads', the same in every thread.  Ends with a
-// barrier.
-template <int kThreads, bool kEnt>
+// The row's Stat from its threads', the same in every thread.  What threads
+// wrote to shared memory before is visible after it.  kAgain: sm was used
+// before.
+template <int kThreads, bool kEnt, bool kAgain>
 __device__ __forceinline__ Stat cta_stat(Stat st, float s2, Stat* sm) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -382,11 +383,13 @@ __device__ __forceinline__ Stat cta_stat(Stat st, float s2, Stat* sm) {
   }
   constexpr int kWarps = kThreads / 32;
   if (kWarps > 1) {
-    row_sync<kThreads>();
+    if (kAgain) row_sync<kThreads>();
     if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = st;
     row_sync<kThreads>();
     const int lane = threadIdx.x % 32;
     st = lane < kWarps ? sm[lane] : Stat{-INFINITY, 0.f, 0.f};
+  } else {
+    row_sync<kThreads>();
   }
 #pragma unroll
   for (int o = kWarps / 2; o > 0; o >>= 1) {
@@ -437,25 +440,25 @@ struct TopSmem {
   unsigned tau;
 };
 
-// The k largest of sm.key[0 .. n) into best[0 .. k), largest first (keys are
-// distinct).  Called by the whole CTA; ends with a barrier.
-template <int kThreads, int kVec>
-__device__ void rank_keys(TopSmem<kThreads, kVec>& sm, int n, int k) {
+// put(place, key) for the k largest of sm.key[0 .. n), place 0 the largest
+// (keys are distinct), each by some thread of the row.
+template <int kThreads, int kVec, typename F>
+__device__ __forceinline__ void rank_keys(const TopSmem<kThreads, kVec>& sm, int n, int k, F put) {
   for (int i = row_tid<kThreads>(); i < n; i += kThreads) {
     const unsigned long long mine = sm.key[i];
     int above = 0;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) above += sm.key[j] > mine;
-    if (above < k) sm.best[above] = mine;
+    if (above < k) put(above, mine);
   }
-  row_sync<kThreads>();
 }
 
+// What the alternatives start from, by every thread after its sweep: its
+// slice's maximum, and the keys of the row's ends, which lie in no slice (fewer
+// than kVec on either side: they are ranked whatever their size).
 template <typename T, int kThreads>
-__device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, int head, int k,
-                                 TopSmem<kThreads, Storage<T>::kVec>& sm) {
-  constexpr int VEC = Storage<T>::kVec;
-  using Smem = TopSmem<kThreads, VEC>;
+__device__ __forceinline__ void top_begin(const T* row, const Part& p,
+                                          TopSmem<kThreads, Storage<T>::kVec>& sm) {
   const int tid = row_tid<kThreads>();
   const Segments<kThreads> segs(p);
   unsigned mine = 0u;  // an empty slice is below every logit
@@ -463,8 +466,26 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
     for (int i = 0; i < segs.count; ++i)
       mine = max(mine, order_of(sm.seg_max[i * kThreads + tid]));
   sm.ord[tid] = mine;
-  if (tid == 0) sm.n = sm.nsel = 0;
-  row_sync<kThreads>();
+  if (tid < p.head + p.tail) {
+    const int64_t v = tid < p.head ? tid : p.t0 + tid - p.head;
+    sm.key[tid] = key_of(Storage<T>::load1(row + v), (unsigned)v);
+  }
+  if (tid == 0) {
+    sm.nsel = 0;
+    sm.n = p.head + p.tail;
+  }
+}
+
+// put(place, key) for the alternatives, after top_begin and a barrier; returns
+// how many there are (k, or all of a short part).
+template <typename T, int kThreads, typename F>
+__device__ int top_alternatives(const uint4* vec, const Part& p, int head, int k,
+                                TopSmem<kThreads, Storage<T>::kVec>& sm, F put) {
+  constexpr int VEC = Storage<T>::kVec;
+  using Smem = TopSmem<kThreads, VEC>;
+  const int tid = row_tid<kThreads>();
+  const Segments<kThreads> segs(p);
+  const unsigned mine = sm.ord[tid];
   if (tid < 32) {
     // tau: the largest bound, of 16 leading bits, that the maxima of k out of
     // at most 64 groups of slices reach (a lower bound than the slices' own
@@ -501,31 +522,24 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
       if (order_of(sm.seg_max[i * kThreads + tid]) >= tau)
         sm.sel[atomicAdd(&sm.nsel, 1)] = (unsigned short)(i * kThreads + tid);
   unsigned long long bound = (unsigned long long)tau << 32;
-  auto push = [&](float x, int64_t v) {
-    const unsigned long long key = key_of(x, (unsigned)v);
-    if (key >= bound) {
-      const int i = atomicAdd(&sm.n, 1);
-      if (i < Smem::kCap) sm.key[i] = key;
-    }
-  };
-  // row ends outside the vectors (fewer than kVec on either side)
-  if (tid < p.head) push(Storage<T>::load1(row + tid), tid);
-  if (tid < p.tail) push(Storage<T>::load1(row + p.t0 + tid), p.t0 + tid);
   row_sync<kThreads>();
   const unsigned nsel = (unsigned)sm.nsel, total = nsel * (unsigned)segs.rounds;
+  const unsigned nvec = (unsigned)(p.v1 - p.v0);
+  int n = p.head + p.tail;  // keys held, the same in every thread
   // keeps the k best keys so far, which raises the bound; at least k are held
-  auto compact = [&](int n) {
-    rank_keys(sm, n, k);
+  auto compact = [&]() {
+    rank_keys(sm, n, k, [&](int i, unsigned long long key) { sm.best[i] = key; });
+    row_sync<kThreads>();
     if (tid < k) sm.key[tid] = sm.best[tid];
     if (tid == 0) sm.n = k;
+    n = k;
     bound = sm.best[k - 1] + 1;  // the k-th itself is held
     row_sync<kThreads>();
   };
   for (unsigned q0 = 0; q0 < total; q0 += Smem::kBatch * kThreads) {
     uint4 v[Smem::kBatch];
     unsigned at[Smem::kBatch];  // vector of the part
-    const unsigned nvec = (unsigned)(p.v1 - p.v0);
-    const int held = sm.n;
+    const int held = n;
 #pragma unroll
     for (int u = 0; u < Smem::kBatch; ++u) {
       const unsigned q = q0 + tid + u * kThreads;
@@ -553,12 +567,12 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
           ++to;
         }
     };
-    row_sync<kThreads>();  // every thread has read sm.n
+    if (q0 > 0) row_sync<kThreads>();  // every thread has read the last batch's sm.n
 #pragma unroll
     for (int u = 0; u < Smem::kBatch; ++u)
       if (at[u] < nvec) push_vec(v[u], at[u]);
     row_sync<kThreads>();
-    const int n = sm.n;
+    n = sm.n;
     if (n > Smem::kCap) {
       // ties: again, in steps that fit, from the keys that were held before
       row_sync<kThreads>();
@@ -574,23 +588,23 @@ __device__ void top_alternatives(const T* row, const uint4* vec, const Part& p, 
             if (i < nvec) push_vec(__ldg(vec + p.v0 + i), i);
           }
           row_sync<kThreads>();
-          const int m = sm.n;
+          n = sm.n;
           row_sync<kThreads>();
-          if (m > Smem::kCompactAt) compact(m);
+          if (n > Smem::kCompactAt) compact();
         }
     } else if (n > Smem::kCompactAt) {
-      compact(n);
+      compact();
     }
   }
-  row_sync<kThreads>();
-  rank_keys(sm, sm.n, k);
+  rank_keys(sm, n, k, put);
+  return min(n, k);
 }
 
 // A row's results, by one thread; xa is its action's logit (NaN for an id out
 // of range).
 template <bool kEnt>
-__device__ __forceinline__ void finish_row(const TokenArgs& a, int64_t r, float xa, Stat w) {
-  const float lnZ = logf(w.Z);
+__device__ __forceinline__ void finish_row(const TokenArgs& a, int64_t r, float xa, Stat w,
+                                           float lnZ) {
   if (a.logps) a.logps[r] = (xa - w.m) * a.inv_t - lnZ;
   if (kEnt) a.entropy[r] = lnZ - kLn2f * (w.D / w.Z);
   if (a.stats) {
@@ -618,10 +632,10 @@ __device__ __forceinline__ void masked_row(const TokenArgs& a, int64_t r, int la
 
 // Alternative i of row r.
 __device__ __forceinline__ void put_top(const TokenArgs& a, int64_t r, int i,
-                                        unsigned long long key, const Stat& st) {
+                                        unsigned long long key, float m, float lnZ) {
   const float x = order_value((unsigned)(key >> 32));
   a.top_ids[r * a.k + i] = (int64_t)(0xFFFFFFFFu - (unsigned)key);
-  a.top_logps[r * a.k + i] = (x - st.m) * a.inv_t - logf(st.Z);
+  a.top_logps[r * a.k + i] = (x - m) * a.inv_t - lnZ;
 }
 
 // Whether row r has a distribution; if not, its alternatives are marked so.
@@ -699,26 +713,30 @@ token_logps_kernel(const TokenArgs a) {
   Stat st;
   bool fast = a.low < 0.f;
   if (fast) {
-    st = cta_stat<kThreads, kEnt>(
-        sweep_fast<T, kThreads, kEnt, kTop>(row, vec, p, a.low, s2, seg_max), s2, warp_stat);
+    st = sweep_fast<T, kThreads, kEnt, kTop>(row, vec, p, a.low, s2, seg_max);
+    if constexpr (kTop) top_begin<T, kThreads>(row, p, top);
+    st = cta_stat<kThreads, kEnt, false>(st, s2, warp_stat);
     fast = fabsf(st.m) * s2 <= kFastRange && st.m > 0.5f * a.low;
   }
-  if (!fast)
-    st = cta_stat<kThreads, kEnt>(sweep_any<T, kThreads, kEnt>(row, vec, p, s2, seg_max), s2,
-                                  warp_stat);
+  if (!fast) {
+    st = sweep_any<T, kThreads, kEnt>(row, vec, p, s2, seg_max);
+    if constexpr (kTop) top_begin<T, kThreads>(row, p, top);
+    st = cta_stat<kThreads, kEnt, true>(st, s2, warp_stat);
+  }
   if constexpr (kSplit) {
-    // every CTA of the cluster runs before its shared memory is written
     cg::cluster_group cluster = cg::this_cluster();
+    int held = 0;
     if constexpr (kTop) {
       // a part may hold fewer than k logits
-      top_alternatives<T, kThreads>(row, vec, p, g.head, a.k, top);
+      held = top_alternatives<T, kThreads>(
+          vec, p, g.head, a.k, top, [&](int i, unsigned long long key) { top.best[i] = key; });
     }
+    // every CTA of the cluster runs before its shared memory is written
     cluster.sync();
     Parts* first = cluster.map_shared_rank(&parts, 0);
     if (tid == 0) first->st[rank] = st;
     if constexpr (kTop) {
-      if (tid < GRPO_MAX_TOP_K)
-        first->key[rank][tid] = tid < min(a.k, top.n) ? top.best[tid] : 0ull;
+      if (tid < GRPO_MAX_TOP_K) first->key[rank][tid] = tid < held ? top.best[tid] : 0ull;
     }
     cluster.sync();
     if (rank != 0) return;
@@ -726,9 +744,11 @@ token_logps_kernel(const TokenArgs a) {
     for (unsigned i = 1; i < ctas; ++i) st = merge<kEnt>(st, parts.st[i], s2);
   }
   if (st.m == -INFINITY) st.Z = NAN;  // no finite logit: no distribution
-  if (tid == 0) finish_row<kEnt>(a, r, xa, st);
+  const float lnZ = logf(st.Z);
+  if (tid == 0) finish_row<kEnt>(a, r, xa, st, lnZ);
   if constexpr (kTop) {
     if (!has_top(a, r, tid, st)) return;
+    auto put = [&](int i, unsigned long long key) { put_top(a, r, i, key, st.m, lnZ); };
     if constexpr (kSplit) {
       // a key's place: how many keys of each part lie above it, by bisection
       // of the parts' ordered lists, all parts at once
@@ -748,11 +768,10 @@ token_logps_kernel(const TokenArgs a) {
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q)
           if (q < (int)ctas) place += above[q] + (parts.key[q][above[q]] > key);
-        if (place < a.k) put_top(a, r, place, key, st);
+        if (place < a.k) put(place, key);
       }
     } else {
-      top_alternatives<T, kThreads>(row, vec, p, g.head, a.k, top);
-      if (tid < a.k) put_top(a, r, tid, top.best[tid], st);
+      top_alternatives<T, kThreads>(vec, p, g.head, a.k, top, put);
     }
   }
 }
