@@ -335,21 +335,18 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   const uint32_t low_word = Words<T>::floor_word(low);
   const int tid = row_tid<kThreads>();
   int64_t j = p.v0 + tid;
+  // one form for whole groups and the last one, which the floor fills up: the
+  // code is fetched cold in every launch
   auto run = [&](int64_t end) {
-    for (; j + (in_flight<kThreads>() - 1) * kThreads < end; j += in_flight<kThreads>() * kThreads) {
-      uint4 v[in_flight<kThreads>()];
+    constexpr int U = in_flight<kThreads>();
+    for (; j < end; j += U * kThreads) {
+      const int left = (int)(end - j);
+      uint4 v[U];
 #pragma unroll
-      for (int u = 0; u < in_flight<kThreads>(); ++u) v[u] = ld_once(vec + j + u * kThreads);
+      for (int u = 0; u < U; ++u)
+        v[u] = u * kThreads < left ? ld_once(vec + j + u * kThreads)
+                                   : make_uint4(low_word, low_word, low_word, low_word);
       f.take(v, low_word, s2);
-    }
-    if (j < end) {  // the rest in one group too, filled up with the floor
-      uint4 v[in_flight<kThreads>()];
-#pragma unroll
-      for (int u = 0; u < in_flight<kThreads>(); ++u)
-        v[u] = j + u * kThreads < end ? ld_once(vec + j + u * kThreads)
-                                      : make_uint4(low_word, low_word, low_word, low_word);
-      f.take(v, low_word, s2);
-      j += in_flight<kThreads>() * kThreads;
     }
   };
   if (kTop) {
@@ -368,42 +365,41 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   return f.stat(s2);
 }
 
+// A tree over kLanes lanes; every lane gets lane 0's result (the lanes'
+// roundings may differ: a row has one value).
+template <bool kEnt, int kLanes>
+__device__ __forceinline__ Stat warp_stat_of(Stat st, float s2) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    Stat other;
+    other.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
+    other.Z = __shfl_xor_sync(0xFFFFFFFFu, st.Z, o);
+    other.D = kEnt ? __shfl_xor_sync(0xFFFFFFFFu, st.D, o) : 0.f;
+    st = merge<kEnt>(st, other, s2);
+  }
+  st.m = __shfl_sync(0xFFFFFFFFu, st.m, 0);
+  st.Z = __shfl_sync(0xFFFFFFFFu, st.Z, 0);
+  st.D = kEnt ? __shfl_sync(0xFFFFFFFFu, st.D, 0) : 0.f;
+  return st;
+}
+
 // The row's Stat from its threads', the same in every thread.  What threads
 // wrote to shared memory before is visible after it.  kAgain: sm was used
 // before.
 template <int kThreads, bool kEnt, bool kAgain>
 __device__ __forceinline__ Stat cta_stat(Stat st, float s2, Stat* sm) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stat other;
-    other.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-    other.Z = __shfl_xor_sync(0xFFFFFFFFu, st.Z, o);
-    other.D = kEnt ? __shfl_xor_sync(0xFFFFFFFFu, st.D, o) : 0.f;
-    st = merge<kEnt>(st, other, s2);
-  }
+  st = warp_stat_of<kEnt, 32>(st, s2);
   constexpr int kWarps = kThreads / 32;
-  if (kWarps > 1) {
-    if (kAgain) row_sync<kThreads>();
-    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = st;
+  if (kWarps == 1) {
     row_sync<kThreads>();
-    const int lane = threadIdx.x % 32;
-    st = lane < kWarps ? sm[lane] : Stat{-INFINITY, 0.f, 0.f};
-  } else {
-    row_sync<kThreads>();
+    return st;
   }
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) {
-    Stat other;
-    other.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-    other.Z = __shfl_xor_sync(0xFFFFFFFFu, st.Z, o);
-    other.D = kEnt ? __shfl_xor_sync(0xFFFFFFFFu, st.D, o) : 0.f;
-    st = merge<kEnt>(st, other, s2);
-  }
-  // (the lanes' roundings may differ: a row has one value)
-  st.m = __shfl_sync(0xFFFFFFFFu, st.m, 0);
-  st.Z = __shfl_sync(0xFFFFFFFFu, st.Z, 0);
-  st.D = __shfl_sync(0xFFFFFFFFu, st.D, 0);
-  return st;
+  if (kAgain) row_sync<kThreads>();
+  if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = st;
+  row_sync<kThreads>();
+  const int lane = threadIdx.x % 32;
+  st = lane < kWarps ? sm[lane] : Stat{-INFINITY, 0.f, 0.f};
+  return warp_stat_of<kEnt, kWarps>(st, s2);
 }
 
 // A logit and its index as one number that orders by value, then by lowest
@@ -489,8 +485,7 @@ __device__ int top_alternatives(const uint4* vec, const Part& p, int head, int k
   if (tid < 32) {
     // tau: the largest bound, of 16 leading bits, that the maxima of k out of
     // at most 64 groups of slices reach (a lower bound than the slices' own
-    // does as well, at the price of a few segments more); two bits a step, the
-    // counts of the three candidates in one word
+    // does as well, at the price of a few segments more); two bits a step
     constexpr int kGroups = kThreads >= 64 ? 2 : 1;  // a lane
     unsigned o[kGroups];
 #pragma unroll
@@ -502,16 +497,14 @@ __device__ int top_alternatives(const uint4* vec, const Part& p, int head, int k
 #pragma unroll 1
     for (int b = 30; b >= 16; b -= 2) {
       const unsigned step = 1u << b;
-      unsigned cnt = 0;
+      int c1 = 0, c2 = 0, c3 = 0;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i)
-        cnt += (o[i] >= t + step ? 1u : 0u) + (o[i] >= t + 2 * step ? 1u << 10 : 0u) +
-               (o[i] >= t + 3 * step ? 1u << 20 : 0u);
-      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-      t += ((cnt >> 20) >= (unsigned)k)              ? 3 * step
-           : (((cnt >> 10) & 1023u) >= (unsigned)k) ? 2 * step
-           : ((cnt & 1023u) >= (unsigned)k)         ? step
-                                                    : 0u;
+      for (int i = 0; i < kGroups; ++i) {
+        c1 += __popc(__ballot_sync(0xFFFFFFFFu, o[i] >= t + step));
+        c2 += __popc(__ballot_sync(0xFFFFFFFFu, o[i] >= t + 2 * step));
+        c3 += __popc(__ballot_sync(0xFFFFFFFFu, o[i] >= t + 3 * step));
+      }
+      t += c3 >= k ? 3 * step : c2 >= k ? 2 * step : c1 >= k ? step : 0u;
     }
     if (tid == 0) sm.tau = t;
   }
@@ -740,8 +733,9 @@ token_logps_kernel(const TokenArgs a) {
     }
     cluster.sync();
     if (rank != 0) return;
-    st = parts.st[0];
-    for (unsigned i = 1; i < ctas; ++i) st = merge<kEnt>(st, parts.st[i], s2);
+    const unsigned lane = tid % 32;
+    st = lane < ctas ? parts.st[lane] : Stat{-INFINITY, 0.f, 0.f};
+    st = warp_stat_of<kEnt, kMaxCluster>(st, s2);
   }
   if (st.m == -INFINITY) st.Z = NAN;  // no finite logit: no distribution
   const float lnZ = logf(st.Z);
