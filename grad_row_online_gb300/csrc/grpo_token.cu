@@ -278,7 +278,7 @@ struct Segments {
 // out uniform.  Out of line: few rows come here.
 template <typename T, int kThreads, bool kEnt>
 __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, float s2,
-                                       float* seg_max) {
+                                       float* seg_max, float* slice_max) {
   constexpr int VEC = Storage<T>::kVec;
   Stat st{-INFINITY, 0.f, 0.f};
   auto one = [&](float x) {
@@ -310,6 +310,7 @@ __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, f
     }
     if (seg_max) seg_max[seg * kThreads + tid] = cur;
   }
+  *slice_max = all.m;
   if (tid < p.head + p.tail) {
     st = Stat{-INFINITY, 0.f, 0.f};
     one(Storage<T>::load1(row + (tid < p.head ? tid : p.t0 + tid - p.head)));
@@ -329,7 +330,7 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
 
 template <typename T, int kThreads, bool kEnt, bool kTop>
 __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const Part& p, float low,
-                                           float s2, float* seg_max) {
+                                           float s2, float* seg_max, float* slice_max) {
   Fast<T, kEnt> f;
   f.init(low, s2);
   const uint32_t low_word = Words<T>::floor_word(low);
@@ -359,6 +360,7 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
   } else {
     run(p.v1);
   }
+  *slice_max = f.m > low ? f.m : -INFINITY;
   if (tid < p.head + p.tail) {
     f.take1(Storage<T>::load1(row + (tid < p.head ? tid : p.t0 + tid - p.head)), low, s2);
   }
@@ -431,6 +433,7 @@ struct TopSmem {
   unsigned long long key[kCap];
   unsigned long long best[GRPO_MAX_TOP_K];
   unsigned ord[kThreads];                   // each slice's maximum
+  uint4 group[16];                          // maxima of 64 (32) groups of slices
   unsigned short sel[kMaxSegs * kThreads];  // segments to read again: seg kThreads + tid
   int nsel, n;
   unsigned tau;
@@ -453,15 +456,11 @@ __device__ __forceinline__ void rank_keys(const TopSmem<kThreads, kVec>& sm, int
 // slice's maximum, and the keys of the row's ends, which lie in no slice (fewer
 // than kVec on either side: they are ranked whatever their size).
 template <typename T, int kThreads>
-__device__ __forceinline__ void top_begin(const T* row, const Part& p,
+__device__ __forceinline__ void top_begin(const T* row, const Part& p, float slice_max,
                                           TopSmem<kThreads, Storage<T>::kVec>& sm) {
   const int tid = row_tid<kThreads>();
-  const Segments<kThreads> segs(p);
-  unsigned mine = 0u;  // an empty slice is below every logit
-  if (p.v0 + tid < p.v1)
-    for (int i = 0; i < segs.count; ++i)
-      mine = max(mine, order_of(sm.seg_max[i * kThreads + tid]));
-  sm.ord[tid] = mine;
+  // an empty slice is below every logit
+  sm.ord[tid] = p.v0 + tid < p.v1 ? order_of(slice_max) : 0u;
   if (tid < p.head + p.tail) {
     const int64_t v = tid < p.head ? tid : p.t0 + tid - p.head;
     sm.key[tid] = key_of(Storage<T>::load1(row + v), (unsigned)v);
@@ -483,41 +482,49 @@ __device__ int top_alternatives(const uint4* vec, const Part& p, int head, int k
   const Segments<kThreads> segs(p);
   const unsigned mine = sm.ord[tid];
   if (tid < 32) {
-    // tau: the largest bound, of 16 leading bits, that the maxima of k out of
-    // at most 64 groups of slices reach (a lower bound than the slices' own
-    // does as well, at the price of a few segments more); two bits a step
+    // tau: the k-th largest maximum of (at most) 64 groups of slices -- a lower
+    // bound than the slices' own, at the price of a few segments more: the
+    // smallest that fewer than k exceed
     constexpr int kGroups = kThreads >= 64 ? 2 : 1;  // a lane
+    unsigned* group = &sm.group[0].x;
     unsigned o[kGroups];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) o[i] = 0u;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i)
       o[i % kGroups] = max(o[i % kGroups], sm.ord[tid + 32 * i]);
-    unsigned t = 0;
-#pragma unroll 1
-    for (int b = 30; b >= 16; b -= 2) {
-      const unsigned step = 1u << b;
-      int c1 = 0, c2 = 0, c3 = 0;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        c1 += __popc(__ballot_sync(0xFFFFFFFFu, o[i] >= t + step));
-        c2 += __popc(__ballot_sync(0xFFFFFFFFu, o[i] >= t + 2 * step));
-        c3 += __popc(__ballot_sync(0xFFFFFFFFu, o[i] >= t + 3 * step));
-      }
-      t += c3 >= k ? 3 * step : c2 >= k ? 2 * step : c1 >= k ? step : 0u;
+    for (int i = 0; i < kGroups; ++i) group[tid + 32 * i] = o[i];
+    __syncwarp();
+    int above[kGroups] = {};
+#pragma unroll
+    for (int j = 0; j < 8 * kGroups; ++j) {
+      const uint4 w = sm.group[j];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        above[i] += (w.x > o[i]) + (w.y > o[i]) + (w.z > o[i]) + (w.w > o[i]);
     }
+    unsigned t = above[0] < k ? o[0] : 0xFFFFFFFFu;
+    if (kGroups == 2) t = min(t, above[kGroups - 1] < k ? o[kGroups - 1] : 0xFFFFFFFFu);
+    t = __reduce_min_sync(0xFFFFFFFFu, t);
     if (tid == 0) sm.tau = t;
   }
   row_sync<kThreads>();
   const unsigned tau = sm.tau;
-  if (mine >= tau && mine != 0u)
-    for (int i = 0; i < segs.count; ++i)
-      if (order_of(sm.seg_max[i * kThreads + tid]) >= tau)
-        sm.sel[atomicAdd(&sm.nsel, 1)] = (unsigned short)(i * kThreads + tid);
+  if (mine >= tau && mine != 0u) {
+    unsigned reach = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxSegs; ++i)
+      if (i < segs.count && order_of(sm.seg_max[i * kThreads + tid]) >= tau) reach |= 1u << i;
+    int to = atomicAdd(&sm.nsel, __popc(reach));
+    for (; reach != 0; reach &= reach - 1)
+      sm.sel[to++] = (unsigned short)((__ffs(reach) - 1) * kThreads + tid);
+  }
   unsigned long long bound = (unsigned long long)tau << 32;
   row_sync<kThreads>();
   const unsigned nsel = (unsigned)sm.nsel, total = nsel * (unsigned)segs.rounds;
   const unsigned nvec = (unsigned)(p.v1 - p.v0);
+  const float per_sel = 1.f / (float)nsel;
   int n = p.head + p.tail;  // keys held, the same in every thread
   // keeps the k best keys so far, which raises the bound; at least k are held
   auto compact = [&]() {
@@ -538,8 +545,13 @@ __device__ int top_alternatives(const uint4* vec, const Part& p, int head, int k
       const unsigned q = q0 + tid + u * kThreads;
       at[u] = nvec;
       if (q < total) {
-        const unsigned seg = sm.sel[q % nsel];
-        at[u] = (seg / kThreads * segs.rounds + q / nsel) * kThreads + seg % kThreads;
+        // q / nsel, off by one at most where q is below 2^22
+        unsigned d = q < 1u << 22 ? (unsigned)((float)q * per_sel) : q / nsel;
+        int rest = (int)(q - d * nsel);
+        if (rest < 0) --d, rest += (int)nsel;
+        if (rest >= (int)nsel) ++d, rest -= (int)nsel;
+        const unsigned seg = sm.sel[rest];
+        at[u] = (seg / kThreads * segs.rounds + d) * kThreads + seg % kThreads;
         if (at[u] < nvec) v[u] = __ldg(vec + p.v0 + at[u]);
       }
     }
@@ -676,11 +688,20 @@ token_logps_kernel(const TokenArgs a) {
   }
   const int64_t r = kRows == 1 ? blockIdx.x / ctas : (int64_t)blockIdx.x * kRows + mine;
   if (kRows > 1 && r >= a.B * a.T) return;
+  // asked for beside the mask; its logit is asked for before the sweep, or in a
+  // cluster, where the wait for the id would delay the sweep, after it
+  const bool scores = tid == 0 && rank == 0 && a.logps;
+  const int64_t act = scores ? a.actions[r] : -1;
   if (a.mask && !a.mask[r]) {  // the whole cluster
     if (rank == 0) masked_row<kEnt, kTop>(a, r, tid);
     return;
   }
-  const unsigned b = (unsigned)r / (unsigned)a.T, t = (unsigned)r % (unsigned)a.T;
+  if constexpr (kSplit) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  unsigned b = (unsigned)r, t = 0;
+  if (a.T > 1) {
+    b = (unsigned)r / (unsigned)a.T;
+    t = (unsigned)r - b * (unsigned)a.T;
+  }
   const T* row = (const T*)a.logits + b * a.sb + t * a.st;
   const Geom<T> g(row, a.V);
   const uint4* vec = reinterpret_cast<const uint4*>(row + g.head);
@@ -691,29 +712,31 @@ token_logps_kernel(const TokenArgs a) {
     p.v1 = min(p.v0 + per, g.nvec);
     if (rank != 0) p.head = p.tail = 0;
   }
-  // the action's logit now, so that the end of the row does not wait for it
-  float xa = NAN;
-  if (tid == 0 && rank == 0 && a.logps) {
-    const int64_t act = a.actions[r];
-    if (act >= 0 && act < a.V)
-      xa = Storage<T>::load1(row + act);
-    else if (a.hdr)
-      atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
-  }
   const float s2 = a.s2;
   float* seg_max = nullptr;
   if constexpr (kTop) seg_max = top.seg_max;
   Stat st;
+  float slice_max, xa = NAN;
+  auto ask = [&]() {
+    if (!scores) return;
+    if (act >= 0 && act < a.V)
+      xa = Storage<T>::load1(row + act);
+    else if (a.hdr)
+      atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
+  };
+  if (!kSplit) ask();
   bool fast = a.low < 0.f;
   if (fast) {
-    st = sweep_fast<T, kThreads, kEnt, kTop>(row, vec, p, a.low, s2, seg_max);
-    if constexpr (kTop) top_begin<T, kThreads>(row, p, top);
+    st = sweep_fast<T, kThreads, kEnt, kTop>(row, vec, p, a.low, s2, seg_max, &slice_max);
+    if (kSplit) ask();
+    if constexpr (kTop) top_begin<T, kThreads>(row, p, slice_max, top);
     st = cta_stat<kThreads, kEnt, false>(st, s2, warp_stat);
     fast = fabsf(st.m) * s2 <= kFastRange && st.m > 0.5f * a.low;
   }
   if (!fast) {
-    st = sweep_any<T, kThreads, kEnt>(row, vec, p, s2, seg_max);
-    if constexpr (kTop) top_begin<T, kThreads>(row, p, top);
+    st = sweep_any<T, kThreads, kEnt>(row, vec, p, s2, seg_max, &slice_max);
+    if (kSplit) ask();
+    if constexpr (kTop) top_begin<T, kThreads>(row, p, slice_max, top);
     st = cta_stat<kThreads, kEnt, true>(st, s2, warp_stat);
   }
   if constexpr (kSplit) {
@@ -723,9 +746,14 @@ token_logps_kernel(const TokenArgs a) {
       // a part may hold fewer than k logits
       held = top_alternatives<T, kThreads>(
           vec, p, g.head, a.k, top, [&](int i, unsigned long long key) { top.best[i] = key; });
+      // parts that are not there hold nothing
+      if (tid / GRPO_MAX_TOP_K >= (int)ctas)
+        parts.key[tid / GRPO_MAX_TOP_K][tid % GRPO_MAX_TOP_K] = 0ull;
+      row_sync<kThreads>();  // best is complete
     }
-    // every CTA of the cluster runs before its shared memory is written
-    cluster.sync();
+    // (arrived at the start) every CTA of the cluster runs before its shared
+    // memory is written
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     Parts* first = cluster.map_shared_rank(&parts, 0);
     if (tid == 0) first->st[rank] = st;
     if constexpr (kTop) {
@@ -748,7 +776,7 @@ token_logps_kernel(const TokenArgs a) {
       // of the parts' ordered lists, all parts at once
       const int part = tid / GRPO_MAX_TOP_K, i = tid % GRPO_MAX_TOP_K;
       static_assert(kThreads >= kMaxCluster * GRPO_MAX_TOP_K, "a thread for each key");
-      const unsigned long long key = part < (int)ctas ? parts.key[part][i] : 0ull;
+      const unsigned long long key = parts.key[part][i];
       if (key != 0ull) {
         int above[kMaxCluster];
 #pragma unroll
@@ -757,11 +785,11 @@ token_logps_kernel(const TokenArgs a) {
         for (int step = GRPO_MAX_TOP_K / 2; step > 0; step /= 2)
 #pragma unroll
           for (int q = 0; q < kMaxCluster; ++q)
-            if (q < (int)ctas && parts.key[q][above[q] + step - 1] > key) above[q] += step;
+            above[q] += parts.key[q][above[q] + step - 1] > key ? step : 0;
         int place = 0;
 #pragma unroll
         for (int q = 0; q < kMaxCluster; ++q)
-          if (q < (int)ctas) place += above[q] + (parts.key[q][above[q]] > key);
+          place += above[q] + (parts.key[q][above[q]] > key);
         if (place < a.k) put(place, key);
       }
     } else {
