@@ -806,15 +806,18 @@ token_logps_kernel(const TokenArgs a) {
 // few rows: more and smaller CTAs hide the ends of short rows better, and on
 // long rows too few CTAs are left at the end (128 / 256 threads: ragged 64 x
 // 1024 rows of 64 KB 337 / 371, 8,192 of them with 8 alternatives 109 / 136;
-// 2,048 rows of 304 KB 117 / 107).
+// 2,000 rows of 80 KB 31.2 / 29.5, of 100 KB 39.7 / 35.1, of 128 KB 49.5 / 45.1).
 static constexpr int64_t kWarpRowBytes = 4096, kManyWarpRowBytes = 24 * 1024, kManyRows = 2000;
-static constexpr int64_t kLongRowBytes = 128 * 1024;
+static constexpr int64_t kLongRowBytes = 72 * 1024;
 static bool to_warps(int64_t bytes, int64_t rows) {
   return bytes <= (rows >= kManyRows ? kManyWarpRowBytes : kWarpRowBytes);
 }
 // A cluster's CTA gets at least this much of a row (40 rows of 64 KB: 4 parts
 // 3.7 us, 8 parts 4.6 us; 152 rows: 2 parts 4.3, 4 parts 6.8).
 static constexpr int64_t kPartBytes = 16384;
+// Rows that are worth halving where they are two an SM (304 rows of 304 KB: 16.4
+// us in halves, 21.0 whole).
+static constexpr int64_t kHalvedRowBytes = 128 * 1024;
 
 template <typename T, int kThreads, bool kSplit>
 static cudaError_t launch_logps_t(const TokenArgs& a, unsigned ctas, cudaStream_t s) {
@@ -859,7 +862,7 @@ static cudaError_t launch_logps_d(TokenArgs a, cudaStream_t s) {
   unsigned ctas = 1;
   while (ctas < kMaxCluster && rows * (2 * ctas) <= 2 * 152 && bytes / (2 * ctas) >= kPartBytes)
     ctas *= 2;
-  if (ctas == 1 && rows <= 2 * 152 && bytes >= kLongRowBytes) ctas = 2;
+  if (ctas == 1 && rows <= 2 * 152 && bytes >= kHalvedRowBytes) ctas = 2;
   if (ctas > 1) return launch_logps_t<T, 256, true>(a, ctas, s);
   return rows > 2 * 152 && bytes < kLongRowBytes ? launch_logps_t<T, 128, false>(a, 1, s)
                                                  : launch_logps_t<T, 256, false>(a, 1, s);
