@@ -15,10 +15,10 @@
 // the tensor's alignment allows.
 //
 // Bound by memory: the tensors are read once for the norm and, where they are
-// larger than L2, again to be scaled.  291 bf16 tensors of 3.6 GB: norm 516 us
-// (6.9 TB/s), both 1560 us for 10.7 GB (6.8 TB/s, the rate of a copy); 111
-// packed tensors of mixed types, 0.45 GB: 84 and 225 us.  Unclipped in place
-// 518 us: the second kernel returns.  Small sets cost latency: one tensor of 1000
+// larger than L2, again to be scaled.  291 bf16 tensors of 3.6 GB: norm 507 us
+// (7.0 TB/s), both 1556 us for 10.7 GB (6.8 TB/s, the rate of a copy); 111
+// packed tensors of mixed types, 0.45 GB: 84 and 228 us.  Unclipped in place
+// 506 us: the second kernel returns.  Small sets cost latency: one tensor of 1000
 // elements 4.5 us, 21 of 7.5 MB in all 10 us.
 #include "grpo_internal.cuh"
 

@@ -664,13 +664,14 @@ struct Parts {
 // contiguous part of the row's vectors: a sweep, a tree over the threads, the
 // part's alternatives, and in a cluster the parts joined by its first CTA.
 // Many independent CTAs an SM keep memory busy over the ends of rows: 36,836 of
-// 65,536 rows of 32768 bf16 logits take 339 us (7.1 TB/s; 38 % of the ALU pipe,
-// 37 % of the exponential unit, 52 % of issue), 4,601 of 8,192 rows of 151936
-// with 8 alternatives 235 us (6.0 TB/s), 4,337 rows of 128256 fp32 304 us (7.3
-// TB/s).  One row of 32768 with 5 alternatives 7.1 us, 64 of 151936 with 20
-// 11.1 us.  (A persistent form -- a producer warp streaming rows through a ring
-// of bulk copies -- measured 387 us and 322 us on the first two when they took
-// 368 and 265: its three CTAs an SM hide a row's end worse.)
+// 65,536 rows of 32768 bf16 logits take 340 us (7.1 TB/s; 44 % of the ALU pipe,
+// 36 % of the exponential unit, 58 % of issue), 4,601 of 8,192 rows of 151936
+// with 8 alternatives 224 us (6.2 TB/s), 4,337 rows of 128256 fp32 303 us (7.3
+// TB/s).  Few rows are a chain of latencies: one of 32768 with 5 alternatives
+// 5.6 us, 64 of 151936 with 20 9.7 us.  (A persistent form -- a producer warp
+// streaming rows through a ring of bulk copies -- measured 387 us and 322 us on
+// the first two when they took 368 and 265: its three CTAs an SM hide a row's
+// end worse.)
 template <typename T, int kThreads, bool kEnt, bool kTop, bool kSplit>
 __global__ void __launch_bounds__(kThreads* rows_per_cta<kThreads>(),
                                   ctas_per_sm<kThreads, kSplit>())
@@ -976,8 +977,8 @@ __device__ __forceinline__ void grad_steps(const T* in, T* out, int64_t step0, i
 
 // CTA c of a row takes its steps [c per, (c + 1) per); the row's unaligned
 // ends go to its first CTA.  Bound by memory: 64 x 512 rows of 32768 bf16 logits
-// (18,404 active) with an entropy term 490 us, 6.85 TB/s; 16 x 256 rows of
-// 128256 fp32 435 us, 6.9 TB/s: the rate of a copy.  Four steps a CTA against
+// (18,404 active) with an entropy term 498 us, 6.7 TB/s; 16 x 256 rows of
+// 128256 fp32 434 us, 6.9 TB/s: the rate of a copy.  Four steps a CTA against
 // one: 182 and 213 us on 8,192 rows of 32768; more CTAs an SM with fewer
 // registers (6 x 4 vectors, 8 x 2) 234 and 202 us.  Short rows go to warps (see
 // to_warps).
