@@ -264,7 +264,8 @@ struct Segments {
   int rounds, count;
   __device__ explicit Segments(const Part& p) {
     const int all = (int)((p.v1 - p.v0 + kThreads - 1) / kThreads);
-    rounds = (all + kMaxSegs * in_flight<kThreads>() - 1) / (kMaxSegs * in_flight<kThreads>()) * in_flight<kThreads>();
+    constexpr int U = in_flight<kThreads>();
+    rounds = (all + kMaxSegs * U - 1) / (kMaxSegs * U) * U;
     count = all > 0 ? (all + rounds - 1) / rounds : 0;
   }
   __device__ int64_t end(const Part& p, int seg) const {
@@ -361,9 +362,8 @@ __device__ __forceinline__ Stat sweep_fast(const T* row, const uint4* vec, const
     run(p.v1);
   }
   *slice_max = f.m > low ? f.m : -INFINITY;
-  if (tid < p.head + p.tail) {
+  if (tid < p.head + p.tail)
     f.take1(Storage<T>::load1(row + (tid < p.head ? tid : p.t0 + tid - p.head)), low, s2);
-  }
   return f.stat(s2);
 }
 

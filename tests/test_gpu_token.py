@@ -358,6 +358,14 @@ def test_python_refusals():
         g.grpo_token_logps_grad(x, ids, mask, f["stats"], grad_logps=w[:1].expand(2, 3))
     with pytest.raises(ValueError):
         g.grpo_token_logps_grad(x, ids, mask, f["stats"], grad_logps=w, grad=x.bfloat16())
+    with pytest.raises(ValueError):
+        g.grpo_token_logps_grad(x, ids, mask, None, grad_logps=w)
+    with pytest.raises(ValueError):
+        g.grpo_token_logps(x, ids, mask, status=torch.zeros(8, device="cuda"))
+    with pytest.raises(TypeError):
+        g.grpo_token_logps(x, ids, mask, temperature="hot")
+    with pytest.raises(g.GrpoError):
+        g.grpo_token_logps(x, ids, mask, top_k=-1)
     with pytest.raises(g.GrpoError):  # rows of the gradient overlap
         g.grpo_token_logps_grad(x, ids, mask, f["stats"], grad_logps=w,
                                 grad=torch.empty((1, 1, 50), device="cuda").expand(2, 3, 50))

@@ -101,10 +101,21 @@ def test_clip_grad_norm_rejects_bad_arguments(lib):  # noqa: F811
     assert lib.grpo_clip_workspace_size(5000) > lib.grpo_clip_workspace_size(5)
 
 
-def test_wrappers_check_before_the_library():
+def test_wrappers_check_before_the_library(lib):  # noqa: F811
     import torch
     x = torch.zeros((2, 3, 10))
+    ids = torch.zeros((2, 3), dtype=torch.int64)
     with pytest.raises(ValueError):  # a host tensor
-        g.grpo_token_logps(x, torch.zeros((2, 3), dtype=torch.int64))
+        g.grpo_token_logps(x, ids)
     with pytest.raises(ValueError):
-        g.grpo_clip_grad_norm([x], 1.0)
+        g.grpo_token_logps_grad(x, ids, None, torch.zeros((2, 2, 3)), grad_logps=x[..., 0])
+    for bad in ([x], [None], ["x"]):
+        with pytest.raises(ValueError):
+            g.grpo_clip_grad_norm(bad, 1.0)
+    for bad in (None, 3, x.double(), x.long(), x[0, 0]):
+        with pytest.raises(ValueError):
+            g.grpo_token_logps(bad, ids)
+    with pytest.raises(TypeError):
+        g.grpo_clip_grad_norm([x], "one")
+    with pytest.raises(TypeError):
+        g.native().token_logps(x)
