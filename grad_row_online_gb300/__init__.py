@@ -690,8 +690,9 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
     max_norm / (norm + eps))``, in place or into ``out`` (tensors of the same
     sizes and dtypes, contiguous or with the same shapes and strides).  ``norm_only`` leaves the tensors alone.
     ``max_norm=math.inf`` applies the scale only.  Returns 0-d device tensors
-    ``norm`` and ``factor``; when the norm is not finite the factor is NaN and
-    nothing is written."""
+    ``norm`` and ``factor``; when the norm is not finite as an f32 number the
+    factor is NaN and nothing is written (with ``norm_only``, a norm that only
+    f32 cannot hold leaves the factor at its value)."""
     if type(tensors) is not list:
         tensors = list(tensors)
     if out is not None and type(out) is not list:

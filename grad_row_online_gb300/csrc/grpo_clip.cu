@@ -264,6 +264,7 @@ struct ClipScale {
   float* out2;
   int first;     // this launch writes out2
   int in_place;  // no tensor has an output of its own
+  int norm_only; // nothing is written
 };
 
 // norm and c from the partial sums, the same in every CTA; by one warp of it,
@@ -279,7 +280,9 @@ __device__ __forceinline__ float clip_factor(const ClipScale& k, ClipSmem& sm) {
     double c = 1.0;
     if (!(k.max_norm >= norm + k.eps)) c = k.max_norm / (norm + k.eps);
     float f = (float)(c * k.scale);
-    if (!(norm < INFINITY)) f = NAN;  // NaN too
+    // (NaN too.)  Finite in fp64 but not as the fp32 number that the caller
+    // sees: nothing may be written, and only a call that writes nothing gets c
+    if (!(norm < INFINITY) || (!k.norm_only && !((float)norm < INFINITY))) f = NAN;
     if (lane == 0) {
       sm.factor = f;
       if (k.first && blockIdx.x == 0) {
@@ -384,7 +387,8 @@ static cudaError_t launch_clip_t(const ClipArgs& a, int sms, cudaStream_t s) {
   const unsigned most = (unsigned)min(sms * kNormCtasPerSm, kClipMaxGrid);
   const unsigned most_scale = (unsigned)(sms * kScaleCtasPerSm);
   ClipTable<kCap> t;
-  ClipScale k{a.partials, 0, a.max_norm, a.eps, a.scale, a.out2, 1, a.outs == nullptr};
+  ClipScale k{a.partials, 0, a.max_norm, a.eps, a.scale, a.out2, 1, a.outs == nullptr,
+              a.norm_only};
   int64_t i = 0;
   do {
     fill_table<kCap, kPer>(a, &i, &t);

@@ -480,9 +480,11 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
  *   eps      : finite, >= 0.     scale : finite, > 0 (1 / loss scale, say).
  *   flags    : GRPO_CLIP_NORM_ONLY: the tensors are only read (outs NULL).
  *   out2     : device [2] f32: norm and c.
- * In place with c == 1, nothing is written.  When the norm is not finite, c
- * is NaN and no output is written, in place or not: the caller skips the
- * step.  The squares are summed in fp32 over at most 64 elements, then in
+ * In place with c == 1, nothing is written.  When the norm is not finite as
+ * the f32 number of out2, c is NaN and no output is written, in place or not:
+ * the caller skips the step.  (With GRPO_CLIP_NORM_ONLY, which writes nothing
+ * in any case, a norm that only f32 cannot hold leaves c at its value.)  The
+ * squares are summed in fp32 over at most 64 elements, then in
  * pairs of fp32 numbers and over the CTAs in fp64 (a thread whose fp32 sum
  * overflows or underflows repeats it in fp64), in an order that depends on the
  * sizes and addresses alone.
