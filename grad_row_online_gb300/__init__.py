@@ -623,14 +623,21 @@ def native():
     return _calls
 
 
-def _native_call(what: str, call, stream, args):
+def _native_call(what: str, call, stream, on, args):
     """A native call on ``stream`` (None: the current one); its outputs come
-    from that stream's memory pool, so they are not reused under it."""
+    from that stream's memory pool, so they are not reused under it.  The call
+    takes the current stream of the device of ``on``, one of its tensors (None:
+    of the current device), so ``stream`` has to be one of that device."""
     if stream is None:
         r = call(*args)
     else:
+        device = getattr(on, "device", None)
+        if device is not None and device.type != "cuda":
+            device = None  # (the call refuses the tensor)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream))
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        elif device is not None and stream.device != device:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             r = call(*args)
     if type(r) is int:
@@ -656,8 +663,8 @@ def grpo_token_logps(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
     GRPO_ERR_ACTION_RANGE.  See include/grpo.h for rows without a
     distribution."""
     return _native_call("grpo_token_logps", (_calls or native()).token_logps, stream,
-                        (logits, action_ids, completion_mask, temperature, top_k, want_entropy,
-                         want_stats, status))
+                        logits, (logits, action_ids, completion_mask, temperature, top_k,
+                                 want_entropy, want_stats, status))
 
 
 def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
@@ -674,8 +681,8 @@ def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tenso
     row strides; ``logits`` itself for an in-place gradient), else a new
     contiguous one of the logits' dtype."""
     return _native_call("grpo_token_logps_grad", (_calls or native()).token_logps_grad, stream,
-                        (logits, action_ids, completion_mask, stats, grad_logps, entropy,
-                         grad_entropy, temperature, grad, skip_masked_grad_rows, status))
+                        logits, (logits, action_ids, completion_mask, stats, grad_logps, entropy,
+                                 grad_entropy, temperature, grad, skip_masked_grad_rows, status))
 
 
 def grpo_clip_workspace_size(num_tensors: int) -> int:
@@ -698,6 +705,7 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
     if out is not None and type(out) is not list:
         out = list(out)
     return _native_call("grpo_clip_grad_norm", (_calls or native()).clip_grad_norm, stream,
+                        tensors[0] if tensors else None,
                         (tensors, max_norm, eps, scale, out, norm_only, workspace))
 
 
