@@ -16,7 +16,7 @@
 #include <math.h>
 #include <string.h>
 
-#include "grpo_internal.cuh"
+#include "grpo_around.cuh"
 
 using namespace grpo;
 

@@ -20,7 +20,7 @@
 // packed tensors of mixed types, 0.45 GB: 84 and 228 us.  Unclipped in place
 // 506 us: the second kernel returns.  Small sets cost latency: one tensor of 1000
 // elements 4.5 us, 21 of 7.5 MB in all 10 us.
-#include "grpo_internal.cuh"
+#include "grpo_around.cuh"
 
 namespace grpo {
 

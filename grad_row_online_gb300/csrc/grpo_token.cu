@@ -21,6 +21,7 @@
 
 #include <type_traits>
 
+#include "grpo_around.cuh"
 #include "grpo_rows_common.cuh"
 
 namespace grpo {
