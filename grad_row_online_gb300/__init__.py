@@ -660,7 +660,8 @@ def grpo_token_logps(logits: torch.Tensor, action_ids: Optional[torch.Tensor],
     grpo_token_logps_grad needs), ``top_ids`` (int64 [..., top_k]; -1 on
     masked tokens) and ``top_logps`` (f32; equal logits by lowest index
     first).  ``status``: a ``status_buffer()`` that collects
-    GRPO_ERR_ACTION_RANGE.  See include/grpo.h for rows without a
+    GRPO_ERR_ACTION_RANGE.  Nothing is recorded for autograd: the gradient is
+    grpo_token_logps_grad's.  See include/grpo.h for rows without a
     distribution."""
     return _native_call("grpo_token_logps", (_calls or native()).token_logps, stream,
                         logits, (logits, action_ids, completion_mask, temperature, top_k,
@@ -679,7 +680,8 @@ def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tenso
     forward's ``entropy``); at least one of the two.  ``stats`` is the
     forward's at the same temperature.  ``grad``: a tensor to write into (any
     row strides; ``logits`` itself for an in-place gradient), else a new
-    contiguous one of the logits' dtype."""
+    contiguous one of the logits' dtype.  Nothing is recorded for autograd, and
+    a tensor written into counts as modified in place."""
     return _native_call("grpo_token_logps_grad", (_calls or native()).token_logps_grad, stream,
                         logits, (logits, action_ids, completion_mask, stats, grad_logps, entropy,
                                  grad_entropy, temperature, grad, skip_masked_grad_rows, status))
@@ -695,7 +697,9 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
     """The global L2 norm of ``scale`` x ``tensors`` (f32, bf16, f16 in any
     mixture; each dense in memory) and the tensors scaled by ``scale x min(1,
     max_norm / (norm + eps))``, in place or into ``out`` (tensors of the same
-    sizes and dtypes, contiguous or with the same shapes and strides).  ``norm_only`` leaves the tensors alone.
+    sizes and dtypes, contiguous or with the same shapes and strides).  Tensors
+    and ``out`` must not overlap one another otherwise; what is written into
+    counts as modified in place.  ``norm_only`` leaves the tensors alone.
     ``max_norm=math.inf`` applies the scale only.  Returns 0-d device tensors
     ``norm`` and ``factor``; when the norm is not finite as an f32 number the
     factor is NaN and nothing is written (with ``norm_only``, a norm that only

@@ -116,6 +116,12 @@ void put(PyObject* dict, const char* name, const at::Tensor& t) {
   if (rc != 0) throw python_error();
 }
 
+// A tensor of the caller's was written through its pointer: autograd has to see
+// that a value it saved is gone.  (Inference tensors count no versions.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -221,6 +227,7 @@ PyObject* token_logps_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              stream);
   Py_END_ALLOW_THREADS
   if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
+  if (a[8] != Py_None) written(grad);
   return THPVariable_Wrap(grad);
   GRPO_CATCH
   END_HANDLE_TH_ERRORS
@@ -242,6 +249,9 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (outs && norm_only) throw Refused("norm_only writes nothing: out must be None");
   if (outs && PyList_GET_SIZE(a[4]) != n)
     throw Refused("out must hold one tensor for each of tensors");
+  // (held: without the GIL, another thread may change the lists)
+  std::vector<at::Tensor> writes;
+  if (!norm_only) writes.reserve(n);
   std::vector<const void*> in(n), seen;
   std::vector<void*> to(outs ? n : 0);
   std::vector<int64_t> numel(n);
@@ -261,7 +271,10 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     in[i] = t.data_ptr();
     numel[i] = t.numel();
     if (numel[i] > 0) seen.push_back(in[i]);
-    if (!outs) continue;
+    if (!outs) {
+      if (!norm_only) writes.push_back(t);
+      continue;
+    }
     const at::Tensor& o = tensor(PyList_GET_ITEM(a[4], i), "an output");
     if (o.device() != dev || o.scalar_type() != t.scalar_type() || o.numel() != t.numel())
       throw Refused("out must hold a tensor of the same size and dtype, on the same device, for "
@@ -271,6 +284,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         !(t.sizes() == o.sizes() && t.strides() == o.strides()))
       throw Refused("out must be contiguous as tensors are, or have their strides");
     to[i] = o.data_ptr();
+    writes.push_back(o);
   }
   std::sort(seen.begin(), seen.end());
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
@@ -303,6 +317,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                            stream);
   Py_END_ALLOW_THREADS
   if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
+  for (const at::Tensor& t : writes) written(t);
   THPObjectPtr out(PyDict_New());
   if (!out) return nullptr;
   put(out, "norm", out2.select(0, 0));
