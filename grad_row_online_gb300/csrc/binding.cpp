@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -291,23 +292,23 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     throw Refused("a tensor is given twice");
   const c10::cuda::CUDAGuard guard(dev);
   const auto f32 = at::TensorOptions().dtype(at::kFloat).device(dev);
-  // the norm, the factor and, 256 bytes further on, the workspace
+  // The workspace goes back to the allocator with this call: the results, which
+  // a caller may keep, are a tensor of two numbers.
   size_t need = 0;
   void* ws = nullptr;
-  at::Tensor given;
+  c10::DataPtr own;
   if (a[6] != Py_None) {
-    given = tensor(a[6], "workspace");
+    const at::Tensor& given = tensor(a[6], "workspace");
     if (given.device() != dev || !given.is_contiguous())
       throw Refused("workspace must be a contiguous tensor on the device of tensors");
     ws = given.data_ptr();
     need = given.nbytes();
+  } else {
+    need = grpo_clip_workspace_size(n);
+    own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+    ws = own.get();
   }
-  const size_t own = given.defined() ? 0 : grpo_clip_workspace_size(n);
-  at::Tensor out2 = at::empty({given.defined() ? 2 : (int64_t)(64 + own / 4)}, f32);
-  if (!given.defined()) {
-    ws = (char*)out2.data_ptr() + 256;
-    need = own;
-  }
+  at::Tensor out2 = at::empty({2}, f32);
   grpo_status_t rc;
   const auto stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
   Py_BEGIN_ALLOW_THREADS
