@@ -704,10 +704,9 @@ def grpo_clip_grad_norm(tensors, max_norm: float, *, eps: float = 1e-6, scale: f
     ``norm`` and ``factor``; when the norm is not finite as an f32 number the
     factor is NaN and nothing is written (with ``norm_only``, a norm that only
     f32 cannot hold leaves the factor at its value)."""
-    if type(tensors) is not list:
-        tensors = list(tensors)
-    if out is not None and type(out) is not list:
-        out = list(out)
+    tensors = tuple(tensors)
+    if out is not None:
+        out = tuple(out)
     return _native_call("grpo_clip_grad_norm", (_calls or native()).clip_grad_norm, stream,
                         tensors[0] if tensors else None,
                         (tensors, max_norm, eps, scale, out, norm_only, workspace))

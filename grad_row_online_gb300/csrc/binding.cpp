@@ -234,25 +234,24 @@ PyObject* token_logps_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// clip_grad_norm(tensors: list, max_norm, eps, scale, out: list or None,
+// clip_grad_norm(tensors: tuple, max_norm, eps, scale, out: tuple or None,
 //                norm_only, workspace) -> dict or status code
+// Tuples hold their tensors while the call runs without the GIL (another thread
+// may change a list); references of its own to each of 291 tensors cost 4 us.
 PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   GRPO_TRY
   if (nargs != 7) return want_args(nargs, 7);
-  if (!PyList_Check(a[0]) || (a[4] != Py_None && !PyList_Check(a[4]))) {
-    PyErr_SetString(PyExc_TypeError, "tensors and out are lists");
+  if (!PyTuple_Check(a[0]) || (a[4] != Py_None && !PyTuple_Check(a[4]))) {
+    PyErr_SetString(PyExc_TypeError, "tensors and out are tuples");
     return nullptr;
   }
-  const int64_t n = PyList_GET_SIZE(a[0]);
+  const int64_t n = PyTuple_GET_SIZE(a[0]);
   const bool outs = a[4] != Py_None, norm_only = PyObject_IsTrue(a[5]);
   const double max_norm = number(a[1]), eps = number(a[2]), scale = number(a[3]);
   if (outs && norm_only) throw Refused("norm_only writes nothing: out must be None");
-  if (outs && PyList_GET_SIZE(a[4]) != n)
+  if (outs && PyTuple_GET_SIZE(a[4]) != n)
     throw Refused("out must hold one tensor for each of tensors");
-  // (held: without the GIL, another thread may change the lists)
-  std::vector<at::Tensor> writes;
-  if (!norm_only) writes.reserve(n);
   std::vector<const void*> in(n), seen;
   std::vector<void*> to(outs ? n : 0);
   std::vector<int64_t> numel(n);
@@ -260,7 +259,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   seen.reserve(n);
   c10::Device dev(at::kCUDA, n > 0 ? (c10::DeviceIndex)0 : c10::cuda::current_device());
   for (int64_t i = 0; i < n; ++i) {
-    const at::Tensor& t = tensor(PyList_GET_ITEM(a[0], i), "a gradient");
+    const at::Tensor& t = tensor(PyTuple_GET_ITEM(a[0], i), "a gradient");
     if (!t.is_cuda()) throw Refused("tensors must be CUDA tensors");
     if (i == 0) dev = t.device();
     if (t.device() != dev) throw Refused("every tensor must be on one device");
@@ -272,11 +271,8 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     in[i] = t.data_ptr();
     numel[i] = t.numel();
     if (numel[i] > 0) seen.push_back(in[i]);
-    if (!outs) {
-      if (!norm_only) writes.push_back(t);
-      continue;
-    }
-    const at::Tensor& o = tensor(PyList_GET_ITEM(a[4], i), "an output");
+    if (!outs) continue;
+    const at::Tensor& o = tensor(PyTuple_GET_ITEM(a[4], i), "an output");
     if (o.device() != dev || o.scalar_type() != t.scalar_type() || o.numel() != t.numel())
       throw Refused("out must hold a tensor of the same size and dtype, on the same device, for "
                     "each of tensors");
@@ -285,7 +281,6 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         !(t.sizes() == o.sizes() && t.strides() == o.strides()))
       throw Refused("out must be contiguous as tensors are, or have their strides");
     to[i] = o.data_ptr();
-    writes.push_back(o);
   }
   std::sort(seen.begin(), seen.end());
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
@@ -318,7 +313,9 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                            stream);
   Py_END_ALLOW_THREADS
   if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
-  for (const at::Tensor& t : writes) written(t);
+  if (!norm_only)
+    for (int64_t i = 0; i < n; ++i)
+      written(THPVariable_Unpack(PyTuple_GET_ITEM(outs ? a[4] : a[0], i)));
   THPObjectPtr out(PyDict_New());
   if (!out) return nullptr;
   put(out, "norm", out2.select(0, 0));
