@@ -13,6 +13,7 @@
 // an int.  No C++ exception leaves a function.
 #include <Python.h>
 
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -303,7 +304,9 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
     ws = own.get();
   }
-  at::Tensor out2 = at::empty({2}, f32);
+  // (a fresh tensor and its two halves: nothing for autograd's dispatch keys)
+  const at::AutoDispatchBelowADInplaceOrView below;
+  const at::Tensor out2 = at::empty({2}, f32);
   grpo_status_t rc;
   const auto stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
   Py_BEGIN_ALLOW_THREADS
