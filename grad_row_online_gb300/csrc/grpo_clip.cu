@@ -27,8 +27,10 @@ namespace grpo {
 static constexpr int kClipThreads = 256;
 // CTAs an SM and vectors a thread in flight in each kernel.  Norm of 3.6 GB,
 // us: 4 CTAs x 8 vectors 508, 5 x 8 498 (but 89 instead of 84 on 0.45 GB), 4 x 4
-// 559, 6 x 4 511, 8 x 4 622.  Scaling: 6 CTAs x 4, chosen with pieces of two
-// chunks on both sets; 32 CTAs an SM cost 70 us where nothing is clipped.
+// 559, 6 x 4 511, 8 x 4 622.  Scaling: a grid of 6 CTAs an SM x 4, chosen with
+// pieces of two chunks on both sets; 32 CTAs an SM cost 70 us where nothing is
+// clipped.  Its registers (71; 51 with the smaller chunks) let 3 (4) of the 6
+// be resident, so the grid runs as two waves, and each forms the norm again.
 static constexpr int kNormCtasPerSm = 4, kNormAhead = 8;
 static constexpr int kScaleCtasPerSm = 6, kScaleAhead = 4;
 static constexpr int kClipMaxGrid = 2048;
@@ -163,7 +165,7 @@ __device__ __forceinline__ void add_squares(const ClipChunk<T, kPer>& k, ClipSum
 #pragma unroll
     for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
   };
-  // the loads of kClipAhead vectors in flight together
+  // the loads of kAhead vectors in flight together
   if (k.nvec == kVecs * kClipThreads) {
 #pragma unroll
     for (int i = 0; i < kVecs; i += kAhead) {
@@ -346,7 +348,8 @@ clip_scale_kernel(const __grid_constant__ ClipTable<kCap> t, const ClipScale k) 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float f = clip_factor(k, sm);
   if (f != f || (f == 1.f && k.in_place)) return;
-  // from the end: what the norm read last is in L2 still
+  // from the end: what the norm read last is in L2 still (the first wave's
+  // pieces: the second one starts from the end again)
   const unsigned pieces = (t.chunks + kPiece - 1) / kPiece;
   for (unsigned q = blockIdx.x; q < pieces; q += gridDim.x)
     each_chunk(t, pieces - 1 - q, [&](const ClipEntry& e, unsigned c) {

@@ -9,14 +9,17 @@
 // rescales both when the maximum moves (from m to m', d = s2 (m - m'):
 // Z' = 2^d Z, D' = 2^d (D + d Z)).
 //
-//   token_logps_kernel  one CTA, or a cluster of CTAs, per row
-//   token_grad_kernel   one CTA per row and up to 64 KB of it
+//   token_logps_kernel  a warp, one CTA, or a cluster of CTAs per row
+//   token_grad_kernel   a warp per row, or one CTA per row and up to 64 KB of it
 //
 // Both are bound by memory: 2 or 4 bytes a logit read once, against about five
 // issued instructions a bf16 logit of the ten that memory speed leaves room
-// for; the gradient also writes as much.  Sums are fp32 (a thread adds 1/128
-// or less of a row, in groups of eight, then a tree), so ln Z is good to a few
-// 1e-7, as log-probs in fp32 are.
+// for; the gradient also writes as much.  Sums are fp32: a thread adds its
+// share of a row (1/32 of rows of up to 24 KB, else 1/128 or 1/256) one 16-byte
+// vector's sum at a time, n of them, then a tree follows, so Z is off by at most
+// n + 20 roundings of 2^-24 beside those of its terms.  n is 74 for 151936 bf16
+// logits, at most 48 for shorter rows, and grows with longer ones (V / 2048,
+// fp32 V / 1024).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -277,7 +280,11 @@ struct Segments {
 
 // The sweep for any values: x - m is formed first, exactly near the maximum
 // and without overflow to +inf, so that rows of the type's lowest value come
-// out uniform.  Out of line: few rows come here.
+// out uniform.  Out of line: at ordinary temperatures few rows come here.  They
+// are those whose maximum passes 2839 temperatures (kFastRange / log2 e), and
+// cost a second, slower sweep: with maxima near 40, 8,192 rows of 32768 bf16
+// logits take 87 us (99 with 8 alternatives) at temperatures of 0.02 and above
+// and 282 us at 0.01.
 template <typename T, int kThreads, bool kEnt>
 __device__ __noinline__ Stat sweep_any(const T* row, const uint4* vec, Part p, float s2,
                                        float* seg_max, float* slice_max) {
@@ -801,14 +808,30 @@ token_logps_kernel(const TokenArgs a) {
 }
 
 // Which threads a row gets.  A warp: up to kWarpRowBytes, and up to
-// kManyWarpRowBytes where there are kManyRows of them (20,000 rows of 8000
-// bf16 logits, us by a warp / 128 threads: 60 / 62, with 8 alternatives 99 /
-// 115, the gradient, against 256 threads, 107 / 121; 1,000 rows: 7.1 / 5.0, 12.3
-// / 9.0, 9.3 / 6.5).  128 threads below kLongRowBytes, 256 from there on and for
-// few rows: more and smaller CTAs hide the ends of short rows better, and on
-// long rows too few CTAs are left at the end (128 / 256 threads: ragged 64 x
-// 1024 rows of 64 KB 337 / 371, 8,192 of them with 8 alternatives 109 / 136;
-// 2,000 rows of 80 KB 31.2 / 29.5, of 100 KB 39.7 / 35.1, of 128 KB 49.5 / 45.1).
+// kManyWarpRowBytes where there are kManyRows of them.  us by a warp / 128
+// threads, for bf16 rows that are not in L2 (alone, with 8 alternatives, and the
+// gradient, whose other side is 256 threads):
+//           1,000 rows                      2,000 rows
+//    8 KB    8.3/6.2  12.4/10.3  8.3/8.3     8.6/9.3  14.3/15.2  10.2/10.6
+//   16 KB   12.0/8.3  16.5/12.3 12.2/8.6    12.5/12.3 18.6/18.4  15.2/12.5
+//   24 KB   14.4/10.2 20.5/12.5 16.5/12.4   16.3/14.5 24.2/21.4  22.7/22.5
+//           5,000 rows                      20,000 rows
+//    8 KB   12.4/14.5 22.6/28.3 18.4/22.3   33.3/45.3 59.8/92.5  56.5/86.2
+//   16 KB   19.6/20.5 30.8/33.4 36.9/32.8   57.7/63.5 91.0/111   107/114
+//   24 KB   26.5/26.7 39.1/38.8 52.8/46.5   81.8/82.7 124/131    157/165
+// (the two constants are a compromise: 8 KB rows cross over below 2,000 of them,
+// 24 KB rows between 5,000 and 20,000.)  128 threads below kLongRowBytes, 256
+// from there on and for few rows: more and smaller CTAs hide the ends of short
+// rows better, and on long rows too few CTAs are left at the end.  us by 128 / 256
+// threads, alone and with 8 alternatives:
+//           2,000 rows            8,192 rows
+//   32 KB   18.3/19.0 24.6/28.7   49.4/59.7 67.5/94.4
+//   64 KB   29.5/30.3 35.4/39.1   86.4/96.2 101/130
+//   72 KB   32.5/30.8 38.8/39.3   96.1/99.3 115/132
+//   80 KB   35.1/32.1 41.2/39.7    106/105  124/134
+//  128 KB   52.5/47.7 57.9/56.1    161/163  179/192
+// (with alternatives and many rows 128 threads stay ahead beyond 72 KB; the rule
+// follows the sweep alone.)
 static constexpr int64_t kWarpRowBytes = 4096, kManyWarpRowBytes = 24 * 1024, kManyRows = 2000;
 static constexpr int64_t kLongRowBytes = 72 * 1024;
 static bool to_warps(int64_t bytes, int64_t rows) {
@@ -820,6 +843,7 @@ static constexpr int64_t kPartBytes = 16384;
 // Rows that are worth halving where they are two an SM (304 rows of 304 KB: 16.4
 // us in halves, 21.0 whole).
 static constexpr int64_t kHalvedRowBytes = 128 * 1024;
+static constexpr int64_t kSms = 152;  // of a GB300
 
 template <typename T, int kThreads, bool kSplit>
 static cudaError_t launch_logps_t(const TokenArgs& a, unsigned ctas, cudaStream_t s) {
@@ -862,11 +886,11 @@ static cudaError_t launch_logps_d(TokenArgs a, cudaStream_t s) {
   // few rows: a cluster for each, while its CTAs are at most two an SM (four
   // for two halves of a long row)
   unsigned ctas = 1;
-  while (ctas < kMaxCluster && rows * (2 * ctas) <= 2 * 152 && bytes / (2 * ctas) >= kPartBytes)
+  while (ctas < kMaxCluster && rows * (2 * ctas) <= 2 * kSms && bytes / (2 * ctas) >= kPartBytes)
     ctas *= 2;
-  if (ctas == 1 && rows <= 2 * 152 && bytes >= kHalvedRowBytes) ctas = 2;
+  if (ctas == 1 && rows <= 2 * kSms && bytes >= kHalvedRowBytes) ctas = 2;
   if (ctas > 1) return launch_logps_t<T, 256, true>(a, ctas, s);
-  return rows > 2 * 152 && bytes < kLongRowBytes ? launch_logps_t<T, 128, false>(a, 1, s)
+  return rows > 2 * kSms && bytes < kLongRowBytes ? launch_logps_t<T, 128, false>(a, 1, s)
                                                  : launch_logps_t<T, 256, false>(a, 1, s);
 }
 
@@ -1066,7 +1090,7 @@ static cudaError_t launch_grad_t(const TokenGradArgs& a, cudaStream_t s) {
   // few to fill the GPU several times over, and enough to keep the grid below
   // 2^31 CTAs
   int64_t per = kRows > 1 ? steps : 1;
-  while (per < 4 && per < steps && rows * ((steps + 2 * per - 1) / (2 * per)) >= 152 * 32) per *= 2;
+  while (per < 4 && per < steps && rows * ((steps + 2 * per - 1) / (2 * per)) >= kSms * 32) per *= 2;
   while (rows * ((steps + per - 1) / per) > 0x7FFFFFFF) per *= 2;
   const int64_t ctas = (steps + per - 1) / per;
   const unsigned grid = (unsigned)(kRows > 1 ? (rows + kRows - 1) / kRows : rows * ctas);

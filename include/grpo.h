@@ -414,8 +414,8 @@ grpo_status_t grpo_vocab_grad(const void *policy_slice, grpo_dtype_t dt, int64_t
  *                     adjacent, 1 <= V < 2^31.
  *   action_ids      : [B,T] int64; may be NULL with logps NULL.
  *   completion_mask : [B,T] uint8, NULL = every token active.  A masked
- *                     token's logits and id are not read; its outputs are 0
- *                     (top ids -1, stats {0, 1}).
+ *                     token's logits are not read and its id is not used; its
+ *                     outputs are 0 (top ids -1, stats {0, 1}).
  *   temperature     : finite, > 0, and not so small (4.3e-39) that
  *                     log2(e) / temperature overflows.
  *   top_k           : 0 .. GRPO_MAX_TOP_K, at most V.
@@ -430,7 +430,9 @@ grpo_status_t grpo_vocab_grad(const void *policy_slice, grpo_dtype_t dt, int64_t
  *                     the caller zeroes it; read with grpo_read_device_status.
  * -inf logits are allowed (p = 0).  A row that holds a NaN or +inf, or only
  * -inf, has no distribution: logp, entropy, Z and top_logps are NaN, top ids
- * -1.  Sums are held in fp32; every result is bitwise reproducible. */
+ * -1.  Sums are held in fp32: Z is off by at most max(48, V es / 4096) + 20
+ * roundings (2^-24 relative; es bytes a logit) beside those of its terms.  Every
+ * result is bitwise reproducible. */
 #define GRPO_MAX_TOP_K 32
 grpo_status_t grpo_token_logps(const void *logits, grpo_dtype_t dt, int64_t B, int64_t T,
                                int64_t V, int64_t stride_b, int64_t stride_t,
@@ -469,7 +471,8 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
 /* The global norm of many gradient tensors, and clipping to it:
  *   norm = scale sqrt(sum_i sum_j g_ij^2)
  *   c    = scale min(1, max_norm / (norm + eps)),   out_ij = c g_ij
- * with c rounded to f32 and each product rounded once to the type of out_i.
+ * with c rounded to f32 and each product formed in f32, then rounded to the
+ * type of out_i.
  *   tensors, outs, numels, dtypes : HOST arrays of num_tensors entries: the
  *     device pointers (aligned to their element size; NULL with numel 0), the
  *     element counts and the grpo_dtype_t of each tensor.  outs NULL, or an
