@@ -130,6 +130,12 @@ double number(PyObject* o) {
   return v;
 }
 
+bool flag(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
+
 PyObject* want_args(Py_ssize_t n, Py_ssize_t want) {
   PyErr_Format(PyExc_TypeError, "%zd arguments, got %zd", want, n);
   return nullptr;
@@ -148,14 +154,15 @@ PyObject* token_logps(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double temperature = number(a[3]);
   const long long k = PyLong_AsLongLong(a[4]);
   if (k == -1 && PyErr_Occurred()) return nullptr;
+  const bool want_entropy = flag(a[5]), want_stats = flag(a[6]);
   void* status = status_word(a[7], x);
   const c10::cuda::CUDAGuard guard(x.device());
   const auto f32 = at::TensorOptions().dtype(at::kFloat).device(x.device());
   const auto lead = x.sizes().slice(0, x.dim() - 1);
   at::Tensor logps, entropy, stats, top_ids, top_logps;
   if (a[1] != Py_None) logps = at::empty(lead, f32);
-  if (PyObject_IsTrue(a[5])) entropy = at::empty(lead, f32);
-  if (PyObject_IsTrue(a[6])) {
+  if (want_entropy) entropy = at::empty(lead, f32);
+  if (want_stats) {
     c10::SmallVector<int64_t, 4> s{2};
     s.append(lead.begin(), lead.end());
     stats = at::empty(s, f32);
@@ -206,6 +213,7 @@ PyObject* token_logps_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* ent = token(a[5], "entropy", x, at::kFloat);
   void* dent = token(a[6], "grad_entropy", x, at::kFloat);
   const double temperature = number(a[7]);
+  const uint32_t flags = flag(a[9]) ? GRPO_SKIP_MASKED_GRAD_ROWS : 0u;
   void* status = status_word(a[10], x);
   const c10::cuda::CUDAGuard guard(x.device());
   at::Tensor grad;
@@ -220,7 +228,6 @@ PyObject* token_logps_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Rows g(grad, "grad");
   grpo_status_t rc;
   const auto stream = c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
-  const uint32_t flags = PyObject_IsTrue(a[9]) ? GRPO_SKIP_MASKED_GRAD_ROWS : 0u;
   Py_BEGIN_ALLOW_THREADS
   rc = grpo_token_logps_grad(x.data_ptr(), (grpo_dtype_t)r.dt, r.B, r.T, r.V, r.sb, r.st,
                              (const int64_t*)ids, (const uint8_t*)mask, (const float*)stats,
@@ -248,7 +255,7 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return nullptr;
   }
   const int64_t n = PyTuple_GET_SIZE(a[0]);
-  const bool outs = a[4] != Py_None, norm_only = PyObject_IsTrue(a[5]);
+  const bool outs = a[4] != Py_None, norm_only = flag(a[5]);
   const double max_norm = number(a[1]), eps = number(a[2]), scale = number(a[3]);
   if (outs && norm_only) throw Refused("norm_only writes nothing: out must be None");
   if (outs && PyTuple_GET_SIZE(a[4]) != n)
