@@ -5,7 +5,7 @@
 // Argument marshalling only, as in the package's ctypes calls.  These three
 // are called once a generated token or with hundreds of tensors, where the
 // checks and allocations in Python cost more than the kernels (0.9 us a tensor
-// of a clipping call there, 10 ns here).
+// of a clipping call there, 47 ns here with the launches' tables).
 //
 // Every function takes its arguments by position, works on the current stream
 // of the tensors' device, raises ValueError for what the C ABI cannot see
