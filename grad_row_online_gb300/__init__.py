@@ -26,6 +26,8 @@ __all__ = ["grpo_workspace_size", "grpo_group_adv", "grpo_loss_fwd_bwd", "grpo_l
            "totals_buffer", "SEQ_TOTAL_BYTES", "grpo_vocab_chunk", "grpo_vocab_partials",
            "grpo_vocab_loss", "grpo_vocab_grad",
            "grpo_token_logps", "grpo_token_logps_grad", "grpo_clip_grad_norm",
+           "grpo_linear_logps", "grpo_linear_logps_grad", "grpo_linear_workspace_size",
+           "grpo_embed_tokens", "grpo_embed_tokens_grad", "grpo_embed_workspace_size",
            "grpo_clip_workspace_size", "status_buffer", "GRPO_MAX_TOP_K",
            "grpo_read_device_status", "grpo_status_string", "GrpoError", "library_path",
            "GRPO_ADV_EPS_ADD", "GRPO_SKIP_MASKED_GRAD_ROWS"]
@@ -155,6 +157,23 @@ def lib():
         L.grpo_token_logps_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, vp, vp,
                                             vp, vp, vp, f32, vp, i64, i64, u32, vp, vp]
         L.grpo_token_logps_grad.restype = ctypes.c_int
+        L.grpo_linear_workspace_size.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, i32]
+        L.grpo_linear_workspace_size.restype = sz
+        L.grpo_linear_logps.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, i64, i64, vp,
+                                        vp, f32, vp, vp, vp, vp, vp, sz, vp]
+        L.grpo_linear_logps.restype = ctypes.c_int
+        L.grpo_linear_logps_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, i64,
+                                             i64, vp, vp, vp, vp, vp, vp, f32, vp, i64, i64, vp,
+                                             ctypes.c_int, i64, vp, i64, u32, vp, vp, sz, vp]
+        L.grpo_linear_logps_grad.restype = ctypes.c_int
+        L.grpo_embed_tokens.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, i64, i64, f32, vp,
+                                        i64, i64, vp, vp]
+        L.grpo_embed_tokens.restype = ctypes.c_int
+        L.grpo_embed_workspace_size.argtypes = [i64, i64, i64]
+        L.grpo_embed_workspace_size.restype = sz
+        L.grpo_embed_tokens_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, i64, vp, vp, i64,
+                                             f32, vp, i64, vp, ctypes.c_int, i64, vp, vp, sz, vp]
+        L.grpo_embed_tokens_grad.restype = ctypes.c_int
         L.grpo_clip_workspace_size.argtypes = [i64]
         L.grpo_clip_workspace_size.restype = sz
         L.grpo_clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, f32, f32, f32, u32, vp, vp, sz, vp]
@@ -687,6 +706,97 @@ def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tenso
                                  grad_entropy, temperature, grad, skip_masked_grad_rows, status))
 
 
+# --------------------------------------------------------------------------
+# the ends of the policy: log-probs from hidden states, token embedding
+def grpo_linear_workspace_size(hidden: torch.Tensor, weight: torch.Tensor,
+                               backward: bool = False) -> int:
+    """Bytes of ``workspace=`` for grpo_linear_logps, or its gradient, of these tensors."""
+    N = hidden.numel() // max(hidden.shape[-1], 1)
+    return int(lib().grpo_linear_workspace_size(_ptr(weight), _DTYPES[hidden.dtype], 1, N,
+                                                hidden.shape[-1], weight.shape[0],
+                                                weight.stride(0), int(backward)))
+
+
+def grpo_linear_logps(hidden: torch.Tensor, weight: torch.Tensor,
+                      action_ids: Optional[torch.Tensor],
+                      completion_mask: Optional[torch.Tensor] = None, *, temperature: float = 1.0,
+                      want_entropy: bool = False, want_stats: bool = False,
+                      workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """grpo_token_logps of the logits ``hidden @ weight.T``, which are not
+    formed in memory.
+
+    ``hidden`` [B, T, K] or [N, K] (f32, bf16, f16; rows of adjacent elements
+    at any strides), ``weight`` [V, K] of the same dtype (a head's weight, or
+    the embedding's where they are tied).  The other arguments and the results
+    ``logps``, ``entropy`` and ``stats`` are grpo_token_logps's.
+    ``workspace``: uint8 memory of grpo_linear_workspace_size bytes, else taken
+    from the allocator for the call.  Nothing is recorded for autograd."""
+    return _native_call("grpo_linear_logps", (_calls or native()).linear_logps, stream,
+                        hidden, (hidden, weight, action_ids, completion_mask, temperature,
+                                 want_entropy, want_stats, workspace, status))
+
+
+def grpo_linear_logps_grad(hidden: torch.Tensor, weight: torch.Tensor,
+                           action_ids: Optional[torch.Tensor],
+                           completion_mask: Optional[torch.Tensor], stats: torch.Tensor, *,
+                           grad_logps: Optional[torch.Tensor] = None,
+                           entropy: Optional[torch.Tensor] = None,
+                           grad_entropy: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                           grad_hidden=True, grad_weight=True,
+                           add_weight: Optional[torch.Tensor] = None,
+                           skip_masked_grad_rows: bool = False,
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """dL/dhidden and dL/dweight from dL/dlogps (``grad_logps``) and
+    dL/dentropy (``grad_entropy``, with the forward's ``entropy``); at least
+    one of the two.  ``stats`` is grpo_linear_logps's at the same temperature.
+
+    ``grad_hidden`` / ``grad_weight``: True (a new tensor), a tensor to write
+    into, or None / False (not wanted).  grad_weight has weight's dtype or is
+    f32; ``add_weight`` (of grad_weight's dtype; may be grad_weight itself) is
+    added to it: a gradient accumulated over batches, or the embedding's part
+    of a tied weight.  Returns a dict of ``grad_hidden`` and ``grad_weight``.
+    A tensor written into counts as modified in place."""
+    return _native_call("grpo_linear_logps_grad", (_calls or native()).linear_logps_grad, stream,
+                        hidden, (hidden, weight, action_ids, completion_mask, stats, grad_logps,
+                                 entropy, grad_entropy, temperature, grad_hidden, grad_weight,
+                                 add_weight, skip_masked_grad_rows, workspace, status))
+
+
+def grpo_embed_tokens(weight: torch.Tensor, token_ids: torch.Tensor,
+                      token_mask: Optional[torch.Tensor] = None, *, scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """``scale * weight[token_ids]`` ([..., K]; ``token_ids`` int64 [B, T] or
+    [N]), rounded once to weight's dtype.  Masked tokens' rows are 0, those of
+    ids outside the vocabulary NaN (``status`` collects
+    GRPO_ERR_ACTION_RANGE).  Nothing is recorded for autograd: the gradient is
+    grpo_embed_tokens_grad's."""
+    return _native_call("grpo_embed_tokens", (_calls or native()).embed_tokens, stream, weight,
+                        (weight, token_ids, token_mask, scale, out, status))
+
+
+def grpo_embed_workspace_size(num_tokens: int, K: int, V: int) -> int:
+    return int(lib().grpo_embed_workspace_size(num_tokens, K, V))
+
+
+def grpo_embed_tokens_grad(grad: torch.Tensor, token_ids: torch.Tensor, V: int,
+                           token_mask: Optional[torch.Tensor] = None, *, scale: float = 1.0,
+                           add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient [V, K] of an embedding of ``token_ids`` from that of its
+    rows (``grad`` [..., K]): for each id ``scale`` times the fp32 sum of its
+    tokens' rows, the same bits every time.  ``add`` ([V, K]; a tied head's
+    part, or earlier batches') is added; with ``out=add`` it is accumulated in
+    place and only rows of ids that occur are touched.  The result has add's
+    dtype: grad's, or f32."""
+    return _native_call("grpo_embed_tokens_grad", (_calls or native()).embed_tokens_grad, stream,
+                        grad, (grad, token_ids, V, token_mask, scale, add, out, workspace, status))
+
+
+# --------------------------------------------------------------------------
 def grpo_clip_workspace_size(num_tensors: int) -> int:
     return int(lib().grpo_clip_workspace_size(num_tensors))
 

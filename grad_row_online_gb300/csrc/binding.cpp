@@ -1,8 +1,9 @@
 // binding.cpp -- the Python calls of the entry points around the loss
-// (grpo_token_logps, grpo_token_logps_grad, grpo_clip_grad_norm): argument
-// checks, output allocation and the C call, natively.
+// (grpo_token_logps, grpo_token_logps_grad, grpo_clip_grad_norm) and at the
+// ends of the policy (grpo_linear_logps, grpo_embed_tokens and their
+// gradients): argument checks, output allocation and the C call, natively.
 //
-// Argument marshalling only, as in the package's ctypes calls.  These three
+// Argument marshalling only, as in the package's ctypes calls.  These
 // are called once a generated token or with hundreds of tensors, where the
 // checks and allocations in Python cost more than the kernels (0.9 us a tensor
 // of a clipping call there, 47 ns here with the launches' tables).
@@ -77,7 +78,46 @@ struct Rows {
     } else {
       throw Refused(n + " must be [B, T, V] or [N, V]");
     }
-    if (sv != 1 && V > 1) throw Refused("the logits of a row of " + n + " must be adjacent (stride 1)");
+    if (sv != 1 && V > 1)
+      throw Refused("the elements of a row of " + n + " must be adjacent (stride 1)");
+  }
+};
+
+// A [rows, cols] matrix of `like`'s device whose rows hold adjacent elements.
+struct Matrix {
+  int64_t rows, cols, stride;
+  int dt;
+  Matrix(const at::Tensor& x, const char* name, const at::Tensor& like) {
+    const std::string n(name);
+    dt = dtype_code(x.scalar_type());
+    if (dt < 0) throw Refused("unsupported " + n + " dtype " + c10::toString(x.scalar_type()));
+    if (!x.is_cuda() || x.device() != like.device())
+      throw Refused(n + " must be a CUDA tensor on the device of the others");
+    if (x.dim() != 2) throw Refused(n + " must be [V, K]");
+    rows = x.size(0); cols = x.size(1); stride = x.stride(0);
+    if (x.stride(1) != 1 && cols > 1)
+      throw Refused("the elements of a row of " + n + " must be adjacent (stride 1)");
+  }
+};
+
+// Workspace of a call: the caller's, or a piece of the allocator's that goes
+// back with the call.
+struct Workspace {
+  void* ptr;
+  size_t bytes;
+  c10::DataPtr own;
+  Workspace(PyObject* given, size_t need, c10::Device dev) : bytes(need) {
+    if (given != Py_None) {
+      if (!THPVariable_Check(given)) throw Refused("workspace must be a tensor");
+      const at::Tensor& t = THPVariable_Unpack(given);
+      if (t.device() != dev || !t.is_contiguous())
+        throw Refused("workspace must be a contiguous tensor on the device of the others");
+      ptr = t.data_ptr();
+      bytes = t.nbytes();
+    } else {
+      own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+      ptr = own.get();
+    }
   }
 };
 
@@ -335,7 +375,243 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// An output that the caller may give: None / False: no output, True: a new
+// tensor, else the tensor itself.
+enum class Output { none, fresh, given };
+Output output(PyObject* o) {
+  if (THPVariable_Check(o)) return Output::given;
+  if (o == Py_None) return Output::none;
+  return flag(o) ? Output::fresh : Output::none;
+}
+
+// linear_logps(hidden, weight, action_ids, completion_mask, temperature,
+//              want_entropy, want_stats, workspace, status) -> dict or status code
+PyObject* linear_logps(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GRPO_TRY
+  if (n != 9) return want_args(n, 9);
+  const at::Tensor& x = tensor(a[0], "hidden");
+  const Rows r(x, "hidden");
+  const at::Tensor& w = tensor(a[1], "weight");
+  const Matrix m(w, "weight", x);
+  if (m.dt != r.dt || m.cols != r.V)
+    throw Refused("weight must be [V, K] with the dtype and the width of hidden");
+  void* ids = token(a[2], "action_ids", x, at::kLong);
+  void* mask = token(a[3], "completion_mask", x, at::kByte);
+  const double temperature = number(a[4]);
+  const bool want_entropy = flag(a[5]), want_stats = flag(a[6]);
+  void* status = status_word(a[8], x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const auto f32 = at::TensorOptions().dtype(at::kFloat).device(x.device());
+  const auto lead = x.sizes().slice(0, x.dim() - 1);
+  const Workspace ws(a[7], grpo_linear_workspace_size(w.data_ptr(), (grpo_dtype_t)r.dt, r.B, r.T,
+                                                      r.V, m.rows, m.stride, 0), x.device());
+  at::Tensor logps, entropy, stats;
+  if (a[2] != Py_None) logps = at::empty(lead, f32);
+  if (want_entropy) entropy = at::empty(lead, f32);
+  if (want_stats) {
+    c10::SmallVector<int64_t, 4> s{2};
+    s.append(lead.begin(), lead.end());
+    stats = at::empty(s, f32);
+  }
+  auto at_ptr = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  grpo_status_t rc;
+  const auto stream = c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
+  Py_BEGIN_ALLOW_THREADS
+  rc = grpo_linear_logps(x.data_ptr(), (grpo_dtype_t)r.dt, r.B, r.T, r.V, r.sb, r.st, w.data_ptr(),
+                         m.rows, m.stride, (const int64_t*)ids, (const uint8_t*)mask,
+                         (float)temperature, (float*)at_ptr(logps), (float*)at_ptr(entropy),
+                         (float*)at_ptr(stats), status, ws.ptr, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
+  THPObjectPtr out(PyDict_New());
+  if (!out) return nullptr;
+  put(out, "logps", logps);
+  put(out, "entropy", entropy);
+  put(out, "stats", stats);
+  return out.release();
+  GRPO_CATCH
+  END_HANDLE_TH_ERRORS
+}
+
+// linear_logps_grad(hidden, weight, action_ids, completion_mask, stats,
+//                   grad_logps, entropy, grad_entropy, temperature, grad_hidden,
+//                   grad_weight, add_weight, skip_masked, workspace, status)
+// -> dict or status code
+PyObject* linear_logps_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GRPO_TRY
+  if (n != 15) return want_args(n, 15);
+  const at::Tensor& x = tensor(a[0], "hidden");
+  const Rows r(x, "hidden");
+  const at::Tensor& w = tensor(a[1], "weight");
+  const Matrix m(w, "weight", x);
+  if (m.dt != r.dt || m.cols != r.V)
+    throw Refused("weight must be [V, K] with the dtype and the width of hidden");
+  void* ids = token(a[2], "action_ids", x, at::kLong);
+  void* mask = token(a[3], "completion_mask", x, at::kByte);
+  if (a[4] == Py_None) throw Refused("stats (of grpo_linear_logps, with want_stats) is required");
+  void* stats = token(a[4], "stats", x, at::kFloat, 2);
+  void* dlogp = token(a[5], "grad_logps", x, at::kFloat);
+  void* ent = token(a[6], "entropy", x, at::kFloat);
+  void* dent = token(a[7], "grad_entropy", x, at::kFloat);
+  const double temperature = number(a[8]);
+  const Output to_hidden = output(a[9]), to_weight = output(a[10]);
+  const uint32_t flags = flag(a[12]) ? GRPO_SKIP_MASKED_GRAD_ROWS : 0u;
+  void* status = status_word(a[14], x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  at::Tensor add, gh, gw;
+  if (a[11] != Py_None) add = tensor(a[11], "add_weight");
+  if (to_hidden == Output::fresh) gh = at::empty(x.sizes(), x.options());
+  if (to_hidden == Output::given) gh = tensor(a[9], "grad_hidden");
+  if (to_weight == Output::fresh)
+    gw = at::empty(w.sizes(), w.options().dtype(add.defined() ? add.scalar_type() : w.scalar_type()));
+  if (to_weight == Output::given) gw = tensor(a[10], "grad_weight");
+  int64_t gsb = 0, gst = 0, gsv = 0, asv = 0;
+  if (gh.defined()) {
+    if (gh.sizes() != x.sizes() || gh.scalar_type() != x.scalar_type() || gh.device() != x.device())
+      throw Refused("grad_hidden must have the shape, dtype and device of hidden");
+    const Rows g(gh, "grad_hidden");
+    gsb = g.sb; gst = g.st;
+  }
+  if (gw.defined()) {
+    const Matrix g(gw, "grad_weight", x);
+    if (gw.sizes() != w.sizes() || (g.dt != m.dt && g.dt != GRPO_F32))
+      throw Refused("grad_weight must have the shape of weight, and its dtype or float32");
+    gsv = g.stride;
+  }
+  if (add.defined()) {
+    const Matrix g(add, "add_weight", x);
+    if (!gw.defined() || add.sizes() != w.sizes() || add.scalar_type() != gw.scalar_type())
+      throw Refused("add_weight must have the shape and dtype of grad_weight");
+    asv = g.stride;
+  }
+  const Workspace ws(a[13], grpo_linear_workspace_size(w.data_ptr(), (grpo_dtype_t)r.dt, r.B, r.T,
+                                                       r.V, m.rows, m.stride, 1), x.device());
+  auto at_ptr = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  grpo_status_t rc;
+  const auto stream = c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
+  const int wdt = gw.defined() ? dtype_code(gw.scalar_type()) : r.dt;
+  Py_BEGIN_ALLOW_THREADS
+  rc = grpo_linear_logps_grad(
+      x.data_ptr(), (grpo_dtype_t)r.dt, r.B, r.T, r.V, r.sb, r.st, w.data_ptr(), m.rows, m.stride,
+      (const int64_t*)ids, (const uint8_t*)mask, (const float*)stats, (const float*)ent,
+      (const float*)dlogp, (const float*)dent, (float)temperature, at_ptr(gh), gsb, gst, at_ptr(gw),
+      (grpo_dtype_t)wdt, gsv, at_ptr(add), asv, flags, status, ws.ptr, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
+  if (to_hidden == Output::given) written(gh);
+  if (to_weight == Output::given) written(gw);
+  THPObjectPtr out(PyDict_New());
+  if (!out) return nullptr;
+  put(out, "grad_hidden", gh);
+  put(out, "grad_weight", gw);
+  return out.release();
+  GRPO_CATCH
+  END_HANDLE_TH_ERRORS
+}
+
+// Token ids [B, T] or [N] (int64), which give the embedding's leading shape.
+const at::Tensor& token_ids(PyObject* o, c10::Device dev) {
+  const at::Tensor& t = tensor(o, "token_ids");
+  if (t.scalar_type() != at::kLong || t.device() != dev || !t.is_contiguous() || t.dim() < 1 ||
+      t.dim() > 2)
+    throw Refused("token_ids must be a contiguous int64 tensor [B, T] or [N] on the device of the "
+                  "others");
+  return t;
+}
+
+// embed_tokens(weight, token_ids, token_mask, scale, out, status) -> tensor or status code
+PyObject* embed_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GRPO_TRY
+  if (n != 6) return want_args(n, 6);
+  const at::Tensor& w = tensor(a[0], "weight");
+  const Matrix m(w, "weight", w);
+  const at::Tensor& ids = token_ids(a[1], w.device());
+  const double scale = number(a[3]);
+  const c10::cuda::CUDAGuard guard(w.device());
+  c10::SmallVector<int64_t, 4> size(ids.sizes().begin(), ids.sizes().end());
+  size.push_back(m.cols);
+  at::Tensor out;
+  if (a[4] == Py_None) {
+    out = at::empty(size, w.options());
+  } else {
+    out = tensor(a[4], "out");
+    if (out.sizes() != at::IntArrayRef(size) || out.scalar_type() != w.scalar_type() ||
+        out.device() != w.device())
+      throw Refused("out must be [..., K] of the ids' shape, with the dtype and device of weight");
+  }
+  const Rows r(out, "out");
+  void* mask = token(a[2], "token_mask", out, at::kByte);
+  void* status = status_word(a[5], out);
+  grpo_status_t rc;
+  const auto stream = c10::cuda::getCurrentCUDAStream(w.device().index()).stream();
+  Py_BEGIN_ALLOW_THREADS
+  rc = grpo_embed_tokens(w.data_ptr(), (grpo_dtype_t)m.dt, m.rows, m.cols, m.stride,
+                         (const int64_t*)ids.data_ptr(), (const uint8_t*)mask, r.B, r.T,
+                         (float)scale, out.data_ptr(), r.sb, r.st, status, stream);
+  Py_END_ALLOW_THREADS
+  if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
+  if (a[4] != Py_None) written(out);
+  return THPVariable_Wrap(out);
+  GRPO_CATCH
+  END_HANDLE_TH_ERRORS
+}
+
+// embed_tokens_grad(grad, token_ids, V, token_mask, scale, add, out, workspace, status)
+// -> tensor or status code
+PyObject* embed_tokens_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  GRPO_TRY
+  if (n != 9) return want_args(n, 9);
+  const at::Tensor& x = tensor(a[0], "grad");
+  const Rows r(x, "grad");
+  const at::Tensor& ids = token_ids(a[1], x.device());
+  if (ids.sizes() != x.sizes().slice(0, x.dim() - 1))
+    throw Refused("grad must be [..., K] of the ids' shape");
+  const long long V = PyLong_AsLongLong(a[2]);
+  if (V == -1 && PyErr_Occurred()) return nullptr;
+  void* mask = token(a[3], "token_mask", x, at::kByte);
+  const double scale = number(a[4]);
+  void* status = status_word(a[8], x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  if (V < 1) throw Refused("V must be at least 1");
+  at::Tensor add, out;
+  if (a[5] != Py_None) add = tensor(a[5], "add");
+  if (a[6] != Py_None) out = tensor(a[6], "out");
+  else out = at::empty({V, r.V}, x.options().dtype(add.defined() ? add.scalar_type() : x.scalar_type()));
+  const Matrix o(out, "out", x);
+  if (o.rows != V || o.cols != r.V || (o.dt != r.dt && o.dt != GRPO_F32))
+    throw Refused("out must be [V, K] with the dtype of grad, or float32");
+  int64_t asv = 0;
+  if (add.defined()) {
+    const Matrix m(add, "add", x);
+    if (add.sizes() != out.sizes() || add.scalar_type() != out.scalar_type())
+      throw Refused("add must have the shape and dtype of the output");
+    asv = m.stride;
+  }
+  const Workspace ws(a[7], grpo_embed_workspace_size(r.B * r.T, r.V, V), x.device());
+  grpo_status_t rc;
+  const auto stream = c10::cuda::getCurrentCUDAStream(x.device().index()).stream();
+  Py_BEGIN_ALLOW_THREADS
+  rc = grpo_embed_tokens_grad(x.data_ptr(), (grpo_dtype_t)r.dt, r.B, r.T, r.V, r.sb, r.st,
+                              (const int64_t*)ids.data_ptr(), (const uint8_t*)mask, V, (float)scale,
+                              add.defined() ? add.data_ptr() : nullptr, asv, out.data_ptr(),
+                              (grpo_dtype_t)o.dt, o.stride, status, ws.ptr, ws.bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (rc != GRPO_OK) return PyLong_FromLong((long)rc);
+  if (a[6] != Py_None) written(out);
+  return THPVariable_Wrap(out);
+  GRPO_CATCH
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
+    {"linear_logps", (PyCFunction)(void (*)(void))linear_logps, METH_FASTCALL, nullptr},
+    {"linear_logps_grad", (PyCFunction)(void (*)(void))linear_logps_grad, METH_FASTCALL, nullptr},
+    {"embed_tokens", (PyCFunction)(void (*)(void))embed_tokens, METH_FASTCALL, nullptr},
+    {"embed_tokens_grad", (PyCFunction)(void (*)(void))embed_tokens_grad, METH_FASTCALL, nullptr},
     {"token_logps", (PyCFunction)(void (*)(void))token_logps, METH_FASTCALL, nullptr},
     {"token_logps_grad", (PyCFunction)(void (*)(void))token_logps_grad, METH_FASTCALL, nullptr},
     {"clip_grad_norm", (PyCFunction)(void (*)(void))clip_grad_norm, METH_FASTCALL, nullptr},

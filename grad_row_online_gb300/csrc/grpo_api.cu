@@ -9,7 +9,9 @@
 //   reduce   fixed-order reduction to the scalars        grpo_reduce.cu
 // or, for the logps-only boundary, prep + the kernel of grpo_logps.cu.
 // The token log-probs, their gradient (grpo_token.cu) and the gradient norm
-// (grpo_clip.cu) are entry points of their own, without header or prep.
+// (grpo_clip.cu) are entry points of their own, without header or prep, and so
+// are the head's log-probs from hidden states (grpo_linear.cu) and the
+// embedding of tokens (grpo_embed.cu), with their gradients.
 // A shard call (grpo_shard_t) runs the same kernels on its sequences, with
 // the whole batch's groups and counts, and leaves the scalar to
 // grpo_loss_finalize.
@@ -17,6 +19,8 @@
 #include <string.h>
 
 #include "grpo_around.cuh"
+#include "grpo_embed.cuh"
+#include "grpo_linear.cuh"
 
 using namespace grpo;
 
@@ -129,6 +133,31 @@ bool rows_disjoint(int64_t B, int64_t T, int64_t V, int64_t sb, int64_t st) {
 // Limits of grpo_clip_grad_norm: chunks are numbered in 32 bits.
 static constexpr int64_t kMaxClipTensors = 1 << 20;
 static constexpr int64_t kMaxClipNumel = (int64_t)1 << 40;
+
+// Limits of the head and the embedding: rows, words and their tiles are
+// numbered in 31 bits, the last tile's end among them.
+static constexpr int64_t kMaxRows = 0x7FFFFFFF - 1024;
+static constexpr int64_t kMaxWidth = 1 << 20;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A [V, K] matrix of rows `sv` apart.
+bool matrix_ok(int64_t V, int64_t K, int64_t sv) {
+  if (V < 1 || V > kMaxRows || K < 1 || K > kMaxWidth) return false;
+  return V == 1 || (sv >= K && sv <= ((int64_t)1 << 36) && (double)V * (double)sv < 4.0e18);
+}
+
+grpo_status_t check_linear_shape(int64_t B, int64_t T, int64_t K, int64_t V, int64_t sb, int64_t st,
+                                 int64_t sv) {
+  grpo_status_t e = check_token_shape(B, T, K, sb, st);
+  if (e != GRPO_OK) return e;
+  if (B * T > kMaxRows || !matrix_ok(V, K, sv)) return GRPO_ERR_SHAPE;
+  const int64_t most = 0x7FFFFFFF, nv = ceil_div(V, 64), nk = ceil_div(K, 64);
+  if (ceil_div(B * T, 128) * nv >= most || ceil_div(V, 128) * nk >= most ||
+      ceil_div(B * T, 128) * nk >= most / 128)
+    return GRPO_ERR_SHAPE;
+  return GRPO_OK;
+}
 
 grpo_status_t check_ws(const void* ws, size_t ws_bytes, int64_t B, int64_t T) {
   if (!ws) return GRPO_ERR_NULL;
@@ -626,6 +655,158 @@ extern "C" grpo_status_t grpo_token_logps_grad(
                   grad_stride_b, grad_stride_t, (flags & GRPO_SKIP_MASKED_GRAD_ROWS) ? 1 : 0,
                   (WsHeader*)status_ws};
   return cuda_status(launch_token_grad(a, dt, (cudaStream_t)stream));
+}
+
+extern "C" size_t grpo_linear_workspace_size(const void* weight, grpo_dtype_t dt, int64_t B,
+                                             int64_t T, int64_t K, int64_t V, int64_t stride_v,
+                                             int32_t backward) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return 0;
+  if (check_linear_shape(B, T, K, V, 0, 0, stride_v) != GRPO_OK) return 0;
+  return linear_ws(weight, dt, B * T, K, V, stride_v, backward != 0);
+}
+
+extern "C" grpo_status_t grpo_linear_logps(
+    const void* hidden, grpo_dtype_t dt, int64_t B, int64_t T, int64_t K, int64_t stride_b,
+    int64_t stride_t, const void* weight, int64_t V, int64_t stride_v, const int64_t* action_ids,
+    const uint8_t* completion_mask, float temperature, float* logps, float* entropy, float* stats,
+    void* status_ws, void* ws, size_t ws_bytes, void* stream) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
+  grpo_status_t st = check_linear_shape(B, T, K, V, stride_b, stride_t, stride_v);
+  if (st != GRPO_OK) return st;
+  if (!temperature_ok(temperature)) return GRPO_ERR_PARAM;
+  if (B * T == 0) return GRPO_OK;
+  if (!hidden || !weight || !ws || (logps && !action_ids)) return GRPO_ERR_NULL;
+  const size_t es = elem_size(dt);
+  if (!aligned(hidden, es) || !aligned(weight, es) || !aligned(action_ids, 8) ||
+      !aligned(logps, 4) || !aligned(entropy, 4) || !aligned(stats, 4) ||
+      !aligned(status_ws, 256) || !aligned(ws, 256))
+    return GRPO_ERR_ALIGN;
+  if (ws_bytes < linear_ws(weight, dt, B * T, K, V, stride_v, false)) return GRPO_ERR_WORKSPACE;
+  LinearArgs a{};
+  a.hidden = hidden;
+  a.weight = weight;
+  a.B = B, a.T = T, a.K = K, a.V = V, a.sb = stride_b, a.st = stride_t, a.sv = stride_v;
+  a.actions = logps ? action_ids : nullptr;
+  a.mask = completion_mask;
+  a.inv_t = (float)(1.0 / (double)temperature);
+  a.s2 = (float)(1.4426950408889634 / (double)temperature);
+  a.hdr = (WsHeader*)status_ws;
+  a.ws = (char*)ws;
+  a.logps = logps, a.entropy = entropy, a.stats = stats;
+  return cuda_status(launch_linear_logps(a, dt, (cudaStream_t)stream));
+}
+
+extern "C" grpo_status_t grpo_linear_logps_grad(
+    const void* hidden, grpo_dtype_t dt, int64_t B, int64_t T, int64_t K, int64_t stride_b,
+    int64_t stride_t, const void* weight, int64_t V, int64_t stride_v, const int64_t* action_ids,
+    const uint8_t* completion_mask, const float* stats, const float* entropy,
+    const float* grad_logps, const float* grad_entropy, float temperature, void* grad_hidden,
+    int64_t grad_stride_b, int64_t grad_stride_t, void* grad_weight, grpo_dtype_t grad_weight_dt,
+    int64_t grad_stride_v, const void* add_weight, int64_t add_stride_v, uint32_t flags,
+    void* status_ws, void* ws, size_t ws_bytes, void* stream) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
+  if (grad_weight && grad_weight_dt != dt && grad_weight_dt != GRPO_F32) return GRPO_ERR_DTYPE;
+  grpo_status_t st = check_linear_shape(B, T, K, V, stride_b, stride_t, stride_v);
+  if (st != GRPO_OK) return st;
+  if (grad_hidden) {
+    if ((st = check_token_shape(B, T, K, grad_stride_b, grad_stride_t)) != GRPO_OK) return st;
+    if (!rows_disjoint(B, T, K, grad_stride_b, grad_stride_t)) return GRPO_ERR_SHAPE;
+  }
+  if (grad_weight && !matrix_ok(V, K, grad_stride_v)) return GRPO_ERR_SHAPE;
+  if (add_weight && (!matrix_ok(V, K, add_stride_v) ||
+                     (add_weight == grad_weight && V > 1 && add_stride_v != grad_stride_v)))
+    return GRPO_ERR_SHAPE;
+  if (!temperature_ok(temperature)) return GRPO_ERR_PARAM;
+  if (flags & ~GRPO_SKIP_MASKED_GRAD_ROWS) return GRPO_ERR_PARAM;
+  if ((!grad_hidden && !grad_weight) || (add_weight && !grad_weight)) return GRPO_ERR_NULL;
+  const int64_t N = B * T;
+  if (N > 0 && ((!grad_logps && !grad_entropy) || !hidden || !stats ||
+                (grad_logps && !action_ids) || (grad_entropy && !entropy)))
+    return GRPO_ERR_NULL;
+  if (N == 0 && !grad_weight) return GRPO_OK;
+  if (!weight || !ws) return GRPO_ERR_NULL;
+  const size_t es = elem_size(dt);
+  const size_t ws_es = grad_weight ? elem_size(grad_weight_dt) : 1;
+  if (!aligned(hidden, es) || !aligned(weight, es) || !aligned(grad_hidden, es) ||
+      !aligned(grad_weight, ws_es) || !aligned(add_weight, ws_es) || !aligned(action_ids, 8) ||
+      !aligned(stats, 4) || !aligned(entropy, 4) || !aligned(grad_logps, 4) ||
+      !aligned(grad_entropy, 4) || !aligned(status_ws, 256) || !aligned(ws, 256))
+    return GRPO_ERR_ALIGN;
+  if (ws_bytes < linear_ws(weight, dt, N, K, V, stride_v, true)) return GRPO_ERR_WORKSPACE;
+  LinearArgs a{};
+  a.hidden = hidden;
+  a.weight = weight;
+  a.B = B, a.T = T, a.K = K, a.V = V, a.sb = stride_b, a.st = stride_t, a.sv = stride_v;
+  a.actions = grad_logps ? action_ids : nullptr;
+  a.mask = completion_mask;
+  a.inv_t = (float)(1.0 / (double)temperature);
+  a.s2 = (float)(1.4426950408889634 / (double)temperature);
+  a.hdr = (WsHeader*)status_ws;
+  a.ws = (char*)ws;
+  a.in_stats = stats;
+  a.in_entropy = grad_entropy ? entropy : nullptr;
+  a.dlogp = grad_logps, a.dent = grad_entropy;
+  a.dhidden = grad_hidden, a.gsb = grad_stride_b, a.gst = grad_stride_t;
+  a.dweight = grad_weight, a.gsv = grad_stride_v;
+  a.add = add_weight, a.asv = add_stride_v, a.wdt = grad_weight ? grad_weight_dt : dt;
+  a.skip_masked = (flags & GRPO_SKIP_MASKED_GRAD_ROWS) ? 1 : 0;
+  return cuda_status(launch_linear_grad(a, dt, (cudaStream_t)stream));
+}
+
+extern "C" grpo_status_t grpo_embed_tokens(const void* weight, grpo_dtype_t dt, int64_t V,
+                                           int64_t K, int64_t stride_v, const int64_t* token_ids,
+                                           const uint8_t* token_mask, int64_t B, int64_t T,
+                                           float scale, void* out, int64_t stride_b,
+                                           int64_t stride_t, void* status_ws, void* stream) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
+  grpo_status_t st = check_token_shape(B, T, K, stride_b, stride_t);
+  if (st != GRPO_OK) return st;
+  if (!matrix_ok(V, K, stride_v) || B * T > kMaxRows || !rows_disjoint(B, T, K, stride_b, stride_t))
+    return GRPO_ERR_SHAPE;
+  if (!isfinite(scale)) return GRPO_ERR_PARAM;
+  if (B * T == 0) return GRPO_OK;
+  if (!weight || !token_ids || !out) return GRPO_ERR_NULL;
+  const size_t es = elem_size(dt);
+  if (!aligned(weight, es) || !aligned(out, es) || !aligned(token_ids, 8) ||
+      !aligned(status_ws, 256))
+    return GRPO_ERR_ALIGN;
+  EmbedArgs a{weight, V, K, stride_v, B * T, T, token_ids, token_mask, scale, out, stride_b,
+              stride_t, (WsHeader*)status_ws};
+  return cuda_status(launch_embed(a, dt, (cudaStream_t)stream));
+}
+
+extern "C" size_t grpo_embed_workspace_size(int64_t N, int64_t K, int64_t V) {
+  if (N < 0 || N > kMaxRows || !matrix_ok(V, K, K)) return 0;
+  return embed_ws(N, K, V);
+}
+
+extern "C" grpo_status_t grpo_embed_tokens_grad(
+    const void* grad, grpo_dtype_t dt, int64_t B, int64_t T, int64_t K, int64_t stride_b,
+    int64_t stride_t, const int64_t* token_ids, const uint8_t* token_mask, int64_t V, float scale,
+    const void* add, int64_t add_stride_v, void* grad_weight, grpo_dtype_t grad_weight_dt,
+    int64_t out_stride_v, void* status_ws, void* ws, size_t ws_bytes, void* stream) {
+  if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
+  if (grad_weight_dt != dt && grad_weight_dt != GRPO_F32) return GRPO_ERR_DTYPE;
+  grpo_status_t st = check_token_shape(B, T, K, stride_b, stride_t);
+  if (st != GRPO_OK) return st;
+  const int64_t N = B * T;
+  if (!matrix_ok(V, K, out_stride_v) || N > kMaxRows ||
+      ceil_div(N, 32) * ceil_div(K, 512) >= 0x7FFFFFFF)
+    return GRPO_ERR_SHAPE;
+  if (add && (!matrix_ok(V, K, add_stride_v) ||
+              (add == grad_weight && V > 1 && add_stride_v != out_stride_v)))
+    return GRPO_ERR_SHAPE;
+  if (!isfinite(scale)) return GRPO_ERR_PARAM;
+  if (!grad_weight || !ws || (N > 0 && (!grad || !token_ids))) return GRPO_ERR_NULL;
+  const size_t es = elem_size(dt), os = elem_size(grad_weight_dt);
+  if (!aligned(grad, es) || !aligned(token_ids, 8) || !aligned(add, os) ||
+      !aligned(grad_weight, os) || !aligned(status_ws, 256) || !aligned(ws, 256))
+    return GRPO_ERR_ALIGN;
+  if (ws_bytes < embed_ws(N, K, V)) return GRPO_ERR_WORKSPACE;
+  EmbedGradArgs a{grad, V, K, stride_b, stride_t, N, T, token_ids, token_mask, scale, add,
+                  add_stride_v, grad_weight, out_stride_v, grad_weight_dt, (WsHeader*)status_ws,
+                  (char*)ws};
+  return cuda_status(launch_embed_grad(a, dt, (cudaStream_t)stream));
 }
 
 extern "C" size_t grpo_clip_workspace_size(int64_t num_tensors) {

@@ -468,6 +468,113 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
                                     int64_t grad_stride_t, uint32_t flags, void *status_ws,
                                     void *stream);
 
+/* Log-probs of given tokens straight from hidden states and the head's weight:
+ * grpo_token_logps of the logits x_v = sum_k h_k W_vk, which are formed a tile
+ * of the vocabulary at a time, on the tensor cores, and never stored.
+ *   hidden          : [B,T,K] of dtype `dt`; row (b, t) starts at element
+ *                     b stride_b + t stride_t, its K elements are adjacent
+ *                     (strides >= 0: a completion's slice of longer sequences,
+ *                     [T,B,K] orders and broadcast rows need no copy).
+ *   weight          : [V,K] of the same dtype, row v at element v stride_v
+ *                     (stride_v >= K where V > 1); must not overlap an output.
+ *   action_ids, completion_mask, temperature, logps, entropy, stats, status_ws:
+ *                     as for grpo_token_logps; a masked token's hidden state is
+ *                     not read.
+ * Products of bf16 and f16 are exact and summed in fp32; f32 operands are split
+ * into three bf16 parts, whose products are formed but for those below 2^-26
+ * of |h_k W_vk|.  A row with a NaN or +inf logit, or only -inf, has no
+ * distribution: logp, entropy and Z are NaN.  (An infinite f32 operand makes
+ * its logits NaN.)  Results are bitwise reproducible.
+ * Sizes: B T and V at most 2^31 - 1025, K at most 2^20, and
+ * ceil(B T / 128) ceil(V / 64) < 2^31.
+ * ws: grpo_linear_workspace_size(..., 0) bytes, 256-byte aligned, needs no
+ * initialisation: the active tokens' hidden states side by side, 16 bytes a
+ * token for each 64 to 256 words of the vocabulary, and a copy of the weight
+ * where its rows are not 16-byte aligned or f32. */
+size_t grpo_linear_workspace_size(const void *weight, grpo_dtype_t dt, int64_t B, int64_t T,
+                                  int64_t K, int64_t V, int64_t stride_v, int32_t backward);
+
+grpo_status_t grpo_linear_logps(const void *hidden, grpo_dtype_t dt, int64_t B, int64_t T,
+                                int64_t K, int64_t stride_b, int64_t stride_t, const void *weight,
+                                int64_t V, int64_t stride_v, const int64_t *action_ids,
+                                const uint8_t *completion_mask, float temperature, float *logps,
+                                float *entropy, float *stats, void *status_ws, void *ws,
+                                size_t ws_bytes, void *stream);
+
+/* The gradients of grpo_linear_logps with respect to hidden states and weight,
+ * from those of its logps (dlogp) and entropy (dH):
+ *   d_v = s (dlogp (1[v = a] - p_v) - dH p_v (log p_v + H))
+ *   dL/dh_k = sum_v d_v W_vk,   dL/dW_vk = add_vk + sum over tokens of d_v h_k
+ * The logits are formed again, and d exists for a piece of the vocabulary at a
+ * time, rounded to the operands' dtype for its products (f32: three bf16
+ * parts; f16: scaled by a power of two that keeps its values in range).
+ *   stats, entropy, grad_logps, grad_entropy, status_ws: as for
+ *                     grpo_token_logps_grad.
+ *   grad_hidden     : [B,T,K] of dtype `dt`, rows at b grad_stride_b +
+ *                     t grad_stride_t, not overlapping; nullable.  Rows of
+ *                     masked tokens and of tokens without a gradient are set
+ *                     to 0, or left as they were where masked with
+ *                     GRPO_SKIP_MASKED_GRAD_ROWS in flags.
+ *   grad_weight     : [V,K] of dtype `dt` or GRPO_F32 (grad_weight_dt), rows
+ *                     grad_stride_v apart; nullable (not with grad_hidden NULL).
+ *   add_weight      : [V,K] of grad_weight's type, rows add_stride_v apart,
+ *                     NULL = 0; may be grad_weight itself with the same stride
+ *                     (accumulation in place), and must not overlap it otherwise.
+ * Outputs must not overlap inputs otherwise.  An id outside [0, V) on an active token with dlogp != 0,
+ * or a row without a distribution, makes its row of grad_hidden and
+ * all of grad_weight NaN (the former sets GRPO_ERR_ACTION_RANGE).
+ * ws: grpo_linear_workspace_size(..., 1) bytes. */
+grpo_status_t grpo_linear_logps_grad(
+    const void *hidden, grpo_dtype_t dt, int64_t B, int64_t T, int64_t K, int64_t stride_b,
+    int64_t stride_t, const void *weight, int64_t V, int64_t stride_v, const int64_t *action_ids,
+    const uint8_t *completion_mask, const float *stats, const float *entropy,
+    const float *grad_logps, const float *grad_entropy, float temperature, void *grad_hidden,
+    int64_t grad_stride_b, int64_t grad_stride_t, void *grad_weight, grpo_dtype_t grad_weight_dt,
+    int64_t grad_stride_v, const void *add_weight, int64_t add_stride_v, uint32_t flags,
+    void *status_ws, void *ws, size_t ws_bytes, void *stream);
+
+/* The embedding of tokens: out_bt = scale W[id_bt], formed in fp32 and rounded
+ * once.
+ *   weight          : [V,K] of dtype `dt`, rows stride_v apart.
+ *   token_ids       : [B,T] int64.
+ *   token_mask      : [B,T] uint8, NULL = every token; a masked token's id is
+ *                     not used and its row is 0.
+ *   scale           : finite.
+ *   out             : [B,T,K] of dtype `dt`, row (b, t) at element
+ *                     b stride_b + t stride_t, rows not overlapping.
+ * An id outside [0, V) makes its row NaN and sets GRPO_ERR_ACTION_RANGE in
+ * status_ws (nullable, as for grpo_token_logps). */
+grpo_status_t grpo_embed_tokens(const void *weight, grpo_dtype_t dt, int64_t V, int64_t K,
+                                int64_t stride_v, const int64_t *token_ids,
+                                const uint8_t *token_mask, int64_t B, int64_t T, float scale,
+                                void *out, int64_t stride_b, int64_t stride_t, void *status_ws,
+                                void *stream);
+
+/* Its gradient: grad_weight_v = add_v + scale sum over tokens n with id_n = v
+ * of grad_n (n = b T + t).  The tokens are sorted by id, each id's rows summed in fp32 in
+ * an order that depends on the ids alone, and rounded once.
+ *   grad            : [B,T,K] of dtype `dt`, row (b, t) at b stride_b +
+ *                     t stride_t.
+ *   token_ids, token_mask, scale, status_ws: as above; masked tokens and ids
+ *                     outside [0, V) (which set GRPO_ERR_ACTION_RANGE) add
+ *                     nothing, and their rows of grad are not read.
+ *   grad_weight     : [V,K] of dtype `dt` or GRPO_F32, rows out_stride_v apart.
+ *   add             : [V,K] of grad_weight's type, NULL = 0 (ids without a
+ *                     token get 0 rows); may be grad_weight itself with the
+ *                     same stride: then only rows that some token has are
+ *                     touched.  No other overlap.
+ * Sizes: B T and V at most 2^31 - 1025, K at most 2^20, and
+ * ceil(B T / 32) ceil(K / 512) < 2^31.
+ * ws: grpo_embed_workspace_size(B T, K, V) bytes, 256-byte aligned. */
+size_t grpo_embed_workspace_size(int64_t N, int64_t K, int64_t V);
+
+grpo_status_t grpo_embed_tokens_grad(const void *grad, grpo_dtype_t dt, int64_t B, int64_t T,
+                                     int64_t K, int64_t stride_b, int64_t stride_t,
+                                     const int64_t *token_ids, const uint8_t *token_mask,
+                                     int64_t V, float scale, const void *add, int64_t add_stride_v, void *grad_weight,
+                                     grpo_dtype_t grad_weight_dt, int64_t out_stride_v,
+                                     void *status_ws, void *ws, size_t ws_bytes, void *stream);
+
 /* The global norm of many gradient tensors, and clipping to it:
  *   norm = scale sqrt(sum_i sum_j g_ij^2)
  *   c    = scale min(1, max_norm / (norm + eps)),   out_ij = c g_ij
