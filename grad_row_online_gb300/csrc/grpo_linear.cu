@@ -11,6 +11,8 @@
 // their online softmax (kStats), the logits again with their gradient
 // (kGrad), and the two products of that gradient (kHidden, kWeight).  The
 // gradient of the logits exists for a piece of the vocabulary at a time.
+// Every kernel here may be set up while the one before it ends, and waits for
+// that before it touches memory.
 #include <cuda.h>
 
 #include <algorithm>
@@ -26,12 +28,13 @@ using namespace tc;
 
 enum Epi { kStats, kGrad, kHidden, kWeight };
 
-static constexpr int kThreads = 256;  // warps: loads, products, tensor memory, (idle), 4 of results
+static constexpr int kThreads = 384;  // warps: loads, products, tensor memory, (idle), 8 of results
 static constexpr int kBlk = 64;       // elements of the reduction a stage holds: 128 bytes a row
 static constexpr int kRows = 128;     // rows of a CTA's tile (lanes of tensor memory)
 static constexpr int kPad = 256;      // packed rows are padded to the rows of a pair's tile
-static constexpr int kMaxStages = 8;
-static constexpr int kSmemStages = 216 * 1024;
+static constexpr int kMaxStages = 12;
+static constexpr int kSmem = 226 * 1024;  // of a CTA's 227 KB
+static constexpr int kTurn = 33;          // words of a row in the results' 16 x 32 turn
 
 struct Product {
   CUtensorMap a, b;
@@ -43,6 +46,10 @@ struct Product {
   int kb;         // blocks of the reduction where it is not over the rows
   int splits;     // parts of the reduction (kHidden)
   int pairs;      // products of planes: 1, or 6 of three planes each
+  int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
+  int kc;         // kStats, kCg 1: sets of accumulators that the reduction is cut into, in order
+  int slot, bufs; // columns of a set; tiles that are in flight, 1 or 2
+  int run;        // kStats: one record of a CTA's tiles, which are of the same rows
   int stages, mb; // tiles of rows that are taken together
   uint32_t fmt;
   float s, s2;
@@ -56,12 +63,12 @@ struct Product {
   // kGrad
   const float4* coef;    // [rpad] of (m, c0, c1, s dlogp)
   const int* target;     // [rpad]
-  int want_entropy;      // (both): D, c1 wanted
   __nv_bfloat16* d;      // [planes][rpad][ldd]
   int64_t ldd;
   const unsigned* bound; // f16: largest |d|, as bits; nullptr: no scaling
   // kHidden: fp32 sums, or results
-  float* acc;            // [splits][rpad][K]
+  float* acc;            // [splits][rpad][ldacc]
+  int64_t ldacc;
   int acc_old, acc_new;  // sums are there, are left there
   void* out;
   int64_t T, osb, ost;   // rows of the results
@@ -75,50 +82,141 @@ struct Tile {
   int m0, n0, k0, k1, split;
 };
 
+struct Stats {
+  float m, Z, D;
+};
+
 // Products of planes, the small ones first: x = x0 + x1 + x2 in bf16, and what
 // is left out is below 2^-26 of |x| |w|.
 __device__ __constant__ signed char kPairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
 
-// 2^e with the largest |d| times it in [2^13, 2^15): fp16 has no range of its
-// own to spare, and 2^-14 / 2^15 of the largest value is still a normal number.
+// 2^e with the largest |d| times it in [2^14, 2^15): fp16 has no range of its
+// own to spare, and 2^-28 of the largest value is still a normal number.
 __device__ __forceinline__ float range_scale(unsigned bits) {
   const int e = (int)(bits >> 23) - 127;
   if (bits == 0 || e > 126) return 1.f;
   return __int_as_float((min(14 - e, 126) + 127) << 23);
 }
 
+__device__ __forceinline__ void launched_early() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ float load1(const T* p) { return Storage<T>::load1(p); }
 
-// 32 results of a row, `n` of them inside, times `scale` plus `add`'s.
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// 32 results of a row, times `scale` plus `add`'s, in 16- or 32-byte stores.
 template <typename T>
-__device__ __forceinline__ void store_row(T* out, const T* add, const float (&v)[32], int n,
-                                          float scale) {
+__device__ __forceinline__ void store_row(T* out, const T* add, const float (&v)[32], float scale) {
   constexpr int kVec = Storage<T>::kVec;
-  if (n >= 32 && ((uintptr_t)out & 15) == 0) {
 #pragma unroll
-    for (int i = 0; i < 32; i += kVec) {
-      float f[kVec];
+  for (int i = 0; i < 32; i += 2 * kVec) {
+    float f[2 * kVec];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f[j] = v[i + j] * scale;
-      if (add) {
+    for (int j = 0; j < 2 * kVec; ++j) f[j] = v[i + j] * scale;
+    if (add) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) f[j] += load1(add + i + j);
-      }
-      *reinterpret_cast<uint4*>(out + i) = Storage<T>::pack(f);
+      for (int j = 0; j < 2 * kVec; ++j) f[j] += load1(add + i + j);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) Storage<T>::store1(out + i, v[i] * scale + (add ? load1(add + i) : 0.f));
+    const uint4 a = Storage<T>::pack(f), b = Storage<T>::pack(f + kVec);
+    if (((uintptr_t)out & 31) == 0) {
+      store32(out + i, a, b);
+    } else {
+      *reinterpret_cast<uint4*>(out + i) = a;
+      *reinterpret_cast<uint4*>(out + i + kVec) = b;
+    }
   }
 }
 
-// ---- results of a tile: thread t has one row, `tm` its accumulators
-template <int kEpi>
+// Where the rows of a warp's results start, in elements (-1: no row), and half
+// of the results on their turn.
+struct Turn {
+  int64_t at[32], add_at[32];
+  float v[16 * kTurn];
+};
+
+// A warp's 32 x 32 results, a row a lane, column `c` of the row on, `n` columns
+// of them inside.  Rows that 16-byte stores cannot take (or the last columns)
+// are turned, so that a store of the warp covers adjacent elements of one row:
+// a lane's own row would be 32 stores of single elements in 32 places each.
+template <typename T>
+__device__ __forceinline__ void store_tile(T* out, const T* add, int c, const float (&v)[32], int n,
+                                           float scale, Turn& turn) {
+  const int lane = threadIdx.x & 31;
+  const int64_t at = turn.at[lane];
+  const bool whole = at < 0 || ((uintptr_t)(out + at + c) & 15) == 0;
+  if (n >= 32 && __all_sync(~0u, whole)) {
+    if (at >= 0) store_row(out + at + c, add ? add + turn.add_at[lane] + c : nullptr, v, scale);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 32; h += 16) {
+    __syncwarp();
+    if (lane >= h && lane < h + 16) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) turn.v[(lane - h) * kTurn + i] = v[i] * scale;
+    }
+    __syncwarp();
+#pragma unroll 8
+    for (int r = 0; r < 16; ++r) {
+      const int64_t to = turn.at[h + r];
+      float x = turn.v[r * kTurn + lane];
+      if (to >= 0 && lane < n) {
+        if (add) x += load1(add + turn.add_at[h + r] + c + lane);
+        Storage<T>::store1(out + to + c + lane, x);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// `n` records into one: their largest maximum first, then one scaled sum.
+template <int n>
+__device__ __forceinline__ float4 join(const float4 (&x)[n], float s2) {
+  float m = x[0].x;
+#pragma unroll
+  for (int i = 1; i < n; ++i) m = fmaxf(m, x[i].x);
+  float4 y = make_float4(m, 0.f, 0.f, 0.f);
+  // (nothing above -inf in any: Z is 0 in all, or NaN)
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const float u = fmaxf((x[i].x - ref) * s2, -1000.f), k = exp2f(u);
+    y.y += x[i].y * k;
+    y.z += k * fmaf(x[i].y, u, x[i].z);
+  }
+  return y;
+}
+
+// The record of a row from the two warps that have its columns (at < 0: none).
+// `pair` takes turns between two places: the barrier of the next record lies
+// between a read and the write that follows it.
+__device__ __forceinline__ void record(const Product& g, const Stats& st, float4* pair, int side,
+                                       int64_t at) {
+  const int row = threadIdx.x & 127;
+  float4 x[2] = {make_float4(st.m, st.Z, st.D, 0.f)};
+  if (side == 1) pair[row] = x[0];
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+  if (side == 1) return;
+  x[1] = pair[row];
+  if (at >= 0) g.part[at] = join(x, g.s2);
+}
+
+// ---- results of a tile: a thread has one row, `tm` its accumulators; two
+// warps share 32 rows and take blocks of 32 columns in turn
+template <int kCg, int kEpi>
 __device__ __forceinline__ void results(const Product& g, const Tile& t, int rank, int count,
-                                        uint32_t tm, bool have, bool failed) {
+                                        uint32_t tm, bool have, bool failed, Stats& st, Turn& turn,
+                                        float4* pair) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const int side = (int)(threadIdx.x >> 5) / 4 - 1;
   const int r = t.m0 + rank * kRows + quad * 32 + lane;
   const float bad = __int_as_float(0x7FFFFFFF);
   auto load = [&](int c, float (&v)[32]) {
@@ -126,6 +224,15 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     if (have) {
       tmem_ld32(tm + c, v);
       tmem_wait(v);
+      if constexpr (kCg == 1 && kEpi == kStats) {
+        for (int j = 1; j < g.kc; ++j) {
+          float w[32];
+          tmem_ld32(tm + j * g.slot + c, w);
+          tmem_wait(w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += w[i];
+        }
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = failed ? bad : 0.f;
@@ -139,17 +246,20 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
       const int64_t id = g.actions[g.idx ? g.idx[r] : r] - t.n0;
       a = id >= 0 && id < n ? (int)id : -1;
     }
-    float m = -INFINITY, Z = 0.f, D = 0.f, xa = 0.f;
-    for (int c = 0; c < n; c += 32) {
+    float m = st.m, Z = st.Z, D = st.D, xa = 0.f;
+    for (int c = 32 * side; c < n; c += 64) {
       float v[32];
       load(c, v);
       if (c + 32 > n) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = c + i < n ? v[i] : -INFINITY;
       }
-      float cm = v[0];
+      float x4[4];  // (four chains of each: their links take longer than their issue)
 #pragma unroll
-      for (int i = 1; i < 32; ++i) cm = fmaxf(cm, v[i]);
+      for (int i = 0; i < 4; ++i) x4[i] = fmaxf(v[i], v[i + 4]);
+#pragma unroll
+      for (int i = 8; i < 32; ++i) x4[i & 3] = fmaxf(x4[i & 3], v[i]);
+      const float cm = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
       if (cm > m) {
         const float u = fmaxf((m - cm) * g.s2, -1000.f);
         const float k = exp2f(u);
@@ -159,24 +269,26 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
       }
       // (a row of -inf so far: 2^-inf = 0 against any finite reference)
       const float ref = m == -INFINITY ? 0.f : m;
-      float z = 0.f, d = 0.f;
+      float z4[4] = {0.f, 0.f, 0.f, 0.f}, d4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float u = (v[i] - ref) * g.s2;
         const float e = ex2_fast(u);
-        z += e;
-        d = fmaf(e, fmaxf(u, -1000.f), d);
+        z4[i & 3] += e;
+        d4[i & 3] = fmaf(e, fmaxf(u, -1000.f), d4[i & 3]);
       }
-      Z += z;
-      D += d;
+      Z += (z4[0] + z4[1]) + (z4[2] + z4[3]);
+      D += (d4[0] + d4[1]) + (d4[2] + d4[3]);
       if (__any_sync(~0u, a >= c && a < c + 32)) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) xa = a == c + i ? v[i] : xa;
       }
     }
-    if (live) {
-      g.part[(int64_t)(t.n0 / g.bn) * g.rpad + r] = make_float4(m, Z, D, 0.f);
-      if (a >= 0) g.xa[r] = xa;
+    if (a >= 0 && (a >> 5 & 1) == side) g.xa[r] = xa;
+    st = Stats{m, Z, D};
+    if (!g.run) {
+      record(g, st, pair, side, live ? (int64_t)(t.n0 / g.bn) * g.rpad + r : -1);
+      st = Stats{-INFINITY, 0.f, 0.f};
     }
   } else if constexpr (kEpi == kGrad) {
     const int n = min(g.bn, g.vp - t.n0);
@@ -187,7 +299,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float c0 = -q.y * scale, c1 = -q.z * scale;
     const int planes = g.pairs == 1 ? 1 : 3;
     __nv_bfloat16* row = g.d + (int64_t)r * g.ldd + t.n0;
-    for (int c = 0; c < g.bn; c += 32) {
+    for (int c = 32 * side; c < g.bn; c += 64) {
       float v[32];
       load(c, v);
 #pragma unroll
@@ -199,28 +311,24 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += a == c + i ? q.w * scale : 0.f;
       }
+      // rows and columns behind the last ones are read by the products to come
+      if (!live || c + 32 > n || failed) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = live && c + i < n ? (failed ? bad : v[i]) : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = live && c + i < n ? (failed ? bad : v[i]) : 0.f;
+      }
       if (g.fmt == 0) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          float f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = v[i + j];
-          *reinterpret_cast<uint4*>(row + c + i) = Storage<__half>::pack(f);
-        }
+        for (int i = 0; i < 32; i += 16)
+          store32(row + c + i, Storage<__half>::pack(v + i), Storage<__half>::pack(v + i + 8));
       } else {
         for (int p = 0; p < planes; ++p) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float f[8];
+          for (int i = 0; i < 32; i += 16)
+            store32(row + (int64_t)p * g.rpad * g.ldd + c + i, Storage<__nv_bfloat16>::pack(v + i),
+                    Storage<__nv_bfloat16>::pack(v + i + 8));
+          if (planes > 1) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              f[j] = v[i + j];
-              v[i + j] -= __bfloat162float(__float2bfloat16_rn(f[j]));
-            }
-            *reinterpret_cast<uint4*>(row + (int64_t)p * g.rpad * g.ldd + c + i) =
-                Storage<__nv_bfloat16>::pack(f);
+            for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
           }
         }
       }
@@ -229,37 +337,40 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float scale = g.bound ? 1.f / range_scale(*g.bound) : 1.f;
     const int64_t dst = kEpi == kWeight ? (r < g.vp ? g.v0 + r : -1)
                                         : (r < count ? (g.idx ? g.idx[r] : r) : -1);
-    const int64_t at = kEpi == kWeight ? dst * g.ost : dst / g.T * g.osb + dst % g.T * g.ost;
-    for (int c = 0; c < g.bn && t.n0 + c < g.K; c += 32) {
+    __syncwarp();
+    turn.at[lane] = dst < 0           ? -1
+                    : kEpi == kWeight ? dst * g.ost + t.n0
+                                      : dst / g.T * g.osb + dst % g.T * g.ost + t.n0;
+    turn.add_at[lane] = kEpi == kWeight ? dst * g.asv + t.n0 : 0;
+    __syncwarp();
+    for (int c = 32 * side; c < g.bn && t.n0 + c < g.K; c += 64) {
       const int n = min(32, g.K - t.n0 - c);
       float v[32];
       load(c, v);
-      if (dst < 0) continue;
       if constexpr (kEpi == kHidden) {
         if (g.acc) {
-          float* acc = g.acc + ((int64_t)t.split * g.rpad + r) * g.K + t.n0 + c;
-          if (g.acc_old) {
+          // (the last columns are padding; rows without a source have no sums)
+          float* acc = g.acc + ((int64_t)t.split * g.rpad + r) * g.ldacc + t.n0 + c;
+          if (g.acc_old && dst >= 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n) v[i] += acc[i];
+            for (int i = 0; i < 32; i += 4) {
+              const float4 o = *reinterpret_cast<const float4*>(acc + i);
+              v[i] += o.x, v[i + 1] += o.y, v[i + 2] += o.z, v[i + 3] += o.w;
+            }
           }
           if (g.acc_new) {
-            store_row<float>(acc, nullptr, v, n, 1.f);
+            if (dst >= 0) store_row<float>(acc, nullptr, v, 1.f);
             continue;
           }
         }
       }
-      const int64_t o = at + t.n0 + c;
-      const int64_t ao = kEpi == kWeight ? dst * g.asv + t.n0 + c : 0;
-      const bool plus = kEpi == kWeight && g.add;
+      const void* add = kEpi == kWeight ? g.add : nullptr;
       if (g.odt == GRPO_F32)
-        store_row<float>((float*)g.out + o, plus ? (const float*)g.add + ao : nullptr, v, n, scale);
+        store_tile((float*)g.out, (const float*)add, c, v, n, scale, turn);
       else if (g.odt == GRPO_BF16)
-        store_row<__nv_bfloat16>((__nv_bfloat16*)g.out + o,
-                                 plus ? (const __nv_bfloat16*)g.add + ao : nullptr, v, n, scale);
+        store_tile((__nv_bfloat16*)g.out, (const __nv_bfloat16*)add, c, v, n, scale, turn);
       else
-        store_row<__half>((__half*)g.out + o, plus ? (const __half*)g.add + ao : nullptr, v, n,
-                          scale);
+        store_tile((__half*)g.out, (const __half*)add, c, v, n, scale, turn);
     }
   }
 }
@@ -267,18 +378,21 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // The products.  A CTA (kCg 1: tiles of 128 rows) or a pair of CTAs (kCg 2:
 // 256 rows, each CTA holds half of either operand's tile) takes tiles in turn;
 // one thread asks for the operands' blocks, one issues the products into one
-// of two sets of accumulators, four warps turn the other into results.
+// of two sets of accumulators, eight warps turn the other into results.
 template <int kCg, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2];
   __shared__ uint32_t s_tmem;
+  __shared__ Turn s_turn[kEpi == kHidden || kEpi == kWeight ? 8 : 1];
+  __shared__ float4 s_pair[2][kEpi == kStats ? kRows : 1];
   constexpr bool kAmn = kEpi == kWeight, kBmn = kEpi == kWeight || kEpi == kHidden;
+  constexpr bool kSets = kCg == 1 && kEpi == kStats;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kCg == 2 ? cluster_rank() : 0u;
   const int half = g.bn / kCg;  // columns of B in this CTA
-  const uint32_t a_bytes = kRows * 128u, b_bytes = (uint32_t)half * 128u;
+  const uint32_t a_bytes = (uint32_t)g.a_rows * 128u, b_bytes = (uint32_t)half * 128u;
   const uint32_t stage_bytes = a_bytes + ((b_bytes + 1023u) & ~1023u);
 
   if (threadIdx.x == 0) {
@@ -290,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_done[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), 4 * kCg);
+      mbar_init(smem_u32(&s_free[i]), 8 * kCg);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -300,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   if (kCg == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = s_tmem;
+  launched_early();
 
   const int count = g.count ? *g.count : g.rows;
   const int rows = kEpi == kWeight ? g.vp : count;
@@ -325,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     return x;
   };
+  const bool two = !kSets || g.bufs == 2;  // tiles in flight
   const int first = blockIdx.x / kCg, step = gridDim.x / kCg;
   bool ok = true;
 
@@ -378,18 +494,27 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const Tile t = tile(i);
       const int n = (t.k1 - t.k0) * g.pairs;
       if (n == 0) continue;
-      const int buf = it & 1;
-      if (!(ok = mbar_wait(smem_u32(&s_free[buf]), ((it >> 1) & 1) ^ 1u))) break;
+      const int buf = two ? it & 1 : 0;
+      if (!(ok = mbar_wait(smem_u32(&s_free[buf]), ((two ? it >> 1 : it) & 1) ^ 1u))) break;
       fence_after();
-      const uint32_t d = tmem + (uint32_t)buf * 256u;
+      uint32_t d = tmem + (uint32_t)buf * 256u;
+      int next = kSets ? n / g.kc : 0, set = 0;  // (the first block of the next set)
+      bool add = false;
       for (int k = 0; k < n; ++k) {
+        if (kSets && k == next && set + 1 < g.kc) {
+          ++set;
+          next = n * (set + 1) / g.kc;
+          d += (uint32_t)g.slot;
+          add = false;
+        }
         if (!(ok = mbar_wait(smem_u32(&s_full[st]), ph))) break;
         fence_after();
         const uint32_t sa = smem + st * stage_bytes;
         const uint64_t da = operand(sa, kAmn), db = operand(sa + a_bytes, kBmn);
 #pragma unroll
         for (int j = 0; j < kBlk / 16; ++j)
-          mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, (k | j) != 0);
+          mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, add || j != 0);
+        add = true;
         commit<kCg>(smem_u32(&s_empty[st]));
         if (++st == g.stages) st = 0, ph ^= 1u;
       }
@@ -399,15 +524,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp >= 4) {
     // ---- results
     int it = 0;
+    Stats st{-INFINITY, 0.f, 0.f};
+    Turn& turn = s_turn[kEpi == kHidden || kEpi == kWeight ? warp - 4 : 0];
     for (int i = first; i < total; i += step) {
       const Tile t = tile(i);
-      const int buf = it & 1;
+      const int buf = two ? it & 1 : 0;
       const bool some = (t.k1 - t.k0) * g.pairs > 0;
-      if (some && ok) ok = mbar_wait(smem_u32(&s_done[buf]), (it >> 1) & 1);
+      if (some && ok) ok = mbar_wait(smem_u32(&s_done[buf]), (two ? it >> 1 : it) & 1);
       ok = __all_sync(~0u, ok);
       fence_after();
-      results<kEpi>(g, t, (int)rank, count,
-                    tmem + (uint32_t)buf * 256u + ((uint32_t)(warp & 3) << 21), some && ok, !ok);
+      results<kCg, kEpi>(g, t, (int)rank, count,
+                         tmem + (uint32_t)buf * 256u + ((uint32_t)(warp & 3) << 21), some && ok,
+                         !ok, st, turn, s_pair[it & 1]);
       fence_before();
       __syncwarp();
       if (lane == 0 && some && ok) {
@@ -415,6 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         mbar_arrive_cluster(kCg == 2 ? map_to(bar, 0) : bar);
       }
       it += some;
+    }
+    if (kEpi == kStats && g.run) {
+      const int r = (warp & 3) * 32 + lane;
+      record(g, st, s_pair[0], warp >= 8, r < count ? (int64_t)blockIdx.x * g.rpad + r : -1);
     }
   }
   if (!ok && g.status) atomicOr(g.status, (unsigned)GRPO_ERR_TIMEOUT);
@@ -431,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // itself, so no CTA waits for another.
 static constexpr int kPrepRows = 1024;
 
-struct Header {  // the first 256 bytes of the workspace, zeroed by the call
+struct Header {  // the first 256 bytes of the workspace
   int count;
-  unsigned bound;  // largest |d| of any row, as bits
+  unsigned bound;  // of |d| over all rows, as bits
 };
 
 struct PrepRows {
@@ -449,7 +581,6 @@ struct PrepRows {
   int* idx;
   float4* coef;  // nullable: the forward pass
   int* target;
-  int rpad;
   Header* h;
   unsigned* status;
   float *logps, *out_entropy, *out_stats;  // of the tokens that take no part
@@ -462,11 +593,22 @@ __device__ __forceinline__ bool takes_part(const PrepRows& a, int r) {
 }
 
 __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
-  __shared__ int s_sum[33];
+  __shared__ int s_sum[32];
+  __shared__ unsigned s_max[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int base = blockIdx.x * kPrepRows, r = base + (int)threadIdx.x;
+  launched_early();
+  // the tokens before this CTA's (the last one meets them all: it has the bound too)
   int before = 0;
-  for (int i = threadIdx.x; i < base; i += 1024) before += takes_part(a, i);
+  float wm = 0.f, hm = 0.f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < base; i += 1024) {
+    const bool m = !a.mask || a.mask[i];
+    const float w = a.dlogp ? a.dlogp[i] : 0.f, h = a.dent ? a.dent[i] : 0.f;
+    const bool on = m && (!a.coef || !(w == 0.f) || !(h == 0.f));
+    before += on;
+    if (on) wm = fmaxf(wm, fabsf(w)), hm = fmaxf(hm, fabsf(h));
+  }
   before = __reduce_add_sync(~0u, before);
   if (lane == 0) s_sum[warp] = before;
   __syncthreads();
@@ -480,11 +622,10 @@ __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
   mine = __reduce_add_sync(~0u, lane < warp ? all : 0);
   all = __reduce_add_sync(~0u, all);
   const int at = before + mine + __popc(votes & ((1u << lane) - 1u));
-  float big = 0.f;
   if (on) {
     a.idx[at] = r;
     if (a.coef) {
-      const float m = a.stats[r], Z = a.stats[a.N + r];
+      const float m = a.stats[r], Z = a.stats[(int64_t)a.N + r];
       const float w = a.dlogp ? a.dlogp[r] : 0.f, h = a.dent ? a.dent[r] : 0.f;
       const float lnZ = logf(Z);
       float c0 = a.s / Z * (w + (a.dent ? h * (a.entropy[r] - lnZ) : 0.f));
@@ -500,20 +641,25 @@ __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
       }
       a.coef[at] = make_float4(m, c0, 0.6931471805599453f * (a.s / Z) * h, a.s * w);
       a.target[at] = t;
-      // |p (log p + H)| <= max(1 / e, ln V)
-      big = a.s * (fabsf(w) + fabsf(h) * (0.37f + logf((float)a.V)));
+      wm = fmaxf(wm, fabsf(w)), hm = fmaxf(hm, fabsf(h));
     }
   } else if (r < a.N) {
     if (a.logps) a.logps[r] = 0.f;
     if (a.out_entropy) a.out_entropy[r] = 0.f;
-    if (a.out_stats) a.out_stats[r] = 0.f, a.out_stats[a.N + r] = 1.f;
+    if (a.out_stats) a.out_stats[r] = 0.f, a.out_stats[(int64_t)a.N + r] = 1.f;
   }
+  if (blockIdx.x != gridDim.x - 1) return;
   if (a.coef) {
-    // (bits order as the values do; a NaN leaves the scale at 1)
-    const unsigned top = __reduce_max_sync(~0u, __float_as_uint(big) & 0x7FFFFFFFu);
-    if (lane == 0 && top) atomicMax(&a.h->bound, top);
+    // |d| <= s (|dlogp| + |dH| max(1 / e, ln V)); the largest of either give a
+    // bound of all (bits order as the values do)
+    const float w = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(wm)));
+    const float h = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(hm)));
+    if (lane == 0) s_max[warp] = __float_as_uint(a.s * (w + h * (0.37f + logf((float)a.V))));
+    __syncthreads();
+    const unsigned top = __reduce_max_sync(~0u, s_max[lane]);
+    if (threadIdx.x == 0) a.h->bound = top;
   }
-  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) a.h->count = before + all;
+  if (threadIdx.x == 0) a.h->count = before + all;
 }
 
 // Rows into the layout of the tile loads: [planes][rows][Kp], zeros behind
@@ -529,11 +675,11 @@ struct PackRows {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(const PackRows a) {
+__device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step) {
   const int count = a.count ? *a.count : a.rows;
   const int end = (count + kPad - 1) / kPad * kPad;
   const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
+  for (int r = first; r < end; r += step) {
     const bool live = r < count;
     const int64_t from = live ? (a.idx ? a.idx[r] : r) : 0;
     const T* src = (const T*)a.src + from / a.T * a.sb + from % a.T * a.st;
@@ -579,6 +725,15 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackRows a) {
   }
 }
 
+// The hidden states' rows by the first CTAs, the weight's by the others.
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const PackRows h, const PackRows w, int ctas) {
+  launched_early();
+  const int warp = threadIdx.x >> 5, cta = blockIdx.x;
+  if (cta < ctas) pack_rows<T>(h, cta * 8 + warp, ctas * 8);
+  else pack_rows<T>(w, (cta - ctas) * 8 + warp, ((int)gridDim.x - ctas) * 8);
+}
+
 // The parts of each row joined: 32 rows a CTA, its warps take tiles in turn.
 struct FoldRows {
   const float4* part;
@@ -587,52 +742,59 @@ struct FoldRows {
   int rows, nt, rpad, N;
   const int* idx;
   const int64_t* actions;
+  const uint8_t* mask;  // of rows that were not chosen by it
   int64_t V;
   float s, s2;
   float *logps, *entropy, *stats;
   unsigned* status;
 };
+static constexpr int kFoldWarps = 16, kFoldAhead = 4;
 
-__device__ __forceinline__ void join(float4& x, const float4& y, float s2) {
-  const float m = fmaxf(x.x, y.x);
-  if (m == -INFINITY) {  // nothing above -inf in either
-    x.y += y.y;
-    return;
-  }
-  const float ux = fmaxf((x.x - m) * s2, -1000.f), uy = fmaxf((y.x - m) * s2, -1000.f);
-  const float kx = exp2f(ux), ky = exp2f(uy);
-  x.z = kx * fmaf(x.y, ux, x.z) + ky * fmaf(y.y, uy, y.z);
-  x.y = x.y * kx + y.y * ky;
-  x.x = m;
-}
-
-__global__ void __launch_bounds__(256) fold_kernel(const FoldRows a) {
-  __shared__ float4 s_part[8][32];
+__global__ void __launch_bounds__(32 * kFoldWarps) fold_kernel(const FoldRows a) {
+  __shared__ float4 s_part[kFoldWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launched_early();
   const int count = a.count ? *a.count : a.rows;
   const int r = blockIdx.x * 32 + lane;
   if (blockIdx.x * 32 >= count) return;
-  float4 x = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  float4 x[kFoldAhead + 1];
+  x[0] = none;
   if (r < count)
-    for (int t = warp; t < a.nt; t += 8) join(x, a.part[(int64_t)t * a.rpad + r], a.s2);
-  s_part[warp][lane] = x;
+    for (int t = warp; t < a.nt; t += kFoldWarps * kFoldAhead) {
+#pragma unroll
+      for (int j = 0; j < kFoldAhead; ++j) {
+        const int u = t + j * kFoldWarps;
+        x[j + 1] = u < a.nt ? a.part[(int64_t)u * a.rpad + r] : none;
+      }
+      x[0] = join(x, a.s2);
+    }
+  s_part[warp][lane] = x[0];
   __syncthreads();
   if (warp != 0 || r >= count) return;
+  float4 y[kFoldWarps];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) join(x, s_part[w][lane], a.s2);
+  for (int w = 0; w < kFoldWarps; ++w) y[w] = s_part[w][lane];
+  const float4 z = join(y, a.s2);
   const int src = a.idx ? a.idx[r] : r;
+  if (a.mask && !a.mask[src]) {
+    if (a.logps) a.logps[src] = 0.f;
+    if (a.entropy) a.entropy[src] = 0.f;
+    if (a.stats) a.stats[src] = 0.f, a.stats[(int64_t)a.N + src] = 1.f;
+    return;
+  }
   // a row without a finite maximum (+inf, nothing above -inf) or with a NaN has no distribution
   const float bad = __int_as_float(0x7FFFFFFF);
-  const float Z = isfinite(x.x) ? x.y : bad;
+  const float Z = isfinite(z.x) ? z.y : bad;
   const float lnZ = logf(Z);
   if (a.logps) {
     const int64_t id = a.actions[src];
     const bool in = id >= 0 && id < a.V;
-    a.logps[src] = in ? fmaf(a.s, a.xa[r] - x.x, -lnZ) : bad;
+    a.logps[src] = in ? fmaf(a.s, a.xa[r] - z.x, -lnZ) : bad;
     if (!in && a.status) atomicOr(a.status, (unsigned)GRPO_ERR_ACTION_RANGE);
   }
-  if (a.entropy) a.entropy[src] = fmaf(-0.6931471805599453f, x.z / Z, lnZ);
-  if (a.stats) a.stats[src] = x.x, a.stats[a.N + src] = Z;
+  if (a.entropy) a.entropy[src] = fmaf(-0.6931471805599453f, z.z / Z, lnZ);
+  if (a.stats) a.stats[src] = z.x, a.stats[(int64_t)a.N + src] = Z;
 }
 
 // The parts of the reduction of dh joined (in their order), rows without a
@@ -640,7 +802,7 @@ __global__ void __launch_bounds__(256) fold_kernel(const FoldRows a) {
 struct HiddenRows {
   const float* acc;  // nullptr: only the rows without a gradient
   int splits, rpad, N;
-  int64_t K;
+  int64_t K, ldacc;
   PrepRows rows;     // which tokens take part
   const int* idx;
   const int* count;
@@ -652,12 +814,13 @@ struct HiddenRows {
 
 template <typename T>
 __global__ void __launch_bounds__(256) hidden_kernel(const HiddenRows a) {
-  // the first N blocks' worth of rows: tokens; then the packed rows
+  launched_early();
+  // first the tokens, then the packed rows
   const int count = *a.count;
-  const int total = a.N + (a.acc ? count : 0);
-  for (int j = blockIdx.x; j < total; j += gridDim.x) {
+  const int64_t total = (int64_t)a.N + (a.acc ? count : 0);
+  for (int64_t j = blockIdx.x; j < total; j += gridDim.x) {
     const bool packed = j >= a.N;
-    const int r = packed ? j - a.N : j;
+    const int r = (int)(packed ? j - a.N : j);
     if (!packed && (takes_part(a.rows, r) || (a.skip_masked && a.rows.mask && !a.rows.mask[r])))
       continue;
     const int64_t dst = packed ? a.idx[r] : r;
@@ -666,7 +829,7 @@ __global__ void __launch_bounds__(256) hidden_kernel(const HiddenRows a) {
     for (int64_t k = threadIdx.x; k < a.K; k += 256) {
       float v = 0.f;
       if (packed)
-        for (int i = 0; i < a.splits; ++i) v += a.acc[((int64_t)i * a.rpad + r) * a.K + k];
+        for (int i = 0; i < a.splits; ++i) v += a.acc[((int64_t)i * a.rpad + r) * a.ldacc + k];
       Storage<T>::store1(out + k, v * scale);
     }
   }
@@ -706,33 +869,48 @@ bool encode(CUtensorMap* m, const void* p, bool bf16, int64_t inner, int64_t out
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <typename... Args>
+cudaError_t launch(void (*k)(Args...), int64_t grid, unsigned block, int cluster, int smem,
+                   cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&c, k, args...);
+}
+
 template <int kCg, int kEpi>
 cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
   const int half = g.bn / kCg;
-  const int stage = kRows * 128 + ((half * 128 + 1023) & ~1023);
-  g.stages = std::min(kMaxStages, kSmemStages / stage);
-  const int smem = g.stages * stage + 1024;
+  const int stage = g.a_rows * 128 + ((half * 128 + 1023) & ~1023);
+  // what the accumulators take has to fit: 512 columns, 256 of each of two tiles
+  if (g.bn > 256 || (g.kc > 1 && g.bn > g.slot) || g.kc * g.slot > (g.bufs == 2 ? 256 : 512))
+    return cudaErrorInvalidValue;
+  // rows of A that are not loaded are read from what lies behind: room for the last stage's
+  const int more = (kRows - g.a_rows) * 128 + 1024;
+  const int fixed = kEpi == kStats ? 2 * kRows * 16
+                    : kEpi == kHidden || kEpi == kWeight ? (int)(8 * sizeof(Turn)) : 0;
+  g.stages = std::min(kMaxStages, (kSmem - fixed - more) / stage);
+  const int smem = g.stages * stage + more;
   auto* k = product_kernel<kCg, kEpi>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)(std::max(1, std::min(sms / kCg, tiles)) * kCg));
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCg;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, k, g);
+  return launch(k, std::max(1, std::min(sms / kCg, tiles)) * kCg, kThreads, kCg, smem, s, g);
 }
 
 template <int kEpi>
-cudaError_t launch_product(Product& g, int cg, int sms, int tiles, cudaStream_t s) {
-  return cg == 2 ? launch_product<2, kEpi>(g, sms, tiles, s)
-                 : launch_product<1, kEpi>(g, sms, tiles, s);
+cudaError_t launch_product(Product& g, int cg, int sms, int64_t tiles, cudaStream_t s) {
+  const int n = (int)std::min<int64_t>(tiles, 1 << 20);
+  return cg == 2 ? launch_product<2, kEpi>(g, sms, n, s) : launch_product<1, kEpi>(g, sms, n, s);
 }
 
 int sm_count() {
@@ -743,6 +921,7 @@ int sm_count() {
 }
 
 int64_t ceil_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool pack_weight(const void* w, grpo_dtype_t dt, int64_t V, int64_t sv) {
   return dt == GRPO_F32 || ((uintptr_t)w & 15) != 0 || (V > 1 && sv % 8 != 0);
@@ -750,19 +929,23 @@ bool pack_weight(const void* w, grpo_dtype_t dt, int64_t V, int64_t sv) {
 
 // What a call keeps in its workspace.
 struct Layout {
-  int64_t rpad, Kp, planes, nt, vc, splits, ldd;
+  bool direct;  // kStats: every row is taken, as it lies
+  int cg, bn;   // CTAs of a tile, its columns (of the vocabulary)
+  int kbn;      // columns of a tile of the width
+  int64_t rpad, Kp, planes, nt, vc, splits, ldd, ldacc;
   size_t idx, coef, target, xa, part, hidden, weight, d, acc, total;
 };
 
-static constexpr int kSmallTile = 64;                // columns of a tile where tiles are few
 static constexpr int64_t kPieceBytes = 512ll << 20;  // of the logits' gradient
 
 Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t V, int64_t sv,
               bool backward) {
   Layout l{};
+  const int sms = sm_count();
   l.rpad = ceil_to(std::max<int64_t>(N, 1), kPad);
   l.Kp = ceil_to(K, 64);
   l.planes = dt == GRPO_F32 ? 3 : 1;
+  l.cg = N > kRows ? 2 : 1;
   size_t o = 256;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -775,40 +958,50 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
   if (backward) {
     l.coef = take(16 * l.rpad);
     l.target = take(4 * l.rpad);
+    l.bn = l.cg == 2 ? 256 : V >= 2 * 128 * sms ? 128 : 64;
+    l.kbn = l.cg == 2 ? 256 : K > 64 ? 128 : 64;
     const int64_t whole = ceil_to(V, 256);
     const int64_t fit = std::max<int64_t>(kPieceBytes / (2 * l.planes * l.rpad) / 256 * 256, 2048);
-    const int64_t pieces = (whole + fit - 1) / fit;
-    l.vc = ceil_to((whole + pieces - 1) / pieces, 256);
+    const int64_t pieces = div_up(whole, fit);
+    l.vc = ceil_to(div_up(whole, pieces), 256);
     l.ldd = l.vc;
     l.d = take((size_t)(2 * l.planes * l.rpad * l.ldd));
-    const int64_t tiles = l.rpad / 256 * ((K + 255) / 256);
-    l.splits = std::max<int64_t>(1, std::min<int64_t>(76 / tiles, l.vc / 64 / 16));
-    if (l.splits > 1 || pieces > 1) l.acc = take((size_t)(4 * l.splits * l.rpad * K));
+    // parts of dh's reduction, at least eight blocks each: as few as keep the SMs busy
+    const int64_t units = sms / l.cg, tiles = div_up(N, kRows * l.cg) * div_up(K, l.kbn);
+    const int64_t most = std::min<int64_t>(64, l.vc / 64 * (l.planes == 3 ? 6 : 1) / 8);
+    double best = 0;
+    l.splits = 1;
+    for (int64_t n = 1; tiles > 0 && n <= std::max<int64_t>(1, std::min<int64_t>(most, 4 * units / tiles)); ++n) {
+      const double use = (double)(n * tiles) / (double)(div_up(n * tiles, units) * units);
+      if (use > best + 0.03) best = use, l.splits = n;
+    }
+    l.ldacc = ceil_to(K, 256);
+    if (l.splits > 1 || pieces > 1) l.acc = take((size_t)(4 * l.splits * l.rpad * l.ldacc));
   } else {
-    const int bn = N > kRows ? 256 : kSmallTile;
-    l.nt = (V + bn - 1) / bn;
+    l.direct = N <= kRows;
+    // one CTA: columns so that the SMs' shares of the vocabulary are even
+    const int64_t waves = div_up(V, (int64_t)sms * 256);
+    l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(256, ceil_to(div_up(V, sms * waves), 16));
+    l.nt = div_up(V, l.bn);
     l.xa = take(4 * l.rpad);
-    l.part = take((size_t)(16 * l.nt * l.rpad));
+    l.part = take((size_t)(16 * (l.direct ? std::min<int64_t>(l.nt, sms) : l.nt) * l.rpad));
   }
   l.total = o;
   return l;
 }
 
-// Rows of `a` (already counted) and the weight where tile loads can take them.
+// The rows that take part, and the weight where tile loads cannot take it as it lies.
 cudaError_t pack(const LinearArgs& a, grpo_dtype_t dt, const Layout& l, const int* idx,
-                 const int* count, int sms, cudaStream_t s) {
-  PackRows p{a.hidden, idx, count, (int)(a.B * a.T), std::max<int64_t>(a.T, 1), a.sb, a.st, a.K, l.Kp, l.rpad * l.Kp,
-             a.ws + l.hidden};
-  const int grid = (int)std::min<int64_t>(l.rpad / 8, sms * 8);
-  if (dt == GRPO_F32) pack_kernel<float><<<grid, 256, 0, s>>>(p);
-  else pack_kernel<__half><<<grid, 256, 0, s>>>(p);
-  if (pack_weight(a.weight, dt, a.V, a.sv)) {
-    PackRows w{a.weight, nullptr, nullptr, (int)a.V, 1, a.sv, 0, a.K, l.Kp,
-               ceil_to(a.V, kPad) * l.Kp, a.ws + l.weight};
-    if (dt == GRPO_F32) pack_kernel<float><<<sms * 8, 256, 0, s>>>(w);
-    else pack_kernel<__half><<<sms * 8, 256, 0, s>>>(w);
-  }
-  return cudaGetLastError();
+                 const int* count, bool rows, int sms, cudaStream_t s) {
+  const PackRows h{a.hidden, idx, count, (int)(a.B * a.T), std::max<int64_t>(a.T, 1), a.sb, a.st,
+                   a.K, l.Kp, l.rpad * l.Kp, a.ws + l.hidden};
+  const PackRows w{a.weight, nullptr, nullptr, (int)a.V, 1, a.sv, 0, a.K, l.Kp,
+                   ceil_to(a.V, kPad) * l.Kp, a.ws + l.weight};
+  const int hc = rows ? (int)std::min<int64_t>(l.rpad / 8, sms * 8) : 0;
+  const int wc = pack_weight(a.weight, dt, a.V, a.sv) ? (int)std::min<int64_t>(div_up(a.V, 8), sms * 8) : 0;
+  if (hc + wc == 0) return cudaSuccess;
+  auto* k = dt == GRPO_F32 ? pack_kernel<float> : pack_kernel<__half>;
+  return launch(k, hc + wc, 256, 1, 0, s, h, w, hc);
 }
 
 Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
@@ -817,6 +1010,10 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   g.K = (int)a.K;
   g.kb = (int)(l.Kp / 64);
   g.splits = 1;
+  g.a_rows = kRows;
+  g.kc = 1;
+  g.slot = 256;
+  g.bufs = 2;
   g.pairs = dt == GRPO_F32 ? 6 : 1;
   g.fmt = dt == GRPO_F16 ? 0 : 1;
   g.s = a.inv_t;
@@ -848,40 +1045,56 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   const int sms = sm_count();
   const Layout l = layout(a.weight, dt, N, a.K, a.V, a.sv, false);
   Header* h = (Header*)a.ws;
-  int* idx = (int*)(a.ws + l.idx);
+  int* idx = l.direct ? nullptr : (int*)(a.ws + l.idx);
+  const int* count = l.direct ? nullptr : &h->count;
   unsigned* status = a.hdr ? &a.hdr->status : nullptr;
-  cudaError_t e = cudaMemsetAsync(a.ws, 0, 256, s);
-  if (e != cudaSuccess) return e;
-  PrepRows p{};
-  p.mask = a.mask;
-  p.N = (int)N;
-  p.idx = idx;
-  p.rpad = (int)l.rpad;
-  p.h = h;
-  p.logps = a.logps;
-  p.out_entropy = a.entropy;
-  p.out_stats = a.stats;
-  rows_kernel<<<(unsigned)((N + kPrepRows - 1) / kPrepRows), 1024, 0, s>>>(p);
-  if ((e = pack(a, dt, l, idx, &h->count, sms, s)) != cudaSuccess) return e;
+  cudaError_t e;
+  if (!l.direct) {
+    PrepRows p{};
+    p.mask = a.mask;
+    p.N = (int)N;
+    p.idx = idx;
+    p.h = h;
+    p.logps = a.logps;
+    p.out_entropy = a.entropy;
+    p.out_stats = a.stats;
+    if ((e = launch(rows_kernel, div_up(N, kPrepRows), 1024, 1, 0, s, p)) != cudaSuccess) return e;
+  }
+  // rows that tile loads can take where they are
+  const int64_t apart = a.T == 1 ? a.sb : a.st;
+  const bool in_place = l.direct && dt != GRPO_F32 && ((uintptr_t)a.hidden & 15) == 0 &&
+                        (a.T == 1 || a.B == 1 || a.sb == a.T * a.st) &&
+                        (N == 1 || (apart % 8 == 0 && apart >= 8));
+  if ((e = pack(a, dt, l, idx, count, !in_place, sms, s)) != cudaSuccess) return e;
   Product g = base(a, dt, l);
-  g.count = &h->count;
+  g.count = count;
   g.idx = idx;
   g.actions = a.logps ? a.actions : nullptr;
   g.vp = (int)a.V;
   g.part = (float4*)(a.ws + l.part);
   g.xa = (float*)(a.ws + l.xa);
-  const int cg = N > kRows ? 2 : 1;
-  g.bn = cg == 2 ? 256 : kSmallTile;
+  g.bn = l.bn;
   g.nt = (int)l.nt;
-  if (!encode(&g.a, a.ws + l.hidden, dt != GRPO_F16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, kRows) ||
-      !encode_weight(&g.b, a, dt, l, g.bn / cg))
-    return cudaErrorUnknown;
-  const int64_t tiles = l.rpad / (kRows * cg) * g.nt;
-  if ((e = launch_product<kStats>(g, cg, sms, (int)std::min<int64_t>(tiles, 1 << 20), s)) != cudaSuccess) return e;
-  FoldRows f{g.part, g.xa, g.count, g.rows, g.nt, g.rpad, (int)N, idx, a.actions, a.V, a.inv_t,
-             a.s2, a.logps, a.entropy, a.stats, status};
-  fold_kernel<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(f);
-  return cudaGetLastError();
+  if (l.direct) {
+    g.run = 1;
+    g.a_rows = (int)ceil_to(N, 8);
+    // two sums of half of the products each: an accumulator is rounded towards
+    // zero at every step, and the memory for the second is free here
+    g.kc = std::min(2, g.kb * g.pairs);
+    g.bufs = g.kc == 1 ? 2 : 1;
+  }
+  const bool mapped =
+      in_place ? encode(&g.a, a.hidden, dt != GRPO_F16, a.K, N, 1, N == 1 ? ceil_to(a.K, 8) : apart,
+                        0, g.a_rows)
+               : encode(&g.a, a.ws + l.hidden, dt != GRPO_F16, l.Kp, l.rpad, l.planes, l.Kp,
+                        l.rpad * l.Kp, g.a_rows);
+  if (!mapped || !encode_weight(&g.b, a, dt, l, g.bn / l.cg)) return cudaErrorUnknown;
+  const int64_t tiles = div_up(N, kRows * l.cg) * g.nt;
+  if ((e = launch_product<kStats>(g, l.cg, sms, tiles, s)) != cudaSuccess) return e;
+  const FoldRows f{g.part, g.xa, count, g.rows, l.direct ? (int)std::min<int64_t>(sms, tiles) : g.nt,
+                   g.rpad, (int)N, idx, a.actions, l.direct ? a.mask : nullptr, a.V, a.inv_t, a.s2,
+                   a.logps, a.entropy, a.stats, status};
+  return launch(fold_kernel, div_up(N, 32), 32 * kFoldWarps, 1, 0, s, f);
 }
 
 cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_t s) {
@@ -890,9 +1103,6 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
   const Layout l = layout(a.weight, dt, N, a.K, a.V, a.sv, true);
   Header* h = (Header*)a.ws;
   int* idx = (int*)(a.ws + l.idx);
-  unsigned* status = a.hdr ? &a.hdr->status : nullptr;
-  cudaError_t e = cudaMemsetAsync(a.ws, 0, 256, s);
-  if (e != cudaSuccess) return e;
   PrepRows p{};
   p.actions = a.actions;
   p.mask = a.mask;
@@ -906,16 +1116,17 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
   p.idx = idx;
   p.coef = (float4*)(a.ws + l.coef);
   p.target = (int*)(a.ws + l.target);
-  p.rpad = (int)l.rpad;
   p.h = h;
-  p.status = status;
-  if (N > 0) rows_kernel<<<(unsigned)((N + kPrepRows - 1) / kPrepRows), 1024, 0, s>>>(p);
-  if ((e = pack(a, dt, l, idx, &h->count, sms, s)) != cudaSuccess) return e;
+  p.status = a.hdr ? &a.hdr->status : nullptr;
+  cudaError_t e = N > 0 ? launch(rows_kernel, div_up(N, kPrepRows), 1024, 1, 0, s, p)
+                        : cudaMemsetAsync(h, 0, sizeof(Header), s);
+  if (e != cudaSuccess) return e;
+  if ((e = pack(a, dt, l, idx, &h->count, true, sms, s)) != cudaSuccess) return e;
   const bool bf16 = dt != GRPO_F16;
   const unsigned* bound = dt == GRPO_F16 ? &h->bound : nullptr;
-  const int cg = N > kRows ? 2 : 1;
-  const int mt = (int)(l.rpad / (kRows * cg));
-  auto count = [&](int64_t n) { return (int)std::min<int64_t>(n, 1 << 20); };
+  const int cg = l.cg;
+  const int a_rows = cg == 2 ? kRows : (int)std::max<int64_t>(ceil_to(N, 8), 8);
+  const int64_t mt = div_up(N, kRows * cg);
   for (int64_t v0 = 0; v0 < a.V; v0 += l.vc) {
     const int vp = (int)std::min<int64_t>(l.vc, a.V - v0);
     Product g = base(a, dt, l);
@@ -928,12 +1139,13 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     g.d = (__nv_bfloat16*)(a.ws + l.d);
     g.ldd = l.ldd;
     g.bound = bound;
-    g.bn = cg == 2 ? 256 : kSmallTile;
+    g.bn = l.bn;
     g.nt = (vp + g.bn - 1) / g.bn;
-    if (!encode(&g.a, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, kRows) ||
+    g.a_rows = a_rows;
+    if (!encode(&g.a, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, a_rows) ||
         !encode_weight(&g.b, a, dt, l, g.bn / cg))
       return cudaErrorUnknown;
-    if ((e = launch_product<kGrad>(g, cg, sms, count((int64_t)mt * g.nt), s)) != cudaSuccess) return e;
+    if ((e = launch_product<kGrad>(g, cg, sms, mt * g.nt, s)) != cudaSuccess) return e;
     if (a.dweight) {
       Product w = g;
       w.out = a.dweight;
@@ -941,13 +1153,14 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
       w.odt = a.wdt;
       w.add = a.add;
       w.asv = a.asv;
-      w.bn = cg == 2 ? 256 : kSmallTile;
-      w.nt = (int)((a.K + w.bn - 1) / w.bn);
+      w.bn = l.kbn;
+      w.nt = (int)div_up(a.K, w.bn);
+      w.a_rows = kRows;
       if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
           !encode(&w.b, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, 64))
         return cudaErrorUnknown;
-      const int64_t tiles = (vp + kRows * cg - 1) / (kRows * cg) * (int64_t)w.nt;
-      if ((e = launch_product<kWeight>(w, cg, sms, count(tiles), s)) != cudaSuccess) return e;
+      if ((e = launch_product<kWeight>(w, cg, sms, div_up(vp, kRows * cg) * w.nt, s)) != cudaSuccess)
+        return e;
     }
     if (a.dhidden && N > 0) {
       Product w = g;
@@ -955,29 +1168,28 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
       w.osb = a.gsb;
       w.ost = a.gst;
       w.odt = dt;
-      w.bn = cg == 2 ? 256 : kSmallTile;
-      w.nt = (int)((a.K + w.bn - 1) / w.bn);
+      w.bn = l.kbn;
+      w.nt = (int)div_up(a.K, w.bn);
       w.kb = (vp + 63) / 64;
       w.splits = (int)l.splits;
       w.acc = l.acc ? (float*)(a.ws + l.acc) : nullptr;
+      w.ldacc = l.ldacc;
       w.acc_old = v0 > 0;
       w.acc_new = v0 + vp < a.V || l.splits > 1;
-      if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, kRows) ||
+      if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, a_rows) ||
           !encode_weight(&w.b, a, dt, l, 64))
         return cudaErrorUnknown;
-      if ((e = launch_product<kHidden>(w, cg, sms, count((int64_t)mt * w.nt * w.splits), s)) != cudaSuccess)
-        return e;
+      if ((e = launch_product<kHidden>(w, cg, sms, mt * w.nt * w.splits, s)) != cudaSuccess) return e;
     }
   }
-  if (a.dhidden && N > 0) {
-    HiddenRows r{l.splits > 1 ? (const float*)(a.ws + l.acc) : nullptr, (int)l.splits, (int)l.rpad,
-                 (int)N, a.K, p, idx, &h->count, bound, a.dhidden, a.T, a.gsb, a.gst, a.skip_masked};
-    const int grid = (int)std::min<int64_t>(2 * N, sms * 8);
-    if (dt == GRPO_F32) hidden_kernel<float><<<grid, 256, 0, s>>>(r);
-    else if (dt == GRPO_BF16) hidden_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(r);
-    else hidden_kernel<__half><<<grid, 256, 0, s>>>(r);
-  }
-  return cudaGetLastError();
+  if (!a.dhidden || N == 0) return cudaSuccess;
+  const HiddenRows r{l.splits > 1 ? (const float*)(a.ws + l.acc) : nullptr, (int)l.splits,
+                     (int)l.rpad, (int)N, a.K, l.ldacc, p, idx, &h->count, bound, a.dhidden,
+                     std::max<int64_t>(a.T, 1), a.gsb, a.gst, a.skip_masked};
+  auto* k = dt == GRPO_F32    ? hidden_kernel<float>
+            : dt == GRPO_BF16 ? hidden_kernel<__nv_bfloat16>
+                              : hidden_kernel<__half>;
+  return launch(k, std::min<int64_t>(2 * N, sms * 8), 256, 1, 0, s, r);
 }
 
 }  // namespace grpo
