@@ -761,7 +761,8 @@ extern "C" grpo_status_t grpo_embed_tokens(const void* weight, grpo_dtype_t dt, 
   if (dt != GRPO_F32 && dt != GRPO_BF16 && dt != GRPO_F16) return GRPO_ERR_DTYPE;
   grpo_status_t st = check_token_shape(B, T, K, stride_b, stride_t);
   if (st != GRPO_OK) return st;
-  if (!matrix_ok(V, K, stride_v) || B * T > kMaxRows || !rows_disjoint(B, T, K, stride_b, stride_t))
+  if (!matrix_ok(V, K, stride_v) || B * T > kMaxRows ||
+      B * T * ceil_div(K, 1024) >= 0x7FFFFFFF || !rows_disjoint(B, T, K, stride_b, stride_t))
     return GRPO_ERR_SHAPE;
   if (!isfinite(scale)) return GRPO_ERR_PARAM;
   if (B * T == 0) return GRPO_OK;
@@ -791,7 +792,7 @@ extern "C" grpo_status_t grpo_embed_tokens_grad(
   if (st != GRPO_OK) return st;
   const int64_t N = B * T;
   if (!matrix_ok(V, K, out_stride_v) || N > kMaxRows ||
-      ceil_div(N, 32) * ceil_div(K, 512) >= 0x7FFFFFFF)
+      ceil_div(N, 32) * ceil_div(K, 128) + ceil_div(V, 16) >= 0x7FFFFFFF)
     return GRPO_ERR_SHAPE;
   if (add && (!matrix_ok(V, K, add_stride_v) ||
               (add == grad_weight && V > 1 && add_stride_v != out_stride_v)))

@@ -14,15 +14,26 @@
 namespace grpo {
 namespace {
 
-// `n` (at most a 16-byte vector's) elements of a row as floats, zeros behind them
+__device__ __forceinline__ void launched_early() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// `n` (at most a 16-byte vector's) elements of a row as they lie, zeros behind them
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, int n, float* f) {
+__device__ __forceinline__ uint4 load_vec(const T* p, int n) {
   constexpr int kVec = Storage<T>::kVec;
-  if (n >= kVec && ((uintptr_t)p & 15) == 0) {
-    Storage<T>::unpack(__ldg(reinterpret_cast<const uint4*>(p)), f);
+  if (n >= kVec && ((uintptr_t)p & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+  if constexpr (kVec == 4) {
+    const unsigned* q = reinterpret_cast<const unsigned*>(p);
+    return make_uint4(n > 0 ? __ldg(q) : 0u, n > 1 ? __ldg(q + 1) : 0u, n > 2 ? __ldg(q + 2) : 0u,
+                      n > 3 ? __ldg(q + 3) : 0u);
   } else {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+    unsigned h[8];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] = i < n ? Storage<T>::load1(p + i) : 0.f;
+    for (int i = 0; i < 8; ++i) h[i] = i < n ? __ldg(q + i) : 0u;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
 }
 // kVec floats, `n` of them inside, to a row of O
@@ -40,28 +51,48 @@ __device__ __forceinline__ void store_vec(O* p, int n, const float* f) {
   }
 }
 
-// A thread takes a vector of a row, a CTA up to 256 of them.
-template <typename T>
+// A thread takes a vector of `kPer` rows one behind the other, a CTA up to 256
+// vectors of them: the rows' loads are in flight together.
+template <typename T, int kPer>
 __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int slices) {
   constexpr int kVec = Storage<T>::kVec;
-  for (int64_t j = blockIdx.x; j < a.N * slices; j += gridDim.x) {
-    const int64_t r = j / slices, k = ((j - r * slices) * 256 + threadIdx.x) * kVec;
-    const bool on = !a.mask || a.mask[r];
-    const int64_t id = on ? a.ids[r] : -1;
-    const bool in = id >= 0 && id < a.V;
-    if (on && !in && a.hdr && k == 0) atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
-    if (k >= a.K) continue;
-    const int n = (int)min((int64_t)kVec, a.K - k);
-    float f[kVec];
-    if (in) {
-      load_vec((const T*)a.weight + id * a.sv + k, n, f);
+  launched_early();
+  const unsigned part = blockIdx.x / (unsigned)slices;
+  const int64_t first = (int64_t)part * kPer;
+  const int64_t k = ((int64_t)(blockIdx.x - part * slices) * 256 + threadIdx.x) * kVec;
+  const int n = (int)min((int64_t)kVec, a.K - k);
+  if (n <= 0) return;
+  // the first row's (b, t): the others follow it
+  int64_t b = 0, t = first;
+  if (a.T < a.N) {
+    b = (unsigned)first / (unsigned)a.T;
+    t = first - b * a.T;
+  }
+  int64_t id[kPer];  // -1: masked, -2: outside the vocabulary
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) f[i] *= a.scale;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) f[i] = on ? __int_as_float(0x7FFFFFFF) : 0.f;
+  for (int j = 0; j < kPer; ++j) {
+    const int64_t r = first + j;
+    const bool on = r < a.N && (!a.mask || a.mask[r]);
+    id[j] = on ? a.ids[r] : -1;
+    if (on && (id[j] < 0 || id[j] >= a.V)) {
+      id[j] = -2;
+      if (a.hdr && k == 0) atomicOr(&a.hdr->status, (unsigned)GRPO_ERR_ACTION_RANGE);
     }
-    store_vec<T, kVec>((T*)a.out + r / a.T * a.sb + r % a.T * a.st + k, n, f);
+  }
+  uint4 v[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    v[j] = id[j] >= 0 ? load_vec((const T*)a.weight + id[j] * a.sv + k, n) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (first + j >= a.N) break;
+    float f[kVec];
+    Storage<T>::unpack(v[j], f);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      f[i] = id[j] == -2 ? __int_as_float(0x7FFFFFFF) : id[j] < 0 ? 0.f : f[i] * a.scale;
+    store_vec<T, kVec>((T*)a.out + b * a.sb + t * a.st + k, n, f);
+    if (++t == a.T) t = 0, ++b;
   }
 }
 
@@ -69,8 +100,9 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int slice
 // Stable sort of (id, token) by id, least significant digits first; tokens
 // that take no part get the id V and end behind the others.  A CTA takes a
 // chunk, each of its warps a part of that in order.
-static constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
+static constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 static constexpr int kMaxDigit = 9;
+static_assert(1 << kMaxDigit <= kSortThreads, "a thread has one digit");
 
 struct SortArgs {
   const int64_t* ids;  // first pass: nullptr afterwards
@@ -78,77 +110,98 @@ struct SortArgs {
   int64_t V;
   const int2* in;
   int2* out;
-  int* hist;  // [digits][chunks]
+  int* hist;  // [chunks][digits]
   unsigned char* taken;  // [V]: ids that occur
   unsigned* status;
   int N, chunk, chunks, shift, bits;
 };
 
-__device__ __forceinline__ int2 sort_key(const SortArgs& a, int i, bool first) {
-  if (!a.ids) return a.in[i];
-  int64_t id = a.V;
-  if (!a.mask || a.mask[i]) {
-    id = a.ids[i];
-    if (id < 0 || id >= a.V) {
-      id = a.V;
-      if (first && a.status) atomicOr(a.status, (unsigned)GRPO_ERR_ACTION_RANGE);
-    } else if (first) {
-      a.taken[id] = 1;
-    }
+// the id that a token is sorted by: V where it takes no part
+__device__ __forceinline__ int sort_id(const SortArgs& a, bool on, int64_t id, bool first) {
+  if (!on) return (int)a.V;
+  if (id < 0 || id >= a.V) {
+    if (first && a.status) atomicOr(a.status, (unsigned)GRPO_ERR_ACTION_RANGE);
+    return (int)a.V;
   }
-  return make_int2((int)id, i);
+  if (first) a.taken[id] = 1;
+  return (int)id;
+}
+// the (id, token) of four rounds of a warp from i on (what is behind `end`: id -1)
+__device__ __forceinline__ void sort_keys(const SortArgs& a, int i, int end, bool first,
+                                          int2 (&key)[4]) {
+  if (!a.ids) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) key[j] = i + 32 * j < end ? a.in[i + 32 * j] : make_int2(-1, 0);
+    return;
+  }
+  int64_t id[4];
+  bool on[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool in = i + 32 * j < end;
+    id[j] = in ? a.ids[i + 32 * j] : 0;
+    on[j] = in && (!a.mask || a.mask[i + 32 * j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    key[j] = i + 32 * j < end ? make_int2(sort_id(a, on[j], id[j], first), i + 32 * j)
+                              : make_int2(-1, 0);
 }
 
 // counts of a chunk's digits, of each warp's part of it
 __device__ __forceinline__ void count_digits(const SortArgs& a, int (*s)[1 << kMaxDigit],
                                              bool first) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, digits = 1 << a.bits;
-  for (int i = threadIdx.x; i < kSortWarps * digits; i += kSortThreads) s[i / digits][i % digits] = 0;
-  __syncthreads();
+  for (int i = threadIdx.x; i < kSortWarps << kMaxDigit; i += kSortThreads) (&s[0][0])[i] = 0;
   const int part = a.chunk / kSortWarps, from = blockIdx.x * a.chunk + warp * part;
-  for (int i = from + lane; i < min(from + part, a.N); i += 32)
-    atomicAdd(&s[warp][(sort_key(a, i, first).x >> a.shift) & (digits - 1)], 1);
+  const int end = min(from + part, a.N);
+  int2 key[4];
+  sort_keys(a, from + lane, end, first, key);
+  __syncthreads();
+  for (int i = from; i < end;) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (key[j].x >= 0) atomicAdd(&s[warp][(key[j].x >> a.shift) & (digits - 1)], 1);
+    if ((i += 128) < end) sort_keys(a, i + lane, end, first, key);
+  }
   __syncthreads();
 }
 
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const SortArgs a) {
   __shared__ int s[kSortWarps][1 << kMaxDigit];
+  launched_early();
   count_digits(a, s, true);
-  for (int d = threadIdx.x; d < 1 << a.bits; d += kSortThreads) {
-    int n = 0;
+  const int d = threadIdx.x, digits = 1 << a.bits;
+  if (d >= digits) return;
+  int n = 0;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) n += s[w][d];
-    a.hist[d * a.chunks + blockIdx.x] = n;
-  }
+  for (int w = 0; w < kSortWarps; ++w) n += s[w][d];
+  a.hist[blockIdx.x * digits + d] = n;
 }
 
 __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
   __shared__ int s[kSortWarps][1 << kMaxDigit];
-  __shared__ int s_base[1 << kMaxDigit], s_before[1 << kMaxDigit], s_sum[kSortWarps];
+  __shared__ int s_sum[kSortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, digits = 1 << a.bits;
-  count_digits(a, s, false);
-  // a digit's place: all of smaller digits, its own of earlier chunks
-  for (int d = warp; d < digits; d += kSortWarps) {
-    int all = 0, before = 0;
-    for (int c = lane; c < a.chunks; c += 32) {
-      const int n = a.hist[d * a.chunks + c];
-      all += n;
-      before += c < (int)blockIdx.x ? n : 0;
-    }
-    all = __reduce_add_sync(~0u, all);
-    before = __reduce_add_sync(~0u, before);
-    if (lane == 0) s_base[d] = all, s_before[d] = before;
-  }
-  __syncthreads();
-  // exclusive sums of the digits' totals: two digits a thread
-  int v[2], sum = 0;
+  launched_early();
+  count_digits(a, s, a.chunks == 1);
+  // a digit's place: all of smaller digits, its own of earlier chunks, of earlier warps
+  const int d = threadIdx.x;
+  int all = 0, before = 0;
+  if (d < digits) {
+    if (a.chunks == 1) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int d = threadIdx.x * 2 + j;
-    v[j] = d < digits ? s_base[d] : 0;
-    sum += v[j];
+      for (int w = 0; w < kSortWarps; ++w) all += s[w][d];
+    } else {
+#pragma unroll 16
+      for (int c = 0; c < a.chunks; ++c) {
+        const int n = a.hist[c * digits + d];
+        all += n;
+        before += c < (int)blockIdx.x ? n : 0;
+      }
+    }
   }
-  int inc = sum;
+  int inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(~0u, inc, o);
@@ -156,17 +209,9 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
   }
   if (lane == 31) s_sum[warp] = inc;
   __syncthreads();
-  int base = inc - sum;
-  for (int w = 0; w < warp; ++w) base += s_sum[w];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int d = threadIdx.x * 2 + j;
-    if (d < digits) s_base[d] = base;
-    base += v[j];
-  }
-  __syncthreads();
-  for (int d = threadIdx.x; d < digits; d += kSortThreads) {
-    int at = s_base[d] + s_before[d];
+  int at = inc - all + before;
+  for (int w = 0; w < warp; ++w) at += s_sum[w];
+  if (d < digits) {
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
       const int n = s[w][d];
@@ -177,21 +222,24 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
   __syncthreads();
   const int part = a.chunk / kSortWarps, from = blockIdx.x * a.chunk + warp * part;
   const int end = min(from + part, a.N);
-  for (int i0 = from; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    const bool in = i < end;
-    const int2 key = in ? sort_key(a, i, false) : make_int2(0, 0);
-    const int d = in ? (key.x >> a.shift) & (digits - 1) : -1;
-    const unsigned same = __match_any_sync(~0u, d);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int at = 0;
-    if (in) at = s[warp][d];
-    __syncwarp();
-    if (in) {
-      a.out[at + rank] = key;
-      if (rank == 0) s[warp][d] = at + __popc(same);
+  for (int i = from; i < end; i += 128) {
+    int2 key[4];
+    sort_keys(a, i + lane, end, false, key);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = key[j].x >= 0;
+      const int digit = in ? (key[j].x >> a.shift) & (digits - 1) : -1;
+      const unsigned same = __match_any_sync(~0u, digit);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      int to = 0;
+      if (in) to = s[warp][digit];
+      __syncwarp();
+      if (in) {
+        a.out[to + rank] = key[j];
+        if (rank == 0) s[warp][digit] = to + __popc(same);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -199,7 +247,8 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
 // A CTA adds up a chunk of the sorted tokens, its threads a vector of columns
 // each.  An id whose tokens lie in one chunk is done; the parts of one that
 // goes on to other chunks are joined by join_kernel in the chunks' order.
-static constexpr int kSumThreads = 128, kSumChunk = 32;
+// Behind those CTAs come the ones that fill the rows of absent ids.
+static constexpr int kSumThreads = 128, kSumChunk = 32, kAbsentRows = 16;
 
 struct SumArgs {
   const void* grad;
@@ -214,6 +263,7 @@ struct SumArgs {
   int64_t so;
   float* parts;  // [chunks][2][K]: of the id that came from before, of the id that goes on
   const unsigned char* taken;
+  int slices, sums;  // of columns; CTAs that add up
 };
 
 template <typename T, typename O>
@@ -228,15 +278,41 @@ __device__ __forceinline__ void finish(const SumArgs& a, int64_t id, int64_t k, 
   store_vec<O, kVec>(out, n, f);
 }
 
+// Rows of ids that no token has: zero, or what is added to.
+template <typename O>
+__device__ __forceinline__ void absent_rows(const SumArgs& a, int64_t first) {
+  constexpr int kVec = Storage<O>::kVec;
+  const int64_t end = min(first + kAbsentRows, a.V);
+  for (int64_t v = first; v < end; ++v) {
+    if (a.taken[v]) continue;
+    for (int64_t k = (int64_t)threadIdx.x * kVec; k < a.K; k += kSumThreads * kVec) {
+      const int n = (int)min((int64_t)kVec, a.K - k);
+      float f[kVec];
+      Storage<O>::unpack(a.add ? load_vec((const O*)a.add + v * a.sa + k, n) : make_uint4(0, 0, 0, 0), f);
+      store_vec<O, kVec>((O*)a.out + v * a.so + k, n, f);
+    }
+  }
+}
+
 template <typename T, typename O>
-__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a, int slices) {
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   constexpr int kVec = Storage<T>::kVec;
-  __shared__ int2 s_tok[kSumChunk + 2];
-  const int c = blockIdx.x / slices, slice = blockIdx.x - c * slices;
+  __shared__ int s_id[kSumChunk + 2];
+  __shared__ const T* s_row[kSumChunk];
+  launched_early();
+  if ((int)blockIdx.x >= a.sums) {
+    absent_rows<O>(a, (int64_t)(blockIdx.x - a.sums) * kAbsentRows);
+    return;
+  }
+  const int c = blockIdx.x / a.slices, slice = blockIdx.x - c * a.slices;
   const int from = c * kSumChunk, n = min(kSumChunk, a.N - from);
   if (threadIdx.x < kSumChunk + 2) {
-    const int i = from + (int)threadIdx.x - 1;
-    s_tok[threadIdx.x] = i >= 0 && i < a.N ? a.sorted[i] : make_int2(-1, 0);
+    const int j = (int)threadIdx.x - 1, i = from + j;
+    const int2 x = i >= 0 && i < a.N ? a.sorted[i] : make_int2(-1, 0);
+    s_id[threadIdx.x] = x.x;
+    // (no row: id V, and what lies behind the chunk)
+    if (j >= 0 && j < kSumChunk)
+      s_row[j] = j < n && x.x < a.V ? (const T*)a.grad + x.y / a.T * a.sb + x.y % a.T * a.st : nullptr;
   }
   __syncthreads();
   const int64_t k = ((int64_t)slice * kSumThreads + threadIdx.x) * kVec;
@@ -247,31 +323,31 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a, int s
   for (int i = 0; i < kVec; ++i) f[i] = 0.f;
   int begin = 0;
   constexpr int kAhead = 8;
+  static_assert(kSumChunk % kAhead == 0, "whole groups");
   for (int j0 = 0; j0 < n; j0 += kAhead) {
-    float g[kAhead][kVec];
+    uint4 g[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int2 t = s_tok[1 + min(j0 + u, n - 1)];
-      if (t.x < a.V) load_vec((const T*)a.grad + t.y / a.T * a.sb + t.y % a.T * a.st + k, cols, g[u]);
+      const T* row = s_row[j0 + u];
+      if (row) g[u] = load_vec(row + k, cols);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
       if (j >= n) break;
-      const int id = s_tok[1 + j].x;
+      const int id = s_id[1 + j];
       if (id >= a.V) return;  // (the rest takes no part)
+      float h[kVec];
+      Storage<T>::unpack(g[u], h);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) f[i] += g[u][i];
-      if (j + 1 < n && s_tok[2 + j].x == id) continue;
-      const bool from_before = begin == 0 && s_tok[0].x == id;
-      const bool goes_on = j + 1 == n && s_tok[2 + j].x == id;
+      for (int i = 0; i < kVec; ++i) f[i] += h[i];
+      if (j + 1 < n && s_id[2 + j] == id) continue;
+      const bool from_before = begin == 0 && s_id[0] == id;
+      const bool goes_on = j + 1 == n && s_id[2 + j] == id;
       if (!from_before && !goes_on) {
         finish<T, O>(a, id, k, cols, f);
       } else {
-        float* p = a.parts + ((int64_t)c * 2 + (from_before ? 0 : 1)) * a.K + k;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          if (i < cols) p[i] = f[i];
+        store_vec<float, kVec>(a.parts + ((int64_t)c * 2 + (from_before ? 0 : 1)) * a.K + k, cols, f);
       }
 #pragma unroll
       for (int i = 0; i < kVec; ++i) f[i] = 0.f;
@@ -280,49 +356,70 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a, int s
   }
 }
 
+// Four warps take a quarter of the chunks each, a lane a vector of columns.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int slices) {
   constexpr int kVec = Storage<T>::kVec;
-  const int c = blockIdx.x / slices, slice = blockIdx.x - c * slices;
-  const int next = (c + 1) * kSumChunk;
+  __shared__ int s_end;
+  __shared__ float s_sum[kSumThreads / 32][32][kVec];
+  launched_early();
+  const unsigned part = blockIdx.x / (unsigned)slices;
+  const int c = part, slice = blockIdx.x - part * slices;
+  const int64_t next = (int64_t)(c + 1) * kSumChunk;
   if (next >= a.N) return;
-  const int id = a.sorted[next - 1].x;
   // only where the id goes on and did not come from before
-  if (id >= a.V || a.sorted[next].x != id) return;
-  if (c > 0 && a.sorted[c * kSumChunk - 1].x == id) return;
-  const int64_t k = ((int64_t)slice * kSumThreads + threadIdx.x) * kVec;
-  if (k >= a.K) return;
-  const int cols = (int)min((int64_t)kVec, a.K - k);
-  float f[kVec];
-  const float* p = a.parts + ((int64_t)c * 2 + 1) * a.K + k;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) f[i] = i < cols ? p[i] : 0.f;
-  for (int d = c + 1;; ++d) {
-    p = a.parts + (int64_t)d * 2 * a.K + k;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (i < cols) f[i] += p[i];
-    const int end = (d + 1) * kSumChunk;
-    if (end >= a.N || a.sorted[end].x != id) break;
-  }
-  finish<T, O>(a, id, k, cols, f);
-}
-
-// Rows of ids that no token has: zero, or what is added to.
-template <typename O>
-__global__ void __launch_bounds__(256) absent_kernel(const SumArgs a) {
-  constexpr int kVec = Storage<O>::kVec;
-  for (int64_t v = blockIdx.x; v < a.V; v += gridDim.x) {
-    if (a.taken[v]) continue;
-    for (int64_t k = (int64_t)threadIdx.x * kVec; k < a.K; k += 256 * kVec) {
-      const int n = (int)min((int64_t)kVec, a.K - k);
-      float f[kVec];
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) f[i] = 0.f;
-      if (a.add) load_vec((const O*)a.add + v * a.sa + k, n, f);
-      store_vec<O, kVec>((O*)a.out + v * a.so + k, n, f);
+  const int id = a.sorted[next - 1].x, after = a.sorted[next].x;
+  const int first = c > 0 ? a.sorted[next - kSumChunk - 1].x : -1;
+  if (id >= a.V || after != id || first == id) return;
+  // the chunk in which it ends: the first whose successor starts with another id
+  int last = c + 1;
+  for (;; last += kSumThreads) {
+    const int64_t i = ((int64_t)last + threadIdx.x + 1) * kSumChunk;
+    const bool ends = i >= a.N || a.sorted[i].x != id;
+    if (threadIdx.x == 0) s_end = kSumThreads;
+    __syncthreads();
+    if (ends) atomicMin(&s_end, (int)threadIdx.x);
+    __syncthreads();
+    const int end = s_end;
+    __syncthreads();
+    if (end < kSumThreads) {
+      last += end;
+      break;
     }
   }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t k = ((int64_t)slice * 32 + lane) * kVec;
+  const int cols = (int)max((int64_t)0, min((int64_t)kVec, a.K - k));
+  // parts 0 (this chunk's) .. last - c, a quarter of them each, in order
+  const int64_t parts = last - c + 1, from = parts * warp / 4, to = parts * (warp + 1) / 4;
+  const bool whole = cols == kVec && (a.K & 3) == 0;
+  float f[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) f[i] = 0.f;
+#pragma unroll 4
+  for (int64_t d = from; d < to; ++d) {
+    const float* q = a.parts + ((c + d) * 2 + (d == 0)) * a.K + k;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kVec; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(q + i);
+        f[i] += v.x, f[i + 1] += v.y, f[i + 2] += v.z, f[i + 3] += v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (i < cols) f[i] += q[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) s_sum[warp][lane][i] = f[i];
+  __syncthreads();
+  if (warp != 0 || cols == 0) return;
+#pragma unroll
+  for (int w = 1; w < kSumThreads / 32; ++w)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] += s_sum[w][lane][i];
+  finish<T, O>(a, id, k, cols, f);
 }
 
 struct Layout {
@@ -337,7 +434,7 @@ Layout layout(int64_t N, int64_t K, int64_t V) {
   l.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   l.bits = (bits + l.passes - 1) / l.passes;
   // up to 256 chunks of at least 2,048 tokens
-  l.chunk = (int)(std::max<int64_t>(2048, (N + 255) / 256) + 255) / 256 * 256;
+  l.chunk = (int)((std::max<int64_t>(2048, (N + 255) / 256) + kSortThreads - 1) / kSortThreads * kSortThreads);
   l.chunks = (int)((N + l.chunk - 1) / l.chunk);
   l.sums = (int)((N + kSumChunk - 1) / kSumChunk);
   size_t o = 0;
@@ -355,16 +452,44 @@ Layout layout(int64_t N, int64_t K, int64_t V) {
   return l;
 }
 
+// A launch that may be set up while the one before it ends (its threads wait
+// for that before they touch memory).
+template <typename... Args>
+cudaError_t launch(void (*k)(Args...), int64_t grid, unsigned block, cudaStream_t s,
+                   const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3(block);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, args...);
+}
+
 template <typename T, typename O>
-cudaError_t sums(const SumArgs& a, const Layout& l, cudaStream_t s) {
-  if (a.N > 0) {
-    constexpr int kCols = kSumThreads * Storage<T>::kVec;
-    const int slices = (int)((a.K + kCols - 1) / kCols);
-    sum_kernel<T, O><<<(unsigned)(l.sums * slices), kSumThreads, 0, s>>>(a, slices);
-    join_kernel<T, O><<<(unsigned)(l.sums * slices), kSumThreads, 0, s>>>(a, slices);
-  }
-  if (a.add != a.out) absent_kernel<O><<<(unsigned)std::min<int64_t>(a.V, 152 * 16), 256, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t sums(SumArgs& a, const Layout& l, cudaStream_t s) {
+  constexpr int kCols = kSumThreads * Storage<T>::kVec, kJoin = 32 * Storage<T>::kVec;
+  a.slices = (int)((a.K + kCols - 1) / kCols);
+  a.sums = l.sums * a.slices;
+  const int joins = (int)((a.K + kJoin - 1) / kJoin);
+  const int64_t absent = a.add == a.out ? 0 : (a.V + kAbsentRows - 1) / kAbsentRows;
+  if (a.sums + absent == 0) return cudaSuccess;
+  const cudaError_t e = launch(sum_kernel<T, O>, a.sums + absent, kSumThreads, s, a);
+  if (e != cudaSuccess || l.sums < 2) return e;
+  return launch(join_kernel<T, O>, (int64_t)l.sums * joins, kSumThreads, s, a, joins);
+}
+
+template <typename T>
+cudaError_t embed(EmbedArgs a, cudaStream_t s) {
+  constexpr int kCols = 256 * Storage<T>::kVec;
+  const int slices = (int)((a.K + kCols - 1) / kCols);
+  if (a.sb == a.T * a.st) a.T = a.N;  // rows evenly apart
+  // rows together where there are enough of them for every SM
+  if (a.N * slices >= 152 * 16) return launch(embed_kernel<T, 4>, (a.N + 3) / 4 * slices, 256, s, a, slices);
+  return launch(embed_kernel<T, 1>, a.N * slices, 256, s, a, slices);
 }
 
 }  // namespace
@@ -372,13 +497,9 @@ cudaError_t sums(const SumArgs& a, const Layout& l, cudaStream_t s) {
 size_t embed_ws(int64_t N, int64_t K, int64_t V) { return layout(N, K, V).total; }
 
 cudaError_t launch_embed(const EmbedArgs& a, grpo_dtype_t dt, cudaStream_t s) {
-  const int vec = dt == GRPO_F32 ? 4 : 8;
-  const int slices = (int)((a.K + 256 * vec - 1) / (256 * vec));
-  const unsigned grid = (unsigned)std::min<int64_t>(a.N * slices, 152 * 32);
-  if (dt == GRPO_F32) embed_kernel<float><<<grid, 256, 0, s>>>(a, slices);
-  else if (dt == GRPO_BF16) embed_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, slices);
-  else embed_kernel<__half><<<grid, 256, 0, s>>>(a, slices);
-  return cudaGetLastError();
+  return dt == GRPO_F32    ? embed<float>(a, s)
+         : dt == GRPO_BF16 ? embed<__nv_bfloat16>(a, s)
+                           : embed<__half>(a, s);
 }
 
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, grpo_dtype_t dt, cudaStream_t s) {
@@ -392,13 +513,14 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, grpo_dtype_t dt, cudaStrea
   for (int i = 0; i < l.passes && a.N > 0; ++i) {
     p.out = keys[i & 1];
     p.shift = i * l.bits;
-    count_kernel<<<l.chunks, kSortThreads, 0, s>>>(p);
-    place_kernel<<<l.chunks, kSortThreads, 0, s>>>(p);
+    // (a single chunk's counts stay in its CTA)
+    if (l.chunks > 1 && (e = launch(count_kernel, l.chunks, kSortThreads, s, p)) != cudaSuccess) return e;
+    if ((e = launch(place_kernel, l.chunks, kSortThreads, s, p)) != cudaSuccess) return e;
     p.ids = nullptr;
     p.in = p.out;
   }
-  SumArgs g{a.grad, a.K, a.sb, a.st, a.V, (int)a.N, (int)std::max<int64_t>(a.T, 1), p.in, a.scale, a.add, a.sa, a.out, a.so,
-            (float*)(a.ws + l.parts), taken};
+  SumArgs g{a.grad, a.K, a.sb, a.st, a.V, (int)a.N, (int)std::max<int64_t>(a.T, 1), p.in, a.scale,
+            a.add, a.sa, a.out, a.so, (float*)(a.ws + l.parts), taken, 0, 0};
   if (dt == GRPO_F32) return sums<float, float>(g, l, s);
   if (dt == GRPO_BF16)
     return a.odt == GRPO_F32 ? sums<__nv_bfloat16, float>(g, l, s)
