@@ -49,6 +49,7 @@ struct Product {
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
   int kc;         // kStats, kCg 1: sets of accumulators that the reduction is cut into, in order
   int slot, bufs; // columns of a set; tiles that are in flight, 1 or 2
+  int want_entropy; // kStats: D is wanted; kGrad: c1 is not 0
   int run;        // kStats: one record of a CTA's tiles, which are of the same rows
   int stages, mb; // tiles of rows that are taken together
   uint32_t fmt;
@@ -105,6 +106,68 @@ __device__ __forceinline__ void launched_early() {
 
 template <typename T>
 __device__ __forceinline__ float load1(const T* p) { return Storage<T>::load1(p); }
+
+// Two fp32 operations in one instruction: a warp of results has less to issue
+// beside the thread that feeds the tensor cores.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// the largest / smallest of 32, NaN left out
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = max3(v[i], v[i + 4], v[i + 8]);
+#pragma unroll
+  for (int i = 12; i < 28; i += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = max3(m[j], v[i + j], v[i + j + 4]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = fmaxf(m[j], v[28 + j]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+__device__ __forceinline__ float min32(const float (&v)[32]) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = min3(v[i], v[i + 4], v[i + 8]);
+#pragma unroll
+  for (int i = 12; i < 28; i += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = min3(m[j], v[i + j], v[i + j + 4]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = fminf(m[j], v[28 + j]);
+  return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
+}
 
 __device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
@@ -201,7 +264,9 @@ __device__ __forceinline__ float4 join(const float4 (&x)[n], float s2) {
 __device__ __forceinline__ void record(const Product& g, const Stats& st, float4* pair, int side,
                                        int64_t at) {
   const int row = threadIdx.x & 127;
-  float4 x[2] = {make_float4(st.m, st.Z, st.D, 0.f)};
+  // (2^(x s2 - ref) = 2^((x - m) s2) 2^d)
+  const float d = fabsf(st.m) < INFINITY ? fmaf(st.m, g.s2, -(st.m * g.s2)) : 0.f, k = exp2f(-d);
+  float4 x[2] = {make_float4(st.m, st.Z * k, (st.D - d * st.Z) * k, 0.f)};
   if (side == 1) pair[row] = x[0];
   asm volatile("bar.sync 1, 256;" ::: "memory");
   if (side == 1) return;
@@ -246,7 +311,10 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
       const int64_t id = g.actions[g.idx ? g.idx[r] : r] - t.n0;
       a = id >= 0 && id < n ? (int)id : -1;
     }
+    // sums of 2^u and 2^u u, u = x s2 - ref, against ref = fl(m s2), and what that
+    // rounded off is put right in the record; 0 while there is no finite m
     float m = st.m, Z = st.Z, D = st.D, xa = 0.f;
+    float ref = m == -INFINITY ? 0.f : m * g.s2;
     for (int c = 32 * side; c < n; c += 64) {
       float v[32];
       load(c, v);
@@ -254,31 +322,39 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = c + i < n ? v[i] : -INFINITY;
       }
-      float x4[4];  // (four chains of each: their links take longer than their issue)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x4[i] = fmaxf(v[i], v[i + 4]);
-#pragma unroll
-      for (int i = 8; i < 32; ++i) x4[i & 3] = fmaxf(x4[i & 3], v[i]);
-      const float cm = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
+      const float cm = max32(v);
       if (cm > m) {
-        const float u = fmaxf((m - cm) * g.s2, -1000.f);
+        const float to = cm * g.s2, u = fmaxf(ref - to, -1000.f);
         const float k = exp2f(u);
-        D = k * (D + Z * u);
+        D = k * fmaf(Z, u, D);
         Z *= k;
         m = cm;
+        ref = to;
       }
-      // (a row of -inf so far: 2^-inf = 0 against any finite reference)
-      const float ref = m == -INFINITY ? 0.f : m;
-      float z4[4] = {0.f, 0.f, 0.f, 0.f}, d4[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-ref, -ref);
+      float2 z2[2], d2[2];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float u = (v[i] - ref) * g.s2;
-        const float e = ex2_fast(u);
-        z4[i & 3] += e;
-        d4[i & 3] = fmaf(e, fmaxf(u, -1000.f), d4[i & 3]);
+      for (int i = 0; i < 2; ++i) z2[i] = d2[i] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 u = fma2(make_float2(v[i], v[i + 1]), s2, r2);
+        const float2 e = make_float2(ex2_fast(u.x), ex2_fast(u.y));
+        z2[i / 2 & 1] = add2(z2[i / 2 & 1], e);
+        if (g.want_entropy) d2[i / 2 & 1] = fma2(e, u, d2[i / 2 & 1]);
       }
-      Z += (z4[0] + z4[1]) + (z4[2] + z4[3]);
-      D += (d4[0] + d4[1]) + (d4[2] + d4[3]);
+      z2[0] = add2(z2[0], z2[1]);
+      d2[0] = add2(d2[0], d2[1]);
+      float d = d2[0].x + d2[0].y;
+      if (!(fabsf(d) < INFINITY)) {  // (a logit of -inf: its term is 0, not 0 x inf)
+        d = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float u = fmaf(v[i], g.s2, -ref);
+          d = fmaf(ex2_fast(u), fmaxf(u, -1000.f), d);
+        }
+      }
+      Z += z2[0].x + z2[0].y;
+      D += d;
       if (__any_sync(~0u, a >= c && a < c + 32)) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) xa = a == c + i ? v[i] : xa;
@@ -296,16 +372,29 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float4 q = live ? g.coef[r] : make_float4(0.f, 0.f, 0.f, 0.f);
     const int a = live ? g.target[r] - g.v0 - t.n0 : -1;
     const float scale = g.bound ? range_scale(*g.bound) : 1.f;
-    const float c0 = -q.y * scale, c1 = -q.z * scale;
+    // 2^(x s2 - ref) (c0 + c1 (x s2 - ref)) with ref = fl(m s2), as in the sums
+    const float ref = q.x * g.s2, off = fmaf(q.x, g.s2, -ref), k = -exp2f(-off) * scale;
+    const float c0 = k * fmaf(-off, q.z, q.y), c1 = k * q.z;
+    const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-ref, -ref);
+    const float2 c02 = make_float2(c0, c0), c12 = make_float2(c1, c1);
     const int planes = g.pairs == 1 ? 1 : 3;
     __nv_bfloat16* row = g.d + (int64_t)r * g.ldd + t.n0;
     for (int c = 32 * side; c < g.bn; c += 64) {
       float v[32];
       load(c, v);
+      // (far below the others, -inf among them: 0, not 0 x inf)
+      const bool low = g.want_entropy && !(min32(v) * g.s2 > -1e20f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float u = fmaxf((v[i] - q.x) * g.s2, -1000.f);
-        v[i] = ex2_fast(u) * fmaf(c1, u, c0);
+      for (int i = 0; i < 32; i += 2) {
+        float2 u = fma2(make_float2(v[i], v[i + 1]), s2, r2);
+        float2 w = make_float2(ex2_fast(u.x), ex2_fast(u.y));
+        if (g.want_entropy) {
+          if (low) u = make_float2(fmaxf(u.x, -1000.f), fmaxf(u.y, -1000.f));
+          w = mul2(w, fma2(c12, u, c02));
+        } else {
+          w = mul2(w, c02);
+        }
+        v[i] = w.x, v[i + 1] = w.y;
       }
       if (__any_sync(~0u, a >= c && a < c + 32)) {
 #pragma unroll
@@ -1073,6 +1162,7 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   g.vp = (int)a.V;
   g.part = (float4*)(a.ws + l.part);
   g.xa = (float*)(a.ws + l.xa);
+  g.want_entropy = a.entropy != nullptr;
   g.bn = l.bn;
   g.nt = (int)l.nt;
   if (l.direct) {
@@ -1136,6 +1226,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     g.vp = vp;
     g.coef = p.coef;
     g.target = p.target;
+    g.want_entropy = a.dent != nullptr;
     g.d = (__nv_bfloat16*)(a.ws + l.d);
     g.ldd = l.ldd;
     g.bound = bound;
