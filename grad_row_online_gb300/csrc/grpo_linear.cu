@@ -33,7 +33,7 @@ static constexpr int kBlk = 64;       // elements of the reduction a stage holds
 static constexpr int kRows = 128;     // rows of a CTA's tile (lanes of tensor memory)
 static constexpr int kPad = 256;      // packed rows are padded to the rows of a pair's tile
 static constexpr int kMaxStages = 12;
-static constexpr int kSmem = 226 * 1024;  // of a CTA's 227 KB
+static constexpr int kSmem = 227 * 1024 - 320;  // of a CTA's, beside the barriers
 static constexpr int kTurn = 33;          // words of a row in the results' 16 x 32 turn
 
 struct Product {
@@ -227,14 +227,23 @@ __device__ __forceinline__ void store_tile(T* out, const T* add, int c, const fl
       for (int i = 0; i < 32; ++i) turn.v[(lane - h) * kTurn + i] = v[i] * scale;
     }
     __syncwarp();
-#pragma unroll 8
-    for (int r = 0; r < 16; ++r) {
-      const int64_t to = turn.at[h + r];
-      float x = turn.v[r * kTurn + lane];
-      if (to >= 0 && lane < n) {
-        if (add) x += load1(add + turn.add_at[h + r] + c + lane);
-        Storage<T>::store1(out + to + c + lane, x);
+#pragma unroll
+    for (int q = 0; q < 16; q += 8) {  // (eight rows' reads in flight together)
+      int64_t to[8];
+      float x[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        to[r] = lane < n ? turn.at[h + q + r] : -1;
+        x[r] = turn.v[(q + r) * kTurn + lane];
       }
+      if (add) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (to[r] >= 0) x[r] += load1(add + turn.add_at[h + q + r] + c + lane);
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (to[r] >= 0) Storage<T>::store1(out + to[r] + c + lane, x[r]);
     }
   }
   __syncwarp();
@@ -259,19 +268,33 @@ __device__ __forceinline__ float4 join(const float4 (&x)[n], float s2) {
 }
 
 // The record of a row from the two warps that have its columns (at < 0: none).
-// `pair` takes turns between two places: the barrier of the next record lies
-// between a read and the write that follows it.
-__device__ __forceinline__ void record(const Product& g, const Stats& st, float4* pair, int side,
+__device__ __forceinline__ void record(const Product& g, const Stats& st, Stats* pair, int side,
                                        int64_t at) {
   const int row = threadIdx.x & 127;
   // (2^(x s2 - ref) = 2^((x - m) s2) 2^d)
   const float d = fabsf(st.m) < INFINITY ? fmaf(st.m, g.s2, -(st.m * g.s2)) : 0.f, k = exp2f(-d);
   float4 x[2] = {make_float4(st.m, st.Z * k, (st.D - d * st.Z) * k, 0.f)};
-  if (side == 1) pair[row] = x[0];
+  asm volatile("bar.sync 1, 256;" ::: "memory");  // (the record before has been read)
+  if (side == 1) pair[row] = Stats{x[0].x, x[0].y, x[0].z};
   asm volatile("bar.sync 1, 256;" ::: "memory");
   if (side == 1) return;
-  x[1] = pair[row];
+  x[1] = make_float4(pair[row].m, pair[row].Z, pair[row].D, 0.f);
   if (at >= 0) g.part[at] = join(x, g.s2);
+}
+
+// What a thread needs of its row, read while the tile's products run.
+struct RowData {
+  int64_t id;  // the token, -1: none
+  float4 q;    // kGrad: the coefficients
+};
+template <int kEpi>
+__device__ __forceinline__ RowData row_data(const Product& g, const Tile& t, int rank, int count) {
+  RowData x{-1, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int r = t.m0 + rank * kRows + (threadIdx.x & 127);
+  if (r >= count) return x;
+  if (kEpi == kStats && g.actions) x.id = g.actions[g.idx ? g.idx[r] : r];
+  if (kEpi == kGrad) x.id = g.target[r], x.q = g.coef[r];
+  return x;
 }
 
 // ---- results of a tile: a thread has one row, `tm` its accumulators; two
@@ -279,7 +302,7 @@ __device__ __forceinline__ void record(const Product& g, const Stats& st, float4
 template <int kCg, int kEpi>
 __device__ __forceinline__ void results(const Product& g, const Tile& t, int rank, int count,
                                         uint32_t tm, bool have, bool failed, Stats& st, Turn& turn,
-                                        float4* pair) {
+                                        Stats* pair, const RowData& row) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int side = (int)(threadIdx.x >> 5) / 4 - 1;
   const int r = t.m0 + rank * kRows + quad * 32 + lane;
@@ -306,11 +329,8 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
   if constexpr (kEpi == kStats) {
     const int n = min(g.bn, g.vp - t.n0);
     const bool live = r < count;
-    int a = -1;
-    if (live && g.actions) {
-      const int64_t id = g.actions[g.idx ? g.idx[r] : r] - t.n0;
-      a = id >= 0 && id < n ? (int)id : -1;
-    }
+    const int64_t id = row.id - t.n0;
+    const int a = id >= 0 && id < n ? (int)id : -1;
     // sums of 2^u and 2^u u, u = x s2 - ref, against ref = fl(m s2), and what that
     // rounded off is put right in the record; 0 while there is no finite m
     float m = st.m, Z = st.Z, D = st.D, xa = 0.f;
@@ -369,8 +389,8 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
   } else if constexpr (kEpi == kGrad) {
     const int n = min(g.bn, g.vp - t.n0);
     const bool live = r < count;
-    const float4 q = live ? g.coef[r] : make_float4(0.f, 0.f, 0.f, 0.f);
-    const int a = live ? g.target[r] - g.v0 - t.n0 : -1;
+    const float4 q = row.q;
+    const int a = live ? (int)row.id - g.v0 - t.n0 : -1;
     const float scale = g.bound ? range_scale(*g.bound) : 1.f;
     // 2^(x s2 - ref) (c0 + c1 (x s2 - ref)) with ref = fl(m s2), as in the sums
     const float ref = q.x * g.s2, off = fmaf(q.x, g.s2, -ref), k = -exp2f(-off) * scale;
@@ -378,7 +398,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-ref, -ref);
     const float2 c02 = make_float2(c0, c0), c12 = make_float2(c1, c1);
     const int planes = g.pairs == 1 ? 1 : 3;
-    __nv_bfloat16* row = g.d + (int64_t)r * g.ldd + t.n0;
+    __nv_bfloat16* dst = g.d + (int64_t)r * g.ldd + t.n0;
     for (int c = 32 * side; c < g.bn; c += 64) {
       float v[32];
       load(c, v);
@@ -408,12 +428,12 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
       if (g.fmt == 0) {
 #pragma unroll
         for (int i = 0; i < 32; i += 16)
-          store32(row + c + i, Storage<__half>::pack(v + i), Storage<__half>::pack(v + i + 8));
+          store32(dst + c + i, Storage<__half>::pack(v + i), Storage<__half>::pack(v + i + 8));
       } else {
         for (int p = 0; p < planes; ++p) {
 #pragma unroll
           for (int i = 0; i < 32; i += 16)
-            store32(row + (int64_t)p * g.rpad * g.ldd + c + i, Storage<__nv_bfloat16>::pack(v + i),
+            store32(dst + (int64_t)p * g.rpad * g.ldd + c + i, Storage<__nv_bfloat16>::pack(v + i),
                     Storage<__nv_bfloat16>::pack(v + i + 8));
           if (planes > 1) {
 #pragma unroll
@@ -474,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2];
   __shared__ uint32_t s_tmem;
   __shared__ Turn s_turn[kEpi == kHidden || kEpi == kWeight ? 8 : 1];
-  __shared__ float4 s_pair[2][kEpi == kStats ? kRows : 1];
+  __shared__ Stats s_pair[kEpi == kStats ? kRows : 1];
   constexpr bool kAmn = kEpi == kWeight, kBmn = kEpi == kWeight || kEpi == kHidden;
   constexpr bool kSets = kCg == 1 && kEpi == kStats;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -507,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   const int count = g.count ? *g.count : g.rows;
   const int rows = kEpi == kWeight ? g.vp : count;
-  const int mt = (rows + kRows * kCg - 1) / (kRows * kCg);
+  constexpr int kTile = kRows * kCg;  // rows of a tile
+  const int mt = (rows + kTile - 1) / kTile;
   const int kb = kEpi == kWeight ? (count + kBlk - 1) / kBlk : g.kb;
   const int per = mt * g.nt;
   const int total = per * (kEpi == kHidden ? g.splits : 1);
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int u = t - x.split * per;
     const int blk = u / (g.mb * g.nt), left = u - blk * g.mb * g.nt;
     const int w = min(g.mb, mt - blk * g.mb);
-    x.m0 = (blk * g.mb + left % w) * kRows * kCg;
+    x.m0 = (blk * g.mb + left % w) * kTile;
     x.n0 = left / w * g.bn;
     x.k0 = 0;
     x.k1 = kb;
@@ -533,34 +554,38 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int first = blockIdx.x / kCg, step = gridDim.x / kCg;
   bool ok = true;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---- operands
+    const bool one = elect();
     int st = 0;
     uint32_t ph = 0;
     for (int i = first; i < total && ok; i += step) {
       const Tile t = tile(i);
+      const int m = t.m0 + (int)rank * kRows, n = t.n0 + (int)rank * half;
       for (int p = 0; p < g.pairs && ok; ++p) {
         const int za = g.pairs == 1 ? 0 : kPairs[p][0], zb = g.pairs == 1 ? 0 : kPairs[p][1];
         for (int k = t.k0; k < t.k1; ++k) {
-          if (!(ok = mbar_wait(smem_u32(&s_empty[st]), ph ^ 1u))) break;
+          if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
           uint32_t bar = smem_u32(&s_full[st]);
-          if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
-          if (kCg == 2) bar = map_to(bar, 0);
           const uint32_t sa = smem + st * stage_bytes, sb = sa + a_bytes;
-          const int m = t.m0 + (int)rank * kRows, n = t.n0 + (int)rank * half;
-          if (kAmn) {
-            for (int j = 0; j < kRows; j += 64)
-              tma_load<kCg>(sa + j * 128u, &g.a, m + j, k * kBlk, za, bar);
-          } else {
-            tma_load<kCg>(sa, &g.a, k * kBlk, m, za, bar);
+          const int y = (kEpi == kHidden ? g.v0 : 0) + k * kBlk;  // (of rows across the reduction)
+          if (one) {
+            if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
+            if (kCg == 2) bar = map_to(bar, 0);
+            if (kAmn) {
+              for (int j = 0; j < kRows; j += 64)
+                tma_load<kCg>(sa + j * 128u, &g.a, m + j, k * kBlk, za, bar);
+            } else {
+              tma_load<kCg>(sa, &g.a, k * kBlk, m, za, bar);
+            }
+            if (kBmn) {
+              for (int j = 0; j < half; j += 64)
+                tma_load<kCg>(sb + j * 128u, &g.b, n + j, y, zb, bar);
+            } else {
+              tma_load<kCg>(sb, &g.b, k * kBlk, g.v0 + n, zb, bar);
+            }
           }
-          if (kBmn) {
-            const int y = (kEpi == kHidden ? g.v0 : 0) + k * kBlk;
-            for (int j = 0; j < half; j += 64)
-              tma_load<kCg>(sb + j * 128u, &g.b, n + j, y, zb, bar);
-          } else {
-            tma_load<kCg>(sb, &g.b, k * kBlk, g.v0 + n, zb, bar);
-          }
+          __syncwarp();
           if (++st == g.stages) st = 0, ph ^= 1u;
         }
       }
@@ -569,11 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     // has been taken (or, after a wait that ran out, has at least arrived)
     // (a stage never asked for is in the phase that this wait takes as done)
     for (int i = 0; i < g.stages; ++i) {
-      if (!mbar_wait(ok ? smem_u32(&s_empty[st]) : smem_u32(&s_full[st]), ph ^ 1u)) break;
+      if (!mbar_wait_all(ok ? smem_u32(&s_empty[st]) : smem_u32(&s_full[st]), ph ^ 1u)) break;
       if (++st == g.stages) st = 0, ph ^= 1u;
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- products
+    const bool one = elect();
+    const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+    const uint64_t da0 = operand(smem, kAmn), db0 = operand(smem + a_bytes, kBmn);
     const uint32_t idesc = instruction(kRows * kCg, g.bn, g.fmt, kAmn, kBmn);
     constexpr uint32_t kStepA = kAmn ? 128u : 2u, kStepB = kBmn ? 128u : 2u;  // 16 elements, in 16 bytes
     int st = 0;
@@ -584,11 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const int n = (t.k1 - t.k0) * g.pairs;
       if (n == 0) continue;
       const int buf = two ? it & 1 : 0;
-      if (!(ok = mbar_wait(smem_u32(&s_free[buf]), ((two ? it >> 1 : it) & 1) ^ 1u))) break;
+      if (!(ok = mbar_wait_all(smem_u32(&s_free[buf]), ((two ? it >> 1 : it) & 1) ^ 1u))) break;
       fence_after();
       uint32_t d = tmem + (uint32_t)buf * 256u;
       int next = kSets ? n / g.kc : 0, set = 0;  // (the first block of the next set)
-      bool add = false;
+      bool add = false, here = false;            // (here: the next block has been seen to be there)
       for (int k = 0; k < n; ++k) {
         if (kSets && k == next && set + 1 < g.kc) {
           ++set;
@@ -596,18 +624,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           d += (uint32_t)g.slot;
           add = false;
         }
-        if (!(ok = mbar_wait(smem_u32(&s_full[st]), ph))) break;
-        fence_after();
-        const uint32_t sa = smem + st * stage_bytes;
-        const uint64_t da = operand(sa, kAmn), db = operand(sa + a_bytes, kBmn);
+        if (!here && !(ok = mbar_wait_all(full0 + 8u * st, ph))) break;
+        const uint64_t off = (uint64_t)((uint32_t)st * stage_bytes >> 4), da = da0 + off, db = db0 + off;
+        if (one) {
 #pragma unroll
-        for (int j = 0; j < kBlk / 16; ++j)
-          mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, add || j != 0);
+          for (int j = 0; j < kBlk / 16; ++j)
+            mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, add || j != 0);
+          commit<kCg>(empty0 + 8u * st);
+        }
+        __syncwarp();
         add = true;
-        commit<kCg>(smem_u32(&s_empty[st]));
         if (++st == g.stages) st = 0, ph ^= 1u;
+        here = k + 1 < n && __all_sync(~0u, mbar_try(full0 + 8u * st, ph));
       }
-      commit<kCg>(smem_u32(&s_done[buf]));
+      if (one) commit<kCg>(smem_u32(&s_done[buf]));
+      __syncwarp();
       ++it;
     }
   } else if (warp >= 4) {
@@ -619,12 +650,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const Tile t = tile(i);
       const int buf = two ? it & 1 : 0;
       const bool some = (t.k1 - t.k0) * g.pairs > 0;
-      if (some && ok) ok = mbar_wait(smem_u32(&s_done[buf]), (two ? it >> 1 : it) & 1);
-      ok = __all_sync(~0u, ok);
+      const RowData row = row_data<kEpi>(g, t, (int)rank, count);
+      if (some && ok) {
+        // (one lane asks: the others would take turns at it with the products' thread)
+        if (lane == 0) ok = mbar_wait(smem_u32(&s_done[buf]), (two ? it >> 1 : it) & 1);
+        ok = __all_sync(~0u, ok);
+      }
       fence_after();
       results<kCg, kEpi>(g, t, (int)rank, count,
                          tmem + (uint32_t)buf * 256u + ((uint32_t)(warp & 3) << 21), some && ok,
-                         !ok, st, turn, s_pair[it & 1]);
+                         !ok, st, turn, s_pair, row);
       fence_before();
       __syncwarp();
       if (lane == 0 && some && ok) {
@@ -635,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if (kEpi == kStats && g.run) {
       const int r = (warp & 3) * 32 + lane;
-      record(g, st, s_pair[0], warp >= 8, r < count ? (int64_t)blockIdx.x * g.rpad + r : -1);
+      record(g, st, s_pair, warp >= 8, r < count ? (int64_t)blockIdx.x * g.rpad + r : -1);
     }
   }
   if (!ok && g.status) atomicOr(g.status, (unsigned)GRPO_ERR_TIMEOUT);
@@ -763,6 +798,60 @@ struct PackRows {
   void* dst;
 };
 
+// A row of 16-bit elements that starts anywhere: a lane reads one aligned
+// vector, takes its neighbour's too and shifts the two together.  A vector
+// that is not wholly inside [begin, end) is put together from its elements.
+__device__ __forceinline__ void pack_shifted(const PackRows& a, const unsigned short* src, int64_t r,
+                                             uintptr_t begin, uintptr_t end) {
+  const int lane = threadIdx.x & 31;
+  const uintptr_t base = (uintptr_t)src & ~(uintptr_t)15, stop = (uintptr_t)(src + a.K);
+  const int skip = (int)((uintptr_t)src & 15) / 2;  // elements of the first vector before the row
+  auto fetch = [&](uintptr_t p) {
+    if (p >= begin && p + 16 <= end) return __ldg((const uint4*)p);
+    unsigned h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uintptr_t q = p + 2 * i;
+      h[i] = q >= (uintptr_t)src && q < stop ? __ldg((const unsigned short*)q) : 0u;
+    }
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  };
+  const int words = skip >> 1, odd = (skip & 1) * 16;
+  for (int64_t k0 = 0; k0 < a.Kp; k0 += 1024) {
+    uint4 x[4], after[4];  // (four vectors in flight; the last lane's neighbour too)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uintptr_t p = base + 2 * (k0 + j * 256 + lane * 8);
+      x[j] = p < stop ? fetch(p) : make_uint4(0, 0, 0, 0);
+      after[j] = lane == 31 && p + 16 < stop ? fetch(p + 16) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t k = k0 + j * 256 + lane * 8;
+      const unsigned y[4] = {__shfl_down_sync(~0u, x[j].x, 1), __shfl_down_sync(~0u, x[j].y, 1),
+                             __shfl_down_sync(~0u, x[j].z, 1), __shfl_down_sync(~0u, x[j].w, 1)};
+      // elements skip .. skip + 7 of the sixteen
+      unsigned w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, lane == 31 ? after[j].x : y[0],
+                       lane == 31 ? after[j].y : y[1], lane == 31 ? after[j].z : y[2],
+                       lane == 31 ? after[j].w : y[3]};
+      unsigned v[4];
+#pragma unroll
+      for (int s = 2; s; s >>= 1)  // (by words, in halves)
+#pragma unroll
+        for (int i = 0; i + s < 8; ++i) w[i] = words & s ? w[i + s] : w[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i], w[i + 1], odd);
+      // nothing behind the row's end
+      const int64_t left = a.K - k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (2 * i + 1 >= left) v[i] = 2 * i < left ? v[i] & 0xFFFFu : 0u;
+      if (k < a.Kp)
+        *reinterpret_cast<uint4*>((unsigned short*)a.dst + r * a.Kp + k) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step) {
   const int count = a.count ? *a.count : a.rows;
@@ -773,6 +862,14 @@ __device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step
     const int64_t from = live ? (a.idx ? a.idx[r] : r) : 0;
     const T* src = (const T*)a.src + from / a.T * a.sb + from % a.T * a.st;
     const bool whole = ((uintptr_t)src & 15) == 0;
+    if constexpr (!std::is_same<T, float>::value) {
+      if (live && !whole) {
+        const int64_t last = a.rows > 0 ? (int64_t)(a.rows - 1) / a.T * a.sb + (a.T - 1) * a.st + a.K : 0;
+        pack_shifted(a, (const unsigned short*)src, r, (uintptr_t)a.src,
+                     (uintptr_t)((const unsigned short*)a.src + last));
+        continue;
+      }
+    }
     for (int64_t k = lane * 8; k < a.Kp; k += 256) {
       if constexpr (std::is_same<T, float>::value) {
         float f[8];
@@ -801,7 +898,7 @@ __device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step
         uint4 v = make_uint4(0, 0, 0, 0);
         if (live && whole && k + 8 <= a.K) {
           v = __ldg((const uint4*)(src + k));
-        } else if (live) {
+        } else if (live) {  // (the row's end)
           const unsigned short* q = (const unsigned short*)src + k;
           unsigned h[8];
 #pragma unroll
@@ -915,11 +1012,21 @@ __global__ void __launch_bounds__(256) hidden_kernel(const HiddenRows a) {
     const int64_t dst = packed ? a.idx[r] : r;
     T* out = (T*)a.out + dst / a.T * a.osb + dst % a.T * a.ost;
     const float scale = a.bound ? 1.f / range_scale(*a.bound) : 1.f;
-    for (int64_t k = threadIdx.x; k < a.K; k += 256) {
-      float v = 0.f;
-      if (packed)
-        for (int i = 0; i < a.splits; ++i) v += a.acc[((int64_t)i * a.rpad + r) * a.ldacc + k];
-      Storage<T>::store1(out + k, v * scale);
+    // (sums are padded to 256 columns)
+    for (int64_t k = threadIdx.x * 4; k < a.K; k += 1024) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (packed) {
+        const float* p = a.acc + (int64_t)r * a.ldacc + k;
+#pragma unroll 4
+        for (int i = 0; i < a.splits; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)i * a.rpad * a.ldacc);
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+      }
+      const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + i < a.K) Storage<T>::store1(out + k + i, f[i]);
     }
   }
 }
@@ -977,6 +1084,13 @@ cudaError_t launch(void (*k)(Args...), int64_t grid, unsigned block, int cluster
   return cudaLaunchKernelEx(&c, k, args...);
 }
 
+int sm_count() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 152;
+}
+
 template <int kCg, int kEpi>
 cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
   const int half = g.bn / kCg;
@@ -986,7 +1100,7 @@ cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
     return cudaErrorInvalidValue;
   // rows of A that are not loaded are read from what lies behind: room for the last stage's
   const int more = (kRows - g.a_rows) * 128 + 1024;
-  const int fixed = kEpi == kStats ? 2 * kRows * 16
+  const int fixed = kEpi == kStats ? (int)(kRows * sizeof(Stats))
                     : kEpi == kHidden || kEpi == kWeight ? (int)(8 * sizeof(Turn)) : 0;
   g.stages = std::min(kMaxStages, (kSmem - fixed - more) / stage);
   const int smem = g.stages * stage + more;
@@ -1000,13 +1114,6 @@ template <int kEpi>
 cudaError_t launch_product(Product& g, int cg, int sms, int64_t tiles, cudaStream_t s) {
   const int n = (int)std::min<int64_t>(tiles, 1 << 20);
   return cg == 2 ? launch_product<2, kEpi>(g, sms, n, s) : launch_product<1, kEpi>(g, sms, n, s);
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 152;
 }
 
 int64_t ceil_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -1111,7 +1218,7 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   g.T = std::max<int64_t>(a.T, 1);
   g.status = a.hdr ? &a.hdr->status : nullptr;
   // 32 MB of the rows at a time, so that they stay in L2 while the vocabulary passes
-  g.mb = (int)std::max<int64_t>(1, (32ll << 20) / (2 * l.planes * 256 * l.Kp));
+  g.mb = (int)std::max<int64_t>(1, (32ll << 20) / (2 * l.planes * kRows * l.cg * l.Kp));
   return g;
 }
 
@@ -1216,7 +1323,8 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
   const unsigned* bound = dt == GRPO_F16 ? &h->bound : nullptr;
   const int cg = l.cg;
   const int a_rows = cg == 2 ? kRows : (int)std::max<int64_t>(ceil_to(N, 8), 8);
-  const int64_t mt = div_up(N, kRows * cg);
+  const int rows = kRows * cg;
+  const int64_t mt = div_up(N, rows);
   for (int64_t v0 = 0; v0 < a.V; v0 += l.vc) {
     const int vp = (int)std::min<int64_t>(l.vc, a.V - v0);
     Product g = base(a, dt, l);
@@ -1250,7 +1358,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
       if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
           !encode(&w.b, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, 64))
         return cudaErrorUnknown;
-      if ((e = launch_product<kWeight>(w, cg, sms, div_up(vp, kRows * cg) * w.nt, s)) != cudaSuccess)
+      if ((e = launch_product<kWeight>(w, cg, sms, div_up(vp, rows) * w.nt, s)) != cudaSuccess)
         return e;
     }
     if (a.dhidden && N > 0) {

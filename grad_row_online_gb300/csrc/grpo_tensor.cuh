@@ -30,7 +30,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -42,15 +42,37 @@ __device__ __forceinline__ unsigned long long global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for a phase of `bar`: false if it did not complete in time.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  if (mbar_try(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
+// Waits for a phase of `bar`: false if it did not complete in time.  (The clock
+// is read every 64 rounds only: a read takes longer than most waits.)
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
+  unsigned long long t0 = 0;
   for (uint32_t i = 0; i < kWaitRounds; ++i) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 15u) == 15u && global_ns() - t0 > kWaitNs) return false;
+    if ((i & 63u) == 63u) {
+      const unsigned long long t = global_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > kWaitNs) return false;
+    }
   }
   return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
+}
+
+// One lane of a converged warp.  (The warps that feed the tensor cores run as a
+// whole and let this lane issue: in a branch of one thread alone each copy and
+// product first moves its operands to the uniform registers, and the tensor
+// cores wait for a fifth of the time.)
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(p));
+  return p != 0;
+}
+// mbar_wait for a whole warp, with one answer
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
+  return __all_sync(~0u, mbar_wait(bar, parity));
 }
 
 // ---------------------------------------------------------------- clusters
