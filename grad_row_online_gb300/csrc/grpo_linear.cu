@@ -798,57 +798,37 @@ struct PackRows {
   void* dst;
 };
 
-// A row of 16-bit elements that starts anywhere: a lane reads one aligned
-// vector, takes its neighbour's too and shifts the two together.  A vector
-// that is not wholly inside [begin, end) is put together from its elements.
+// A row of 16-bit elements that starts anywhere: five aligned words give the
+// four of a vector, shifted together where the row starts in the middle of a
+// word.  Words that are not wholly inside [begin, end) are not read as such.
 __device__ __forceinline__ void pack_shifted(const PackRows& a, const unsigned short* src, int64_t r,
                                              uintptr_t begin, uintptr_t end) {
-  const int lane = threadIdx.x & 31;
-  const uintptr_t base = (uintptr_t)src & ~(uintptr_t)15, stop = (uintptr_t)(src + a.K);
-  const int skip = (int)((uintptr_t)src & 15) / 2;  // elements of the first vector before the row
-  auto fetch = [&](uintptr_t p) {
-    if (p >= begin && p + 16 <= end) return __ldg((const uint4*)p);
-    unsigned h[8];
+  const int odd = ((uintptr_t)src & 2) * 8;
+  const uintptr_t base = (uintptr_t)src & ~(uintptr_t)3, stop = (uintptr_t)(src + a.K);
+#pragma unroll 4
+  for (int64_t k = (threadIdx.x & 31) * 8; k < a.Kp; k += 256) {
+    const uintptr_t p = base + 2 * k;
+    unsigned w[5] = {0u, 0u, 0u, 0u, 0u};
+    if (p >= begin && p + 20 <= end) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uintptr_t q = p + 2 * i;
-      h[i] = q >= (uintptr_t)src && q < stop ? __ldg((const unsigned short*)q) : 0u;
+      for (int i = 0; i < 5; ++i) w[i] = __ldg((const unsigned*)p + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        const uintptr_t q = p + 2 * i;
+        if (q >= (uintptr_t)src && q < stop) w[i / 2] |= (unsigned)__ldg((const unsigned short*)q) << (i & 1) * 16;
+      }
     }
-    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-  };
-  const int words = skip >> 1, odd = (skip & 1) * 16;
-  for (int64_t k0 = 0; k0 < a.Kp; k0 += 1024) {
-    uint4 x[4], after[4];  // (four vectors in flight; the last lane's neighbour too)
+    unsigned v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uintptr_t p = base + 2 * (k0 + j * 256 + lane * 8);
-      x[j] = p < stop ? fetch(p) : make_uint4(0, 0, 0, 0);
-      after[j] = lane == 31 && p + 16 < stop ? fetch(p + 16) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t k = k0 + j * 256 + lane * 8;
-      const unsigned y[4] = {__shfl_down_sync(~0u, x[j].x, 1), __shfl_down_sync(~0u, x[j].y, 1),
-                             __shfl_down_sync(~0u, x[j].z, 1), __shfl_down_sync(~0u, x[j].w, 1)};
-      // elements skip .. skip + 7 of the sixteen
-      unsigned w[8] = {x[j].x, x[j].y, x[j].z, x[j].w, lane == 31 ? after[j].x : y[0],
-                       lane == 31 ? after[j].y : y[1], lane == 31 ? after[j].z : y[2],
-                       lane == 31 ? after[j].w : y[3]};
-      unsigned v[4];
-#pragma unroll
-      for (int s = 2; s; s >>= 1)  // (by words, in halves)
-#pragma unroll
-        for (int i = 0; i + s < 8; ++i) w[i] = words & s ? w[i + s] : w[i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i], w[i + 1], odd);
-      // nothing behind the row's end
-      const int64_t left = a.K - k;
+    for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(w[i], w[i + 1], odd);
+    const int64_t left = a.K - k;
+    if (left < 8) {  // nothing behind the row's end
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (2 * i + 1 >= left) v[i] = 2 * i < left ? v[i] & 0xFFFFu : 0u;
-      if (k < a.Kp)
-        *reinterpret_cast<uint4*>((unsigned short*)a.dst + r * a.Kp + k) = make_uint4(v[0], v[1], v[2], v[3]);
     }
+    *reinterpret_cast<uint4*>((unsigned short*)a.dst + r * a.Kp + k) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -881,18 +861,33 @@ __device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = live && k + i < a.K ? __ldg(src + k + i) : 0.f;
         }
+        float top = 0.f;
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          __nv_bfloat16* dst = (__nv_bfloat16*)a.dst + p * a.plane + r * a.Kp + k;
-          float h[8];
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+        __nv_bfloat16* dst = (__nv_bfloat16*)a.dst + r * a.Kp + k;
+        if (top < 0x1.FEp127f) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // (values that round beyond bf16 take its largest; the rest follows in the next plane)
-            h[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
-            if (isinf(h[i]) && !isinf(f[i])) h[i] = copysignf(0x1.FEp127f, f[i]);
-            f[i] = isfinite(h[i]) ? f[i] - h[i] : 0.f;
+          for (int p = 0; p < 3; ++p) {
+            const uint4 h = Storage<__nv_bfloat16>::pack(f);
+            *reinterpret_cast<uint4*>(dst + p * a.plane) = h;
+            float x[8];
+            Storage<__nv_bfloat16>::unpack(h, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] -= x[i];
           }
-          *reinterpret_cast<uint4*>(dst) = Storage<__nv_bfloat16>::pack(h);
+        } else {
+          // values that round beyond bf16 take its largest, and the rest follows
+          // in the next plane; infinities stand in the first alone
+          for (int p = 0; p < 3; ++p) {
+            float h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              h[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
+              if (isinf(h[i]) && !isinf(f[i])) h[i] = copysignf(0x1.FEp127f, f[i]);
+              f[i] = isfinite(h[i]) ? f[i] - h[i] : 0.f;
+            }
+            *reinterpret_cast<uint4*>(dst + p * a.plane) = Storage<__nv_bfloat16>::pack(h);
+          }
         }
       } else {
         uint4 v = make_uint4(0, 0, 0, 0);
