@@ -792,7 +792,7 @@ extern "C" grpo_status_t grpo_embed_tokens_grad(
   if (st != GRPO_OK) return st;
   const int64_t N = B * T;
   if (!matrix_ok(V, K, out_stride_v) || N > kMaxRows ||
-      ceil_div(N, 32) * ceil_div(K, 128) + ceil_div(V, 16) >= 0x7FFFFFFF)
+      ceil_div(N, 32) * ceil_div(K, 128) + ceil_div(V, 8) >= 0x7FFFFFFF)
     return GRPO_ERR_SHAPE;
   if (add && (!matrix_ok(V, K, add_stride_v) ||
               (add == grad_weight && V > 1 && add_stride_v != out_stride_v)))

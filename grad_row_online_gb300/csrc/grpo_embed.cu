@@ -51,6 +51,23 @@ __device__ __forceinline__ void store_vec(O* p, int n, const float* f) {
   }
 }
 
+// an element that a vector holds, and a vector as it lies
+template <typename T>
+__device__ __forceinline__ void store_raw(T* p, int n, const uint4& v) {
+  constexpr int kVec = Storage<T>::kVec;
+  if (n >= kVec && ((uintptr_t)p & 15) == 0) {
+    *reinterpret_cast<uint4*>(p) = v;
+  } else {
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i < n) {
+        if constexpr (kVec == 4) reinterpret_cast<unsigned*>(p)[i] = w[i];
+        else reinterpret_cast<unsigned short*>(p)[i] = (unsigned short)(w[i / 2] >> (i & 1) * 16);
+      }
+  }
+}
+
 // A thread takes a vector of `kPer` rows one behind the other, a CTA up to 256
 // vectors of them: the rows' loads are in flight together.
 template <typename T, int kPer>
@@ -86,13 +103,74 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int slice
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     if (first + j >= a.N) break;
-    float f[kVec];
-    Storage<T>::unpack(v[j], f);
+    T* out = (T*)a.out + b * a.sb + t * a.st + k;
+    if (a.scale == 1.f && id[j] != -2) {  // (as it lies: a copy)
+      store_raw(out, n, v[j]);
+    } else {
+      float f[kVec];
+      Storage<T>::unpack(v[j], f);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      f[i] = id[j] == -2 ? __int_as_float(0x7FFFFFFF) : id[j] < 0 ? 0.f : f[i] * a.scale;
-    store_vec<T, kVec>((T*)a.out + b * a.sb + t * a.st + k, n, f);
+      for (int i = 0; i < kVec; ++i) f[i] = id[j] == -2 ? __int_as_float(0x7FFFFFFF) : f[i] * a.scale;
+      store_vec<T, kVec>(out, n, f);
+    }
     if (++t == a.T) t = 0, ++b;
+  }
+}
+
+// ---------------------------------------------------------------- absent ids
+struct SumArgs {
+  const void* grad;
+  int64_t K, sb, st;
+  int64_t V;
+  int N, T;
+  const int2* sorted;
+  float scale;
+  const void* add;
+  int64_t sa;
+  void* out;
+  int64_t so;
+  float* parts;  // [chunks][2][K]: of the id that came from before, of the id that goes on
+  const unsigned char* taken;
+  int slices, sums;  // of columns; CTAs that add up
+};
+
+// Rows of ids that no token has: zero, or what is added to.  A CTA takes eight
+// of them, a thread a vector of four rows at a time.
+static constexpr int kAbsentRows = 8, kSumThreads = 128;
+
+template <typename O>
+__device__ __forceinline__ void absent_rows(const SumArgs& a, int64_t first) {
+  constexpr int kVec = Storage<O>::kVec;
+  for (int64_t v0 = first; v0 < min(first + kAbsentRows, a.V); v0 += 4) {
+    O* out[4];
+    bool go[4];
+    int64_t off[4];  // elements of the row's first 16-byte vector before the row
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      go[j] = v0 + j < a.V && !a.taken[v0 + j];
+      out[j] = (O*)a.out + (v0 + j) * a.so;
+      off[j] = ((uintptr_t)out[j] & 15) / sizeof(O);
+    }
+    for (int64_t q = (int64_t)threadIdx.x * kVec; q < a.K + kVec; q += kSumThreads * kVec) {
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = q - off[j];
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (a.add && go[j] && k >= 0 && k + kVec <= a.K) x[j] = load_vec((const O*)a.add + (v0 + j) * a.sa + k, kVec);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = q - off[j];
+        if (!go[j]) continue;
+        if (k >= 0 && k + kVec <= a.K) {
+          __stcs(reinterpret_cast<uint4*>(out[j] + k), x[j]);  // (first to leave L2)
+        } else {  // (a row's ends)
+          for (int64_t i = max(k, (int64_t)0); i < min(k + kVec, a.K); ++i)
+            Storage<O>::store1(out[j] + i, a.add ? Storage<O>::load1((const O*)a.add + (v0 + j) * a.sa + i) : 0.f);
+        }
+      }
+    }
   }
 }
 
@@ -248,23 +326,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
 // each.  An id whose tokens lie in one chunk is done; the parts of one that
 // goes on to other chunks are joined by join_kernel in the chunks' order.
 // Behind those CTAs come the ones that fill the rows of absent ids.
-static constexpr int kSumThreads = 128, kSumChunk = 32, kAbsentRows = 16;
-
-struct SumArgs {
-  const void* grad;
-  int64_t K, sb, st;
-  int64_t V;
-  int N, T;
-  const int2* sorted;
-  float scale;
-  const void* add;
-  int64_t sa;
-  void* out;
-  int64_t so;
-  float* parts;  // [chunks][2][K]: of the id that came from before, of the id that goes on
-  const unsigned char* taken;
-  int slices, sums;  // of columns; CTAs that add up
-};
+static constexpr int kSumChunk = 32;
 
 template <typename T, typename O>
 __device__ __forceinline__ void finish(const SumArgs& a, int64_t id, int64_t k, int n, float* f) {
@@ -276,22 +338,6 @@ __device__ __forceinline__ void finish(const SumArgs& a, int64_t id, int64_t k, 
     if (a.add && i < n) f[i] += Storage<O>::load1((const O*)a.add + id * a.sa + k + i);
   }
   store_vec<O, kVec>(out, n, f);
-}
-
-// Rows of ids that no token has: zero, or what is added to.
-template <typename O>
-__device__ __forceinline__ void absent_rows(const SumArgs& a, int64_t first) {
-  constexpr int kVec = Storage<O>::kVec;
-  const int64_t end = min(first + kAbsentRows, a.V);
-  for (int64_t v = first; v < end; ++v) {
-    if (a.taken[v]) continue;
-    for (int64_t k = (int64_t)threadIdx.x * kVec; k < a.K; k += kSumThreads * kVec) {
-      const int n = (int)min((int64_t)kVec, a.K - k);
-      float f[kVec];
-      Storage<O>::unpack(a.add ? load_vec((const O*)a.add + v * a.sa + k, n) : make_uint4(0, 0, 0, 0), f);
-      store_vec<O, kVec>((O*)a.out + v * a.so + k, n, f);
-    }
-  }
 }
 
 template <typename T, typename O>
@@ -356,7 +402,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   }
 }
 
-// Four warps take a quarter of the chunks each, a lane a vector of columns.
+// Ids that go on from one chunk to others: a CTA looks at a chunk for one that
+// begins there; four warps take a quarter of its parts each, a lane a vector
+// of columns.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int slices) {
   constexpr int kVec = Storage<T>::kVec;
@@ -392,20 +440,22 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int 
   const int cols = (int)max((int64_t)0, min((int64_t)kVec, a.K - k));
   // parts 0 (this chunk's) .. last - c, a quarter of them each, in order
   const int64_t parts = last - c + 1, from = parts * warp / 4, to = parts * (warp + 1) / 4;
-  const bool whole = cols == kVec && (a.K & 3) == 0;
   float f[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) f[i] = 0.f;
+  if (cols == kVec && (a.K & 3) == 0) {
 #pragma unroll 4
-  for (int64_t d = from; d < to; ++d) {
-    const float* q = a.parts + ((c + d) * 2 + (d == 0)) * a.K + k;
-    if (whole) {
+    for (int64_t d = from; d < to; ++d) {
+      const float* q = a.parts + ((c + d) * 2 + (d == 0)) * a.K + k;
 #pragma unroll
       for (int i = 0; i < kVec; i += 4) {
         const float4 v = *reinterpret_cast<const float4*>(q + i);
         f[i] += v.x, f[i + 1] += v.y, f[i + 2] += v.z, f[i + 3] += v.w;
       }
-    } else {
+    }
+  } else {
+    for (int64_t d = from; d < to; ++d) {
+      const float* q = a.parts + ((c + d) * 2 + (d == 0)) * a.K + k;
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
         if (i < cols) f[i] += q[i];
@@ -470,15 +520,27 @@ cudaError_t launch(void (*k)(Args...), int64_t grid, unsigned block, cudaStream_
 }
 
 template <typename T, typename O>
-cudaError_t sums(SumArgs& a, const Layout& l, cudaStream_t s) {
+cudaError_t sorted_sums(SortArgs p, SumArgs a, const Layout& l, char* ws, cudaStream_t s) {
   constexpr int kCols = kSumThreads * Storage<T>::kVec, kJoin = 32 * Storage<T>::kVec;
   a.slices = (int)((a.K + kCols - 1) / kCols);
   a.sums = l.sums * a.slices;
-  const int joins = (int)((a.K + kJoin - 1) / kJoin);
-  const int64_t absent = a.add == a.out ? 0 : (a.V + kAbsentRows - 1) / kAbsentRows;
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < l.passes && a.N > 0; ++i) {
+    p.out = (int2*)(ws + l.keys[i & 1]);
+    p.shift = i * l.bits;
+    // (a single chunk's counts stay in its CTA)
+    if (l.chunks > 1 && (e = launch(count_kernel, l.chunks, kSortThreads, s, p)) != cudaSuccess) return e;
+    if ((e = launch(place_kernel, l.chunks, kSortThreads, s, p)) != cudaSuccess) return e;
+    p.ids = nullptr;
+    p.in = p.out;
+  }
+  a.sorted = p.in;
+  // (in place, absent ids' rows stay)
+  const int absent = a.add == a.out ? 0 : (int)((a.V + kAbsentRows - 1) / kAbsentRows);
   if (a.sums + absent == 0) return cudaSuccess;
-  const cudaError_t e = launch(sum_kernel<T, O>, a.sums + absent, kSumThreads, s, a);
+  e = launch(sum_kernel<T, O>, (int64_t)a.sums + absent, kSumThreads, s, a);
   if (e != cudaSuccess || l.sums < 2) return e;
+  const int joins = (int)((a.K + kJoin - 1) / kJoin);
   return launch(join_kernel<T, O>, (int64_t)l.sums * joins, kSumThreads, s, a, joins);
 }
 
@@ -507,25 +569,16 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, grpo_dtype_t dt, cudaStrea
   unsigned char* taken = (unsigned char*)(a.ws + l.taken);
   cudaError_t e = cudaMemsetAsync(taken, 0, (size_t)a.V, s);
   if (e != cudaSuccess) return e;
-  int2* keys[2] = {(int2*)(a.ws + l.keys[0]), (int2*)(a.ws + l.keys[1])};
-  SortArgs p{a.ids, a.mask, a.V, nullptr, nullptr, (int*)(a.ws + l.hist), taken,
-             a.hdr ? &a.hdr->status : nullptr, (int)a.N, l.chunk, l.chunks, 0, l.bits};
-  for (int i = 0; i < l.passes && a.N > 0; ++i) {
-    p.out = keys[i & 1];
-    p.shift = i * l.bits;
-    // (a single chunk's counts stay in its CTA)
-    if (l.chunks > 1 && (e = launch(count_kernel, l.chunks, kSortThreads, s, p)) != cudaSuccess) return e;
-    if ((e = launch(place_kernel, l.chunks, kSortThreads, s, p)) != cudaSuccess) return e;
-    p.ids = nullptr;
-    p.in = p.out;
-  }
-  SumArgs g{a.grad, a.K, a.sb, a.st, a.V, (int)a.N, (int)std::max<int64_t>(a.T, 1), p.in, a.scale,
-            a.add, a.sa, a.out, a.so, (float*)(a.ws + l.parts), taken, 0, 0};
-  if (dt == GRPO_F32) return sums<float, float>(g, l, s);
+  const SortArgs p{a.ids, a.mask, a.V, nullptr, nullptr, (int*)(a.ws + l.hist), taken,
+                   a.hdr ? &a.hdr->status : nullptr, (int)a.N, l.chunk, l.chunks, 0, l.bits};
+  const SumArgs g{a.grad, a.K, a.sb, a.st, a.V, (int)a.N, (int)std::max<int64_t>(a.T, 1), nullptr,
+                  a.scale, a.add, a.sa, a.out, a.so, (float*)(a.ws + l.parts), taken, 0, 0};
+  if (dt == GRPO_F32) return sorted_sums<float, float>(p, g, l, a.ws, s);
   if (dt == GRPO_BF16)
-    return a.odt == GRPO_F32 ? sums<__nv_bfloat16, float>(g, l, s)
-                             : sums<__nv_bfloat16, __nv_bfloat16>(g, l, s);
-  return a.odt == GRPO_F32 ? sums<__half, float>(g, l, s) : sums<__half, __half>(g, l, s);
+    return a.odt == GRPO_F32 ? sorted_sums<__nv_bfloat16, float>(p, g, l, a.ws, s)
+                             : sorted_sums<__nv_bfloat16, __nv_bfloat16>(p, g, l, a.ws, s);
+  return a.odt == GRPO_F32 ? sorted_sums<__half, float>(p, g, l, a.ws, s)
+                           : sorted_sums<__half, __half>(p, g, l, a.ws, s);
 }
 
 }  // namespace grpo

@@ -722,23 +722,33 @@ __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int base = blockIdx.x * kPrepRows, r = base + (int)threadIdx.x;
   launched_early();
+  // what this thread's token needs, asked for at once
+  const bool mine_in = r < a.N;
+  float w = 0.f, h = 0.f, m = 0.f, Z = 1.f, H = 0.f;
+  int64_t id = -1;
+  bool on = mine_in && (!a.mask || a.mask[r]);
+  if (a.coef && mine_in) {
+    if (a.dlogp) w = a.dlogp[r], id = a.actions[r];
+    if (a.dent) h = a.dent[r], H = a.entropy[r];
+    m = a.stats[r], Z = a.stats[(int64_t)a.N + r];
+    on = on && (!(w == 0.f) || !(h == 0.f));
+  }
   // the tokens before this CTA's (the last one meets them all: it has the bound too)
   int before = 0;
   float wm = 0.f, hm = 0.f;
 #pragma unroll 4
   for (int i = threadIdx.x; i < base; i += 1024) {
-    const bool m = !a.mask || a.mask[i];
-    const float w = a.dlogp ? a.dlogp[i] : 0.f, h = a.dent ? a.dent[i] : 0.f;
-    const bool on = m && (!a.coef || !(w == 0.f) || !(h == 0.f));
-    before += on;
-    if (on) wm = fmaxf(wm, fabsf(w)), hm = fmaxf(hm, fabsf(h));
+    const bool in = !a.mask || a.mask[i];
+    const float wi = a.dlogp ? a.dlogp[i] : 0.f, hi = a.dent ? a.dent[i] : 0.f;
+    const bool part = in && (!a.coef || !(wi == 0.f) || !(hi == 0.f));
+    before += part;
+    if (part) wm = fmaxf(wm, fabsf(wi)), hm = fmaxf(hm, fabsf(hi));
   }
   before = __reduce_add_sync(~0u, before);
   if (lane == 0) s_sum[warp] = before;
   __syncthreads();
   before = __reduce_add_sync(~0u, s_sum[lane]);
   __syncthreads();
-  const bool on = r < a.N && takes_part(a, r);
   const unsigned votes = __ballot_sync(~0u, on);
   if (lane == 0) s_sum[warp] = __popc(votes);
   __syncthreads();
@@ -749,13 +759,10 @@ __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
   if (on) {
     a.idx[at] = r;
     if (a.coef) {
-      const float m = a.stats[r], Z = a.stats[(int64_t)a.N + r];
-      const float w = a.dlogp ? a.dlogp[r] : 0.f, h = a.dent ? a.dent[r] : 0.f;
       const float lnZ = logf(Z);
-      float c0 = a.s / Z * (w + (a.dent ? h * (a.entropy[r] - lnZ) : 0.f));
+      float c0 = a.s / Z * (w + (a.dent ? h * (H - lnZ) : 0.f));
       int t = -1;
       if (w != 0.f) {
-        const int64_t id = a.actions[r];
         if (id >= 0 && id < a.V) {
           t = (int)id;
         } else {
@@ -767,7 +774,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
       a.target[at] = t;
       wm = fmaxf(wm, fabsf(w)), hm = fmaxf(hm, fabsf(h));
     }
-  } else if (r < a.N) {
+  } else if (mine_in) {
     if (a.logps) a.logps[r] = 0.f;
     if (a.out_entropy) a.out_entropy[r] = 0.f;
     if (a.out_stats) a.out_stats[r] = 0.f, a.out_stats[(int64_t)a.N + r] = 1.f;
@@ -776,9 +783,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(const PrepRows a) {
   if (a.coef) {
     // |d| <= s (|dlogp| + |dH| max(1 / e, ln V)); the largest of either give a
     // bound of all (bits order as the values do)
-    const float w = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(wm)));
-    const float h = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(hm)));
-    if (lane == 0) s_max[warp] = __float_as_uint(a.s * (w + h * (0.37f + logf((float)a.V))));
+    const float wt = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(wm)));
+    const float ht = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(hm)));
+    if (lane == 0) s_max[warp] = __float_as_uint(a.s * (wt + ht * (0.37f + logf((float)a.V))));
     __syncthreads();
     const unsigned top = __reduce_max_sync(~0u, s_max[lane]);
     if (threadIdx.x == 0) a.h->bound = top;

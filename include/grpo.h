@@ -564,7 +564,7 @@ grpo_status_t grpo_embed_tokens(const void *weight, grpo_dtype_t dt, int64_t V, 
  *                     same stride: then only rows that some token has are
  *                     touched.  No other overlap.
  * Sizes: B T and V at most 2^31 - 1025, K at most 2^20, and
- * ceil(B T / 32) ceil(K / 128) + ceil(V / 16) < 2^31.
+ * ceil(B T / 32) ceil(K / 128) + ceil(V / 8) < 2^31.
  * ws: grpo_embed_workspace_size(B T, K, V) bytes, 256-byte aligned. */
 size_t grpo_embed_workspace_size(int64_t N, int64_t K, int64_t V);
 
