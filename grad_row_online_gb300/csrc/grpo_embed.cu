@@ -328,19 +328,39 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
 // Behind those CTAs come the ones that fill the rows of absent ids.
 static constexpr int kSumChunk = 32;
 
+// kVec elements of what is added to a row, as they lie: one or two vectors
 template <typename T, typename O>
-__device__ __forceinline__ void finish(const SumArgs& a, int64_t id, int64_t k, int n, float* f) {
-  constexpr int kVec = Storage<T>::kVec;
-  O* out = (O*)a.out + id * a.so + k;
+struct Addend {
+  static constexpr int kVec = Storage<T>::kVec, kOut = Storage<O>::kVec;
+  uint4 v[kVec / kOut];
+  __device__ __forceinline__ void load(const SumArgs& a, int64_t id, int64_t k, int n) {
+    const O* p = (const O*)a.add + id * a.sa + k;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    f[i] *= a.scale;
-    if (a.add && i < n) f[i] += Storage<O>::load1((const O*)a.add + id * a.sa + k + i);
+    for (int i = 0; i < kVec / kOut; ++i)
+      v[i] = n > i * kOut ? load_vec(p + i * kOut, n - i * kOut) : make_uint4(0, 0, 0, 0);
   }
-  store_vec<O, kVec>(out, n, f);
-}
+  __device__ __forceinline__ void plus(float* f) const {
+#pragma unroll
+    for (int i = 0; i < kVec / kOut; ++i) {
+      float x[kOut];
+      Storage<O>::unpack(v[i], x);
+#pragma unroll
+      for (int j = 0; j < kOut; ++j) f[i * kOut + j] += x[j];
+    }
+  }
+};
 
 template <typename T, typename O>
+__device__ __forceinline__ void finish(const SumArgs& a, int64_t id, int64_t k, int n, float* f,
+                                       const Addend<T, O>& add) {
+  constexpr int kVec = Storage<T>::kVec;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) f[i] *= a.scale;
+  if (a.add) add.plus(f);
+  store_vec<O, kVec>((O*)a.out + id * a.so + k, n, f);
+}
+
+template <typename T, typename O, bool kAdd>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   constexpr int kVec = Storage<T>::kVec;
   __shared__ int s_id[kSumChunk + 2];
@@ -372,10 +392,13 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   static_assert(kSumChunk % kAhead == 0, "whole groups");
   for (int j0 = 0; j0 < n; j0 += kAhead) {
     uint4 g[kAhead];
+    Addend<T, O> add[kAdd ? kAhead : 1];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const T* row = s_row[j0 + u];
       if (row) g[u] = load_vec(row + k, cols);
+      // (an id's last token: what is added is on its way with the rows)
+      if (kAdd && row && s_id[2 + j0 + u] != s_id[1 + j0 + u]) add[u].load(a, s_id[1 + j0 + u], k, cols);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -391,7 +414,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
       const bool from_before = begin == 0 && s_id[0] == id;
       const bool goes_on = j + 1 == n && s_id[2 + j] == id;
       if (!from_before && !goes_on) {
-        finish<T, O>(a, id, k, cols, f);
+        finish<T, O>(a, id, k, cols, f, add[kAdd ? u : 0]);
       } else {
         store_vec<float, kVec>(a.parts + ((int64_t)c * 2 + (from_before ? 0 : 1)) * a.K + k, cols, f);
       }
@@ -469,7 +492,9 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int 
   for (int w = 1; w < kSumThreads / 32; ++w)
 #pragma unroll
     for (int i = 0; i < kVec; ++i) f[i] += s_sum[w][lane][i];
-  finish<T, O>(a, id, k, cols, f);
+  Addend<T, O> add;
+  if (a.add) add.load(a, id, k, cols);
+  finish<T, O>(a, id, k, cols, f, add);
 }
 
 struct Layout {
@@ -483,8 +508,8 @@ Layout layout(int64_t N, int64_t K, int64_t V) {
   while (bits < 31 && (V >> bits) != 0) ++bits;  // ids 0 .. V
   l.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   l.bits = (bits + l.passes - 1) / l.passes;
-  // up to 256 chunks of at least 2,048 tokens
-  l.chunk = (int)((std::max<int64_t>(2048, (N + 255) / 256) + kSortThreads - 1) / kSortThreads * kSortThreads);
+  // one chunk of up to 4,096 tokens, or up to 256 of at least 2,048
+  l.chunk = (int)((std::max<int64_t>(N <= 4096 ? N : 2048, (N + 255) / 256) + kSortThreads - 1) / kSortThreads * kSortThreads);
   l.chunks = (int)((N + l.chunk - 1) / l.chunk);
   l.sums = (int)((N + kSumChunk - 1) / kSumChunk);
   size_t o = 0;
@@ -538,7 +563,8 @@ cudaError_t sorted_sums(SortArgs p, SumArgs a, const Layout& l, char* ws, cudaSt
   // (in place, absent ids' rows stay)
   const int absent = a.add == a.out ? 0 : (int)((a.V + kAbsentRows - 1) / kAbsentRows);
   if (a.sums + absent == 0) return cudaSuccess;
-  e = launch(sum_kernel<T, O>, (int64_t)a.sums + absent, kSumThreads, s, a);
+  auto* k = a.add ? sum_kernel<T, O, true> : sum_kernel<T, O, false>;
+  e = launch(k, (int64_t)a.sums + absent, kSumThreads, s, a);
   if (e != cudaSuccess || l.sums < 2) return e;
   const int joins = (int)((a.K + kJoin - 1) / kJoin);
   return launch(join_kernel<T, O>, (int64_t)l.sums * joins, kSumThreads, s, a, joins);
