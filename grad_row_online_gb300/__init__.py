@@ -14,6 +14,7 @@ raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -710,11 +711,14 @@ def grpo_token_logps_grad(logits: torch.Tensor, action_ids: Optional[torch.Tenso
 # the ends of the policy: log-probs from hidden states, token embedding
 def grpo_linear_workspace_size(hidden: torch.Tensor, weight: torch.Tensor,
                                backward: bool = False) -> int:
-    """Bytes of ``workspace=`` for grpo_linear_logps, or its gradient, of these tensors."""
-    N = hidden.numel() // max(hidden.shape[-1], 1)
-    return int(lib().grpo_linear_workspace_size(_ptr(weight), _DTYPES[hidden.dtype], 1, N,
-                                                hidden.shape[-1], weight.shape[0],
-                                                weight.stride(0), int(backward)))
+    """Bytes of ``workspace=`` for grpo_linear_logps, or its gradient, of these
+    tensors (the weight's address and row stride decide whether its rows are
+    copied to aligned ones)."""
+    N = math.prod(hidden.shape[:-1])
+    with torch.cuda.device(weight.device if weight.is_cuda else -1):
+        return int(lib().grpo_linear_workspace_size(_ptr(weight), _DTYPES[hidden.dtype], 1, N,
+                                                    hidden.shape[-1], weight.shape[0],
+                                                    weight.stride(0), int(backward)))
 
 
 def grpo_linear_logps(hidden: torch.Tensor, weight: torch.Tensor,

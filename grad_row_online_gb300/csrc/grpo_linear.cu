@@ -271,9 +271,7 @@ __device__ __forceinline__ float4 join(const float4 (&x)[n], float s2) {
 __device__ __forceinline__ void record(const Product& g, const Stats& st, Stats* pair, int side,
                                        int64_t at) {
   const int row = threadIdx.x & 127;
-  // (2^(x s2 - ref) = 2^((x - m) s2) 2^d)
-  const float d = fabsf(st.m) < INFINITY ? fmaf(st.m, g.s2, -(st.m * g.s2)) : 0.f, k = exp2f(-d);
-  float4 x[2] = {make_float4(st.m, st.Z * k, (st.D - d * st.Z) * k, 0.f)};
+  float4 x[2] = {make_float4(st.m, st.Z, st.D, 0.f)};
   asm volatile("bar.sync 1, 256;" ::: "memory");  // (the record before has been read)
   if (side == 1) pair[row] = Stats{x[0].x, x[0].y, x[0].z};
   asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -331,10 +329,8 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const bool live = r < count;
     const int64_t id = row.id - t.n0;
     const int a = id >= 0 && id < n ? (int)id : -1;
-    // sums of 2^u and 2^u u, u = x s2 - ref, against ref = fl(m s2), and what that
-    // rounded off is put right in the record; 0 while there is no finite m
+    // sums of 2^u and 2^u u, u = (x - m) s2
     float m = st.m, Z = st.Z, D = st.D, xa = 0.f;
-    float ref = m == -INFINITY ? 0.f : m * g.s2;
     for (int c = 32 * side; c < n; c += 64) {
       float v[32];
       load(c, v);
@@ -344,20 +340,21 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
       }
       const float cm = max32(v);
       if (cm > m) {
-        const float to = cm * g.s2, u = fmaxf(ref - to, -1000.f);
+        const float u = fmaxf((m - cm) * g.s2, -1000.f);
         const float k = exp2f(u);
         D = k * fmaf(Z, u, D);
         Z *= k;
         m = cm;
-        ref = to;
       }
+      // (a row of -inf so far: 2^-inf = 0 against any finite reference)
+      const float ref = m == -INFINITY ? 0.f : m;
       const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-ref, -ref);
       float2 z2[2], d2[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) z2[i] = d2[i] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const float2 u = fma2(make_float2(v[i], v[i + 1]), s2, r2);
+        const float2 u = mul2(add2(make_float2(v[i], v[i + 1]), r2), s2);
         const float2 e = make_float2(ex2_fast(u.x), ex2_fast(u.y));
         z2[i / 2 & 1] = add2(z2[i / 2 & 1], e);
         if (g.want_entropy) d2[i / 2 & 1] = fma2(e, u, d2[i / 2 & 1]);
@@ -369,7 +366,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
         d = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float u = fmaf(v[i], g.s2, -ref);
+          const float u = (v[i] - ref) * g.s2;
           d = fmaf(ex2_fast(u), fmaxf(u, -1000.f), d);
         }
       }
@@ -392,10 +389,8 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float4 q = row.q;
     const int a = live ? (int)row.id - g.v0 - t.n0 : -1;
     const float scale = g.bound ? range_scale(*g.bound) : 1.f;
-    // 2^(x s2 - ref) (c0 + c1 (x s2 - ref)) with ref = fl(m s2), as in the sums
-    const float ref = q.x * g.s2, off = fmaf(q.x, g.s2, -ref), k = -exp2f(-off) * scale;
-    const float c0 = k * fmaf(-off, q.z, q.y), c1 = k * q.z;
-    const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-ref, -ref);
+    const float c0 = -q.y * scale, c1 = -q.z * scale;
+    const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-q.x, -q.x);
     const float2 c02 = make_float2(c0, c0), c12 = make_float2(c1, c1);
     const int planes = g.pairs == 1 ? 1 : 3;
     __nv_bfloat16* dst = g.d + (int64_t)r * g.ldd + t.n0;
@@ -403,10 +398,10 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
       float v[32];
       load(c, v);
       // (far below the others, -inf among them: 0, not 0 x inf)
-      const bool low = g.want_entropy && !(min32(v) * g.s2 > -1e20f);
+      const bool low = g.want_entropy && !((min32(v) - q.x) * g.s2 > -1e20f);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        float2 u = fma2(make_float2(v[i], v[i + 1]), s2, r2);
+        float2 u = mul2(add2(make_float2(v[i], v[i + 1]), r2), s2);
         float2 w = make_float2(ex2_fast(u.x), ex2_fast(u.y));
         if (g.want_entropy) {
           if (low) u = make_float2(fmaxf(u.x, -1000.f), fmaxf(u.y, -1000.f));
