@@ -1,5 +1,6 @@
-"""A GRPO training loop on a policy small enough to read: the log-prob entry
-points, the loss and the gradient clipping together, as a trainer calls them.
+"""A GRPO training loop on a policy small enough to read: the embedding, the
+head's log-probs, the loss and the gradient clipping together, as a trainer
+calls them.
 
     python examples/train_step.py [--steps N]
 
@@ -8,8 +9,9 @@ step samples completions at a temperature, scores them (grpo_token_logps: the
 behaviour log-probs, with the alternatives a log would show), rewards a
 completion for the tokens it takes from a target set, and takes a few updates:
 
-    logits -> grpo_token_logps -> grpo_loss_from_logps (dL/dlogp)
-           -> grpo_token_logps_grad (+ entropy bonus) -> the model's gradients
+    tokens -> grpo_embed_tokens -> grpo_linear_logps (no logits in memory)
+           -> grpo_loss_from_logps (dL/dlogp)
+           -> grpo_linear_logps_grad (+ entropy bonus) -> grpo_embed_tokens_grad
            -> grpo_clip_grad_norm -> SGD
 """
 import argparse
@@ -26,7 +28,9 @@ class Policy:
     def __init__(self, V: int, D: int, seed: int):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         self.embedding = torch.randn((V, D), generator=gen, device="cuda") * 0.3
-        self.head = torch.randn((D, V), generator=gen, device="cuda") * 0.3
+        # the head's weight as a linear layer keeps it, [V, D], and its transpose
+        self.weight = (torch.randn((D, V), generator=gen, device="cuda") * 0.3).t().contiguous()
+        self.head = self.weight.t()
 
     def parameters(self):
         return [self.embedding, self.head]
@@ -40,6 +44,18 @@ class Policy:
         hidden = self.embedding[t]
         demb = torch.zeros_like(self.embedding).index_add_(0, t, d @ self.head.t())
         return [demb, hidden.t() @ d]
+
+    def hidden(self, tokens):
+        return g.grpo_embed_tokens(self.embedding, tokens)
+
+    def backward(self, tokens, hidden, actions, mask, scored, dlogp, dentropy, temperature, status=None):
+        """[dL/dembedding, dL/dhead] from the gradients of the scores, without
+        the logits or their gradient in memory."""
+        d = g.grpo_linear_logps_grad(hidden, self.weight, actions, mask, scored["stats"], grad_logps=dlogp,
+                                     entropy=scored["entropy"], grad_entropy=dentropy, temperature=temperature,
+                                     status=status)
+        demb = g.grpo_embed_tokens_grad(d["grad_hidden"], tokens, self.embedding.shape[0], mask)
+        return [demb, d["grad_weight"].t()]
 
 
 def train(steps=30, prompts=8, samples=8, T=24, V=601, D=32, lr=300.0, updates=2, temperature=1.0,
@@ -68,18 +84,14 @@ def train(steps=30, prompts=8, samples=8, T=24, V=601, D=32, lr=300.0, updates=2
         rewards = (good[actions] & mask).sum(1).float() / lengths
         history.append(float(rewards.mean()))
         for _ in range(updates):
-            z = policy.logits(inputs)
-            new = g.grpo_token_logps(z, actions, mask, temperature=temperature, want_entropy=True,
-                                     want_stats=True, status=status)
+            h = policy.hidden(inputs)
+            new = g.grpo_linear_logps(h, policy.weight, actions, mask, temperature=temperature,
+                                      want_entropy=True, want_stats=True, status=status)
             loss = g.grpo_loss_from_logps(new["logps"], old, None, mask, rewards,
                                           samples_per_prompt=samples, beta=0.0, clip_eps=0.2,
                                           clip_eps_hi=0.28)
             dentropy = mask * (-entropy_bonus / mask.sum())
-            dlogits = g.grpo_token_logps_grad(z, actions, mask, new["stats"],
-                                              grad_logps=loss["grad"], entropy=new["entropy"],
-                                              grad_entropy=dentropy, temperature=temperature,
-                                              grad=z)  # in place: z is not needed again
-            grads = policy.gradients(inputs, dlogits)
+            grads = policy.backward(inputs, h, actions, mask, new, loss["grad"], dentropy, temperature, status)
             g.grpo_clip_grad_norm(grads, max_norm)
             for p, d in zip(policy.parameters(), grads):
                 p.sub_(d, alpha=lr)
