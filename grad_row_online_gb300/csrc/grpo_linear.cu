@@ -34,6 +34,9 @@ static constexpr int kRows = 128;     // rows of a CTA's tile (lanes of tensor m
 static constexpr int kPad = 256;      // packed rows are padded to the rows of a pair's tile
 static constexpr int kMaxStages = 12;
 static constexpr int kSmem = 227 * 1024 - 320;  // of a CTA's, beside the barriers
+// kParts: registers a thread of the first four warps and of the others, of 168 at the launch
+static constexpr int kFewRegs = 56, kManyRegs = 224;
+static_assert(4 * kFewRegs + 8 * kManyRegs <= 12 * 168, "what the launch gives");
 static constexpr int kTurn = 33;          // words of a row in the results' 16 x 32 turn
 
 struct Product {
@@ -47,6 +50,7 @@ struct Product {
   int splits;     // parts of the reduction (kHidden)
   int pairs;      // products of planes: 1, or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
+  int sums;       // kParts: blocks that one accumulator sums up
   int kc;         // kStats, kCg 1: sets of accumulators that the reduction is cut into, in order
   int slot, bufs; // columns of a set; tiles that are in flight, 1 or 2
   int want_entropy; // kStats: D is wanted; kGrad: c1 is not 0
@@ -295,33 +299,46 @@ __device__ __forceinline__ RowData row_data(const Product& g, const Tile& t, int
   return x;
 }
 
-// ---- results of a tile: a thread has one row, `tm` its accumulators; two
-// warps share 32 rows and take blocks of 32 columns in turn
-template <int kCg, int kEpi>
+// ---- results of a tile: a thread has one row; two warps share 32 rows and take
+// blocks of 32 columns in turn, from tensor memory at `tm` or (kParts) added
+// up in `acc`
+template <int kCg, int kEpi, bool kParts>
 __device__ __forceinline__ void results(const Product& g, const Tile& t, int rank, int count,
-                                        uint32_t tm, bool have, bool failed, Stats& st, Turn& turn,
+                                        uint32_t tm, bool have, bool failed,
+                                        float (&acc)[kParts ? 4 : 1][32], Stats& st, Turn& turn,
                                         Stats* pair, const RowData& row) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
   const int side = (int)(threadIdx.x >> 5) / 4 - 1;
   const int r = t.m0 + rank * kRows + quad * 32 + lane;
   const float bad = __int_as_float(0x7FFFFFFF);
-  auto load = [&](int c, float (&v)[32]) {
-    __syncwarp();
-    if (have) {
-      tmem_ld32(tm + c, v);
-      tmem_wait(v);
-      if constexpr (kCg == 1 && kEpi == kStats) {
-        for (int j = 1; j < g.kc; ++j) {
-          float w[32];
-          tmem_ld32(tm + j * g.slot + c, w);
-          tmem_wait(w);
+  // f(c, columns c .. c + 31) for this warp's blocks below `end`
+  auto blocks = [&](int end, auto&& f) {
+    if constexpr (kParts) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += w[i];
-        }
-      }
+      for (int j = 0; j < 4; ++j)
+        if (32 * side + 64 * j < end) f(32 * side + 64 * j, acc[j]);
     } else {
+      for (int c = 32 * side; c < end; c += 64) {
+        float v[32];
+        __syncwarp();
+        if (have) {
+          tmem_ld32(tm + c, v);
+          tmem_wait(v);
+          if constexpr (kCg == 1 && kEpi == kStats) {
+            for (int j = 1; j < g.kc; ++j) {
+              float w[32];
+              tmem_ld32(tm + j * g.slot + c, w);
+              tmem_wait(w);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = failed ? bad : 0.f;
+              for (int i = 0; i < 32; ++i) v[i] += w[i];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = failed ? bad : 0.f;
+        }
+        f(c, v);
+      }
     }
   };
   if constexpr (kEpi == kStats) {
@@ -331,9 +348,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const int a = id >= 0 && id < n ? (int)id : -1;
     // sums of 2^u and 2^u u, u = (x - m) s2
     float m = st.m, Z = st.Z, D = st.D, xa = 0.f;
-    for (int c = 32 * side; c < n; c += 64) {
-      float v[32];
-      load(c, v);
+    blocks(n, [&](int c, float(&v)[32]) {
       if (c + 32 > n) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = c + i < n ? v[i] : -INFINITY;
@@ -376,7 +391,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 #pragma unroll
         for (int i = 0; i < 32; ++i) xa = a == c + i ? v[i] : xa;
       }
-    }
+    });
     if (a >= 0 && (a >> 5 & 1) == side) g.xa[r] = xa;
     st = Stats{m, Z, D};
     if (!g.run) {
@@ -394,9 +409,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float2 c02 = make_float2(c0, c0), c12 = make_float2(c1, c1);
     const int planes = g.pairs == 1 ? 1 : 3;
     __nv_bfloat16* dst = g.d + (int64_t)r * g.ldd + t.n0;
-    for (int c = 32 * side; c < g.bn; c += 64) {
-      float v[32];
-      load(c, v);
+    blocks(g.bn, [&](int c, float(&v)[32]) {
       // (far below the others, -inf among them: 0, not 0 x inf)
       const bool low = g.want_entropy && !((min32(v) - q.x) * g.s2 > -1e20f);
 #pragma unroll
@@ -436,7 +449,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
           }
         }
       }
-    }
+    });
   } else {
     const float scale = g.bound ? 1.f / range_scale(*g.bound) : 1.f;
     const int64_t dst = kEpi == kWeight ? (r < g.vp ? g.v0 + r : -1)
@@ -447,24 +460,22 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
                                       : dst / g.T * g.osb + dst % g.T * g.ost + t.n0;
     turn.add_at[lane] = kEpi == kWeight ? dst * g.asv + t.n0 : 0;
     __syncwarp();
-    for (int c = 32 * side; c < g.bn && t.n0 + c < g.K; c += 64) {
+    blocks(min(g.bn, g.K - t.n0), [&](int c, float(&v)[32]) {
       const int n = min(32, g.K - t.n0 - c);
-      float v[32];
-      load(c, v);
       if constexpr (kEpi == kHidden) {
         if (g.acc) {
           // (the last columns are padding; rows without a source have no sums)
-          float* acc = g.acc + ((int64_t)t.split * g.rpad + r) * g.ldacc + t.n0 + c;
+          float* sums = g.acc + ((int64_t)t.split * g.rpad + r) * g.ldacc + t.n0 + c;
           if (g.acc_old && dst >= 0) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 o = *reinterpret_cast<const float4*>(acc + i);
+              const float4 o = *reinterpret_cast<const float4*>(sums + i);
               v[i] += o.x, v[i + 1] += o.y, v[i + 2] += o.z, v[i + 3] += o.w;
             }
           }
           if (g.acc_new) {
-            if (dst >= 0) store_row<float>(acc, nullptr, v, 1.f);
-            continue;
+            if (dst >= 0) store_row<float>(sums, nullptr, v, 1.f);
+            return;
           }
         }
       }
@@ -475,7 +486,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
         store_tile((__nv_bfloat16*)g.out, (const __nv_bfloat16*)add, c, v, n, scale, turn);
       else
         store_tile((__half*)g.out, (const __half*)add, c, v, n, scale, turn);
-    }
+    });
   }
 }
 
@@ -483,7 +494,12 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // 256 rows, each CTA holds half of either operand's tile) takes tiles in turn;
 // one thread asks for the operands' blocks, one issues the products into one
 // of two sets of accumulators, eight warps turn the other into results.
-template <int kCg, int kEpi>
+//
+// An accumulator is rounded towards zero at every step, 16 products long, so
+// a sum's error grows with its length and has its sign.  kParts: sums of `sums`
+// blocks each are added up in registers, rounded to nearest (fp32 operands,
+// and widths whose logits would be off by more than fp32 log-probs are).
+template <int kCg, int kEpi, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2];
@@ -491,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   __shared__ Turn s_turn[kEpi == kHidden || kEpi == kWeight ? 8 : 1];
   __shared__ Stats s_pair[kEpi == kStats ? kRows : 1];
   constexpr bool kAmn = kEpi == kWeight, kBmn = kEpi == kWeight || kEpi == kHidden;
-  constexpr bool kSets = kCg == 1 && kEpi == kStats;
+  constexpr bool kSets = kCg == 1 && kEpi == kStats && !kParts;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kCg == 2 ? cluster_rank() : 0u;
@@ -545,127 +561,184 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     return x;
   };
+  // (kParts) where the part of a tile's n blocks that starts at k ends: the
+  // small planes' products, whose roundings are small too, are one part
+  auto part_end = [&](int k, int n) {
+    const int small = n - n / g.pairs;
+    return k < small ? small : min(n, k + g.sums);
+  };
   const bool two = !kSets || g.bufs == 2;  // tiles in flight
   const int first = blockIdx.x / kCg, step = gridDim.x / kCg;
   bool ok = true;
 
-  if (warp == 0) {
-    // ---- operands
-    const bool one = elect();
-    int st = 0;
-    uint32_t ph = 0;
-    for (int i = first; i < total && ok; i += step) {
-      const Tile t = tile(i);
-      const int m = t.m0 + (int)rank * kRows, n = t.n0 + (int)rank * half;
-      for (int p = 0; p < g.pairs && ok; ++p) {
-        const int za = g.pairs == 1 ? 0 : kPairs[p][0], zb = g.pairs == 1 ? 0 : kPairs[p][1];
-        for (int k = t.k0; k < t.k1; ++k) {
-          if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
-          uint32_t bar = smem_u32(&s_full[st]);
-          const uint32_t sa = smem + st * stage_bytes, sb = sa + a_bytes;
-          const int y = (kEpi == kHidden ? g.v0 : 0) + k * kBlk;  // (of rows across the reduction)
-          if (one) {
-            if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
-            if (kCg == 2) bar = map_to(bar, 0);
-            if (kAmn) {
-              for (int j = 0; j < kRows; j += 64)
-                tma_load<kCg>(sa + j * 128u, &g.a, m + j, k * kBlk, za, bar);
-            } else {
-              tma_load<kCg>(sa, &g.a, k * kBlk, m, za, bar);
-            }
-            if (kBmn) {
-              for (int j = 0; j < half; j += 64)
-                tma_load<kCg>(sb + j * 128u, &g.b, n + j, y, zb, bar);
-            } else {
-              tma_load<kCg>(sb, &g.b, k * kBlk, g.v0 + n, zb, bar);
-            }
-          }
-          __syncwarp();
-          if (++st == g.stages) st = 0, ph ^= 1u;
-        }
-      }
-    }
-    // nothing of this CTA's is in flight when it ends: every stage asked for
-    // has been taken (or, after a wait that ran out, has at least arrived)
-    // (a stage never asked for is in the phase that this wait takes as done)
-    for (int i = 0; i < g.stages; ++i) {
-      if (!mbar_wait_all(ok ? smem_u32(&s_empty[st]) : smem_u32(&s_full[st]), ph ^ 1u)) break;
-      if (++st == g.stages) st = 0, ph ^= 1u;
-    }
-  } else if (warp == 1 && rank == 0) {
-    // ---- products
-    const bool one = elect();
-    const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
-    const uint64_t da0 = operand(smem, kAmn), db0 = operand(smem + a_bytes, kBmn);
-    const uint32_t idesc = instruction(kRows * kCg, g.bn, g.fmt, kAmn, kBmn);
-    constexpr uint32_t kStepA = kAmn ? 128u : 2u, kStepB = kBmn ? 128u : 2u;  // 16 elements, in 16 bytes
-    int st = 0;
-    uint32_t ph = 0;
-    int it = 0;
-    for (int i = first; i < total && ok; i += step) {
-      const Tile t = tile(i);
-      const int n = (t.k1 - t.k0) * g.pairs;
-      if (n == 0) continue;
-      const int buf = two ? it & 1 : 0;
-      if (!(ok = mbar_wait_all(smem_u32(&s_free[buf]), ((two ? it >> 1 : it) & 1) ^ 1u))) break;
-      fence_after();
-      uint32_t d = tmem + (uint32_t)buf * 256u;
-      int next = kSets ? n / g.kc : 0, set = 0;  // (the first block of the next set)
-      bool add = false, here = false;            // (here: the next block has been seen to be there)
-      for (int k = 0; k < n; ++k) {
-        if (kSets && k == next && set + 1 < g.kc) {
-          ++set;
-          next = n * (set + 1) / g.kc;
-          d += (uint32_t)g.slot;
-          add = false;
-        }
-        if (!here && !(ok = mbar_wait_all(full0 + 8u * st, ph))) break;
-        const uint64_t off = (uint64_t)((uint32_t)st * stage_bytes >> 4), da = da0 + off, db = db0 + off;
-        if (one) {
-#pragma unroll
-          for (int j = 0; j < kBlk / 16; ++j)
-            mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, add || j != 0);
-          commit<kCg>(empty0 + 8u * st);
-        }
-        __syncwarp();
-        add = true;
-        if (++st == g.stages) st = 0, ph ^= 1u;
-        here = k + 1 < n && __all_sync(~0u, mbar_try(full0 + 8u * st, ph));
-      }
-      if (one) commit<kCg>(smem_u32(&s_done[buf]));
-      __syncwarp();
-      ++it;
-    }
-  } else if (warp >= 4) {
+  if (warp >= 4) {
+    if constexpr (kParts) registers_up<kManyRegs>();
     // ---- results
     int it = 0;
     Stats st{-INFINITY, 0.f, 0.f};
-    Turn& turn = s_turn[kEpi == kHidden || kEpi == kWeight ? warp - 4 : 0];
-    for (int i = first; i < total; i += step) {
-      const Tile t = tile(i);
-      const int buf = two ? it & 1 : 0;
-      const bool some = (t.k1 - t.k0) * g.pairs > 0;
-      const RowData row = row_data<kEpi>(g, t, (int)rank, count);
-      if (some && ok) {
-        // (one lane asks: the others would take turns at it with the products' thread)
-        if (lane == 0) ok = mbar_wait(smem_u32(&s_done[buf]), (two ? it >> 1 : it) & 1);
-        ok = __all_sync(~0u, ok);
-      }
-      fence_after();
-      results<kCg, kEpi>(g, t, (int)rank, count,
-                         tmem + (uint32_t)buf * 256u + ((uint32_t)(warp & 3) << 21), some && ok,
-                         !ok, st, turn, s_pair, row);
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    // (one lane asks: the others would take turns at it with the products' thread)
+    auto done = [&](int buf, int phase) {
+      bool there = true;
+      if (lane == 0) there = mbar_wait(smem_u32(&s_done[buf]), phase & 1);
+      return __all_sync(~0u, there) != 0;
+    };
+    auto release = [&](int buf) {
       fence_before();
       __syncwarp();
-      if (lane == 0 && some && ok) {
+      if (lane == 0) {
         const uint32_t bar = smem_u32(&s_free[buf]);
         mbar_arrive_cluster(kCg == 2 ? map_to(bar, 0) : bar);
       }
-      it += some;
+    };
+    auto fill = [](auto& v, float x) {
+      for (auto& row : v)
+#pragma unroll
+        for (int c = 0; c < 32; ++c) row[c] = x;
+    };
+    Turn& turn = s_turn[kEpi == kHidden || kEpi == kWeight ? warp - 4 : 0];
+    for (int i = first; i < total; i += step) {
+      const Tile t = tile(i);
+      const int n = (t.k1 - t.k0) * g.pairs;
+      const RowData row = row_data<kEpi>(g, t, (int)rank, count);
+      float acc[kParts ? 4 : 1][32];
+      if constexpr (kParts) {
+        if (n == 0) fill(acc, 0.f);
+        for (int k = 0; k < n; k = part_end(k, n)) {
+          const int buf = it & 1;
+          ok = ok && done(buf, it >> 1);
+          if (!ok) {
+            fill(acc, __int_as_float(0x7FFFFFFF));
+            break;
+          }
+          fence_after();
+          const uint32_t tm = lanes + (uint32_t)buf * 256u + 32u * (uint32_t)(warp / 4 - 1);
+          if (k == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (64 * j < g.bn) tmem_ld32(tm + 64 * j, acc[j]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_wait(acc[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (64 * j >= g.bn) break;
+              float v[32];
+              tmem_ld32(tm + 64 * j, v);
+              tmem_wait(v);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) acc[j][c] += v[c];
+            }
+          }
+          release(buf);
+          ++it;
+        }
+        results<kCg, kEpi, true>(g, t, (int)rank, count, 0u, true, !ok, acc, st, turn, s_pair, row);
+      } else {
+        const int buf = two ? it & 1 : 0;
+        if (n > 0) ok = ok && done(buf, two ? it >> 1 : it);
+        fence_after();
+        results<kCg, kEpi, false>(g, t, (int)rank, count, lanes + (uint32_t)buf * 256u, n > 0 && ok, !ok,
+                                  acc, st, turn, s_pair, row);
+        if (n > 0 && ok) release(buf);
+        it += n > 0;
+      }
     }
     if (kEpi == kStats && g.run) {
       const int r = (warp & 3) * 32 + lane;
       record(g, st, s_pair, warp >= 8, r < count ? (int64_t)blockIdx.x * g.rpad + r : -1);
+    }
+  } else {
+    if constexpr (kParts) registers_down<kFewRegs>();
+    if (warp == 0) {
+      // ---- operands
+      const bool one = elect();
+      int st = 0;
+      uint32_t ph = 0;
+      for (int i = first; i < total && ok; i += step) {
+        const Tile t = tile(i);
+        const int m = t.m0 + (int)rank * kRows, n = t.n0 + (int)rank * half;
+        for (int p = 0; p < g.pairs && ok; ++p) {
+          const int za = g.pairs == 1 ? 0 : kPairs[p][0], zb = g.pairs == 1 ? 0 : kPairs[p][1];
+          for (int k = t.k0; k < t.k1; ++k) {
+            if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
+            uint32_t bar = smem_u32(&s_full[st]);
+            const uint32_t sa = smem + st * stage_bytes, sb = sa + a_bytes;
+            const int y = (kEpi == kHidden ? g.v0 : 0) + k * kBlk;  // (of rows across the reduction)
+            if (one) {
+              if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
+              if (kCg == 2) bar = map_to(bar, 0);
+              if (kAmn) {
+                for (int j = 0; j < kRows; j += 64)
+                  tma_load<kCg>(sa + j * 128u, &g.a, m + j, k * kBlk, za, bar);
+              } else {
+                tma_load<kCg>(sa, &g.a, k * kBlk, m, za, bar);
+              }
+              if (kBmn) {
+                for (int j = 0; j < half; j += 64)
+                  tma_load<kCg>(sb + j * 128u, &g.b, n + j, y, zb, bar);
+              } else {
+                tma_load<kCg>(sb, &g.b, k * kBlk, g.v0 + n, zb, bar);
+              }
+            }
+            __syncwarp();
+            if (++st == g.stages) st = 0, ph ^= 1u;
+          }
+        }
+      }
+      // nothing of this CTA's is in flight when it ends: every stage asked for
+      // has been taken (or, after a wait that ran out, has at least arrived)
+      // (a stage never asked for is in the phase that this wait takes as done)
+      for (int i = 0; i < g.stages; ++i) {
+        if (!mbar_wait_all(ok ? smem_u32(&s_empty[st]) : smem_u32(&s_full[st]), ph ^ 1u)) break;
+        if (++st == g.stages) st = 0, ph ^= 1u;
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---- products
+      const bool one = elect();
+      const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+      const uint64_t da0 = operand(smem, kAmn), db0 = operand(smem + a_bytes, kBmn);
+      const uint32_t idesc = instruction(kRows * kCg, g.bn, g.fmt, kAmn, kBmn);
+      constexpr uint32_t kStepA = kAmn ? 128u : 2u, kStepB = kBmn ? 128u : 2u;  // 16 elements, in 16 bytes
+      int st = 0;
+      uint32_t ph = 0;
+      int it = 0;
+      for (int i = first; i < total && ok; i += step) {
+        const Tile t = tile(i);
+        const int n = (t.k1 - t.k0) * g.pairs;
+        if (n == 0) continue;
+        for (int k = 0; k < n && ok; ++it) {
+          // a tile, or (kParts) a part of its reduction, into one of two accumulators
+          const int buf = two ? it & 1 : 0, end = kParts ? part_end(k, n) : n;
+          if (!(ok = mbar_wait_all(smem_u32(&s_free[buf]), ((two ? it >> 1 : it) & 1) ^ 1u))) break;
+          fence_after();
+          uint32_t d = tmem + (uint32_t)buf * 256u;
+          int next = kSets ? n / g.kc : 0, set = 0;  // (the first block of the next set)
+          bool add = false, here = false;            // (here: the next block has been seen to be there)
+          for (; k < end; ++k) {
+            if (kSets && k == next && set + 1 < g.kc) {
+              ++set;
+              next = n * (set + 1) / g.kc;
+              d += (uint32_t)g.slot;
+              add = false;
+            }
+            if (!here && !(ok = mbar_wait_all(full0 + 8u * st, ph))) break;
+            const uint64_t off = (uint64_t)((uint32_t)st * stage_bytes >> 4), da = da0 + off, db = db0 + off;
+            if (one) {
+  #pragma unroll
+              for (int j = 0; j < kBlk / 16; ++j)
+                mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, add || j != 0);
+              commit<kCg>(empty0 + 8u * st);
+            }
+            __syncwarp();
+            add = true;
+            if (++st == g.stages) st = 0, ph ^= 1u;
+            here = k + 1 < end && __all_sync(~0u, mbar_try(full0 + 8u * st, ph));
+          }
+          if (one) commit<kCg>(smem_u32(&s_done[buf]));
+          __syncwarp();
+        }
+      }
     }
   }
   if (!ok && g.status) atomicOr(g.status, (unsigned)GRPO_ERR_TIMEOUT);
@@ -1088,7 +1161,7 @@ int sm_count() {
   return n > 0 ? n : 152;
 }
 
-template <int kCg, int kEpi>
+template <int kCg, int kEpi, bool kParts>
 cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
   const int half = g.bn / kCg;
   const int stage = g.a_rows * 128 + ((half * 128 + 1023) & ~1023);
@@ -1101,7 +1174,7 @@ cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
                     : kEpi == kHidden || kEpi == kWeight ? (int)(8 * sizeof(Turn)) : 0;
   g.stages = std::min(kMaxStages, (kSmem - fixed - more) / stage);
   const int smem = g.stages * stage + more;
-  auto* k = product_kernel<kCg, kEpi>;
+  auto* k = product_kernel<kCg, kEpi, kParts>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch(k, std::max(1, std::min(sms / kCg, tiles)) * kCg, kThreads, kCg, smem, s, g);
@@ -1110,7 +1183,9 @@ cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
 template <int kEpi>
 cudaError_t launch_product(Product& g, int cg, int sms, int64_t tiles, cudaStream_t s) {
   const int n = (int)std::min<int64_t>(tiles, 1 << 20);
-  return cg == 2 ? launch_product<2, kEpi>(g, sms, n, s) : launch_product<1, kEpi>(g, sms, n, s);
+  if (g.sums > 0)
+    return cg == 2 ? launch_product<2, kEpi, true>(g, sms, n, s) : launch_product<1, kEpi, true>(g, sms, n, s);
+  return cg == 2 ? launch_product<2, kEpi, false>(g, sms, n, s) : launch_product<1, kEpi, false>(g, sms, n, s);
 }
 
 int64_t ceil_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -1129,6 +1204,14 @@ struct Layout {
   size_t idx, coef, target, xa, part, hidden, weight, d, acc, total;
 };
 
+// Blocks of a reduction, 64 elements each, that one accumulator sums up.  A
+// logit of 16-bit operands is off by about 2e-8 of its size for each block:
+// sharp log-probs (temperature 0.6, deviation 3) by 2.2e-6 at a width of 1,024,
+// 4e-6 at 2,048 and 8e-6 at 4,096, where parts of 2,048 make it 2e-6 and cost
+// 8 % (4,096 x 4,096 x 128,256: 2,069 and 2,244 us).  Sums of fp32 operands are
+// as exact as chains of fp32 additions with 8 (and 5e-5 off in the gradients of
+// sharp log-probs without parts).
+static constexpr int kSumsF32 = 8, kSumsWide = 32;
 static constexpr int64_t kPieceBytes = 512ll << 20;  // of the logits' gradient
 
 Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t V, int64_t sv,
@@ -1204,6 +1287,7 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   g.kb = (int)(l.Kp / 64);
   g.splits = 1;
   g.a_rows = kRows;
+  g.sums = dt == GRPO_F32 ? kSumsF32 : 0;
   g.kc = 1;
   g.slot = 256;
   g.bufs = 2;
@@ -1269,12 +1353,13 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   g.want_entropy = a.entropy != nullptr;
   g.bn = l.bn;
   g.nt = (int)l.nt;
+  if (!g.sums && g.kb > (l.direct ? 2 * kSumsWide : kSumsWide)) g.sums = kSumsWide;
   if (l.direct) {
     g.run = 1;
     g.a_rows = (int)ceil_to(N, 8);
     // two sums of half of the products each: an accumulator is rounded towards
     // zero at every step, and the memory for the second is free here
-    g.kc = std::min(2, g.kb * g.pairs);
+    if (!g.sums) g.kc = std::min(2, g.kb * g.pairs);
     g.bufs = g.kc == 1 ? 2 : 1;
   }
   const bool mapped =

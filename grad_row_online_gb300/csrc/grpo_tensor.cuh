@@ -46,7 +46,7 @@ __device__ __forceinline__ unsigned long long global_ns() {
 }
 // Waits for a phase of `bar`: false if it did not complete in time.  (The clock
 // is read every 64 rounds only: a read takes longer than most waits.)
-static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
   unsigned long long t0 = 0;
   for (uint32_t i = 0; i < kWaitRounds; ++i) {
     if (mbar_try(bar, parity)) return true;
@@ -75,6 +75,17 @@ __device__ __forceinline__ bool elect() {
 // mbar_wait for a whole warp, with one answer
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
   return __all_sync(~0u, mbar_wait(bar, parity));
+}
+
+// Registers a thread, from one group of four warps to others (each of its warps
+// runs this): a rise waits for what the launch gave and others gave up.
+template <int kRegs>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // ---------------------------------------------------------------- clusters
