@@ -1280,6 +1280,9 @@ cudaError_t pack(const LinearArgs& a, grpo_dtype_t dt, const Layout& l, const in
   return launch(k, hc + wc, 256, 1, 0, s, h, w, hc);
 }
 
+// Parts of a reduction of `kb` blocks: none where one accumulator holds it.
+int sums_of(grpo_dtype_t dt, int64_t kb) { return dt == GRPO_F32 && kb > kSumsF32 ? kSumsF32 : 0; }
+
 Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   Product g{};
   g.rows = (int)(a.B * a.T);
@@ -1287,7 +1290,7 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   g.kb = (int)(l.Kp / 64);
   g.splits = 1;
   g.a_rows = kRows;
-  g.sums = dt == GRPO_F32 ? kSumsF32 : 0;
+  g.sums = sums_of(dt, g.kb);
   g.kc = 1;
   g.slot = 256;
   g.bufs = 2;
@@ -1353,7 +1356,7 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   g.want_entropy = a.entropy != nullptr;
   g.bn = l.bn;
   g.nt = (int)l.nt;
-  if (!g.sums && g.kb > (l.direct ? 2 * kSumsWide : kSumsWide)) g.sums = kSumsWide;
+  if (dt != GRPO_F32 && g.kb > (l.direct ? 2 * kSumsWide : kSumsWide)) g.sums = kSumsWide;
   if (l.direct) {
     g.run = 1;
     g.a_rows = (int)ceil_to(N, 8);
@@ -1437,6 +1440,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
       w.bn = l.kbn;
       w.nt = (int)div_up(a.K, w.bn);
       w.a_rows = kRows;
+      w.sums = sums_of(dt, div_up(N, 64));
       if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
           !encode(&w.b, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, 64))
         return cudaErrorUnknown;
@@ -1453,6 +1457,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
       w.nt = (int)div_up(a.K, w.bn);
       w.kb = (vp + 63) / 64;
       w.splits = (int)l.splits;
+      w.sums = sums_of(dt, div_up(w.kb, w.splits));
       w.acc = l.acc ? (float*)(a.ws + l.acc) : nullptr;
       w.ldacc = l.ldacc;
       w.acc_old = v0 > 0;
