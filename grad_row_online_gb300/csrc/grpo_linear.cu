@@ -9,7 +9,7 @@
 //
 // One kernel does the four products on the tensor cores: the logits with
 // their online softmax (kStats), the logits again with their gradient
-// (kGrad), and the two products of that gradient (kHidden, kWeight).  The
+// (kGrad), and the two products of that gradient, in one launch (kBack).  The
 // gradient of the logits exists for a piece of the vocabulary at a time.
 // Every kernel here may be set up while the one before it ends, and waits for
 // that before it touches memory.
@@ -26,7 +26,7 @@ namespace {
 
 using namespace tc;
 
-enum Epi { kStats, kGrad, kHidden, kWeight };
+enum Epi { kStats, kGrad, kBack };
 
 static constexpr int kThreads = 384;  // warps: loads, products, tensor memory, (idle), 8 of results
 static constexpr int kBlk = 64;       // elements of the reduction a stage holds: 128 bytes a row
@@ -47,7 +47,8 @@ struct Product {
   int K;          // width
   int bn, nt;     // columns of a tile, tiles of columns
   int kb;         // blocks of the reduction where it is not over the rows
-  int splits;     // parts of the reduction (kHidden)
+  int on;         // kBack: this product is wanted
+  int splits;     // kBack, dh: parts of the reduction
   int pairs;      // products of planes: 1, or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
   int sums;       // kParts: blocks that one accumulator sums up
@@ -71,20 +72,21 @@ struct Product {
   __nv_bfloat16* d;      // [planes][rpad][ldd]
   int64_t ldd;
   const unsigned* bound; // f16: largest |d|, as bits; nullptr: no scaling
-  // kHidden: fp32 sums, or results
+  // kBack.  dh: fp32 sums, or results
   float* acc;            // [splits][rpad][ldacc]
   int64_t ldacc;
   int acc_old, acc_new;  // sums are there, are left there
   void* out;
   int64_t T, osb, ost;   // rows of the results
   int odt;
-  const void* add;       // kWeight
+  const void* add;       // dW
   int64_t asv;
   unsigned* status;
 };
 
 struct Tile {
   int m0, n0, k0, k1, split;
+  bool weight;  // kBack: of dW
 };
 
 struct Stats {
@@ -452,34 +454,32 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     });
   } else {
     const float scale = g.bound ? 1.f / range_scale(*g.bound) : 1.f;
-    const int64_t dst = kEpi == kWeight ? (r < g.vp ? g.v0 + r : -1)
+    const int64_t dst = t.weight ? (r < g.vp ? g.v0 + r : -1)
                                         : (r < count ? (g.idx ? g.idx[r] : r) : -1);
     __syncwarp();
-    turn.at[lane] = dst < 0           ? -1
-                    : kEpi == kWeight ? dst * g.ost + t.n0
-                                      : dst / g.T * g.osb + dst % g.T * g.ost + t.n0;
-    turn.add_at[lane] = kEpi == kWeight ? dst * g.asv + t.n0 : 0;
+    turn.at[lane] = dst < 0    ? -1
+                    : t.weight ? dst * g.ost + t.n0
+                               : dst / g.T * g.osb + dst % g.T * g.ost + t.n0;
+    turn.add_at[lane] = t.weight ? dst * g.asv + t.n0 : 0;
     __syncwarp();
     blocks(min(g.bn, g.K - t.n0), [&](int c, float(&v)[32]) {
       const int n = min(32, g.K - t.n0 - c);
-      if constexpr (kEpi == kHidden) {
-        if (g.acc) {
-          // (the last columns are padding; rows without a source have no sums)
-          float* sums = g.acc + ((int64_t)t.split * g.rpad + r) * g.ldacc + t.n0 + c;
-          if (g.acc_old && dst >= 0) {
+      if (!t.weight && g.acc) {
+        // (the last columns are padding; rows without a source have no sums)
+        float* sums = g.acc + ((int64_t)t.split * g.rpad + r) * g.ldacc + t.n0 + c;
+        if (g.acc_old && dst >= 0) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 o = *reinterpret_cast<const float4*>(sums + i);
-              v[i] += o.x, v[i + 1] += o.y, v[i + 2] += o.z, v[i + 3] += o.w;
-            }
-          }
-          if (g.acc_new) {
-            if (dst >= 0) store_row<float>(sums, nullptr, v, 1.f);
-            return;
+          for (int i = 0; i < 32; i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(sums + i);
+            v[i] += o.x, v[i + 1] += o.y, v[i + 2] += o.z, v[i + 3] += o.w;
           }
         }
+        if (g.acc_new) {
+          if (dst >= 0) store_row<float>(sums, nullptr, v, 1.f);
+          return;
+        }
       }
-      const void* add = kEpi == kWeight ? g.add : nullptr;
+      const void* add = t.weight ? g.add : nullptr;
       if (g.odt == GRPO_F32)
         store_tile((float*)g.out, (const float*)add, c, v, n, scale, turn);
       else if (g.odt == GRPO_BF16)
@@ -500,13 +500,15 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // blocks each are added up in registers, rounded to nearest (fp32 operands,
 // and widths whose logits would be off by more than fp32 log-probs are).
 template <int kCg, int kEpi, bool kParts>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product g) {
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ Product g,
+                   const __grid_constant__ std::conditional_t<kEpi == kBack, Product, int> w) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_done[2], s_free[2];
   __shared__ uint32_t s_tmem;
-  __shared__ Turn s_turn[kEpi == kHidden || kEpi == kWeight ? 8 : 1];
+  __shared__ Turn s_turn[kEpi == kBack ? 8 : 1];
   __shared__ Stats s_pair[kEpi == kStats ? kRows : 1];
-  constexpr bool kAmn = kEpi == kWeight, kBmn = kEpi == kWeight || kEpi == kHidden;
+  constexpr bool kBmn = kEpi == kBack;
   constexpr bool kSets = kCg == 1 && kEpi == kStats && !kParts;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -518,6 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   if (threadIdx.x == 0) {
     tma_prefetch(&g.a);
     tma_prefetch(&g.b);
+    if constexpr (kEpi == kBack) {
+      tma_prefetch(&w.a);
+      tma_prefetch(&w.b);
+    }
     for (int i = 0; i < g.stages; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_empty[i]), 1);
@@ -537,38 +543,65 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   launched_early();
 
   const int count = g.count ? *g.count : g.rows;
-  const int rows = kEpi == kWeight ? g.vp : count;
   constexpr int kTile = kRows * kCg;  // rows of a tile
-  const int mt = (rows + kTile - 1) / kTile;
-  const int kb = kEpi == kWeight ? (count + kBlk - 1) / kBlk : g.kb;
-  const int per = mt * g.nt;
-  const int total = per * (kEpi == kHidden ? g.splits : 1);
-  // tiles: parts of the reduction, then blocks of mb rows of tiles, in which
-  // the rows' tiles come first
-  auto tile = [&](int t) {
-    Tile x;
-    x.split = kEpi == kHidden ? t / per : 0;
-    const int u = t - x.split * per;
-    const int blk = u / (g.mb * g.nt), left = u - blk * g.mb * g.nt;
-    const int w = min(g.mb, mt - blk * g.mb);
-    x.m0 = (blk * g.mb + left % w) * kTile;
-    x.n0 = left / w * g.bn;
+  const int mt = (count + kTile - 1) / kTile, per = mt * g.nt;
+  const int first = blockIdx.x / kCg, step = gridDim.x / kCg;
+  // tiles: (kBack) parts of the reduction, then blocks of mb rows of tiles, in
+  // which the rows' tiles come first
+  auto place = [&](Tile& x, int u, int mt, int mb, int nt, int bn) {
+    const int blk = u / (mb * nt), left = u - blk * mb * nt;
+    const int across = min(mb, mt - blk * mb);
+    x.m0 = (blk * mb + left % across) * kTile;
+    x.n0 = left / across * bn;
+  };
+  // the j-th tile of this cluster: whether there is one, and which
+  auto tile = [&](int j, Tile& x) {
+    x.weight = false;
+    x.split = 0;
     x.k0 = 0;
-    x.k1 = kb;
-    if (kEpi == kHidden) {
-      x.k0 = (int)((int64_t)kb * x.split / g.splits);
-      x.k1 = (int)((int64_t)kb * (x.split + 1) / g.splits);
+    x.k1 = g.kb;
+    if constexpr (kEpi != kBack) {
+      const int i = first + j * step;
+      if (i >= per) return false;
+      place(x, i, mt, g.mb, g.nt, g.bn);
+    } else {
+      // dh's tiles, which are long, in turn; then dW's, of which the clusters
+      // with one long tile less take as many more as that one lasts
+      const int hidden = g.on ? per * g.splits : 0, wmt = (w.vp + kTile - 1) / kTile;
+      const int weight = w.on ? wmt * w.nt : 0, wkb = (count + kBlk - 1) / kBlk;
+      const int mine = hidden > first ? (hidden - first + step - 1) / step : 0;
+      if (j < mine) {
+        const int i = first + j * step;
+        x.split = i / per;
+        place(x, i - x.split * per, mt, g.mb, g.nt, g.bn);
+        x.k0 = (int)((int64_t)g.kb * x.split / g.splits);
+        x.k1 = (int)((int64_t)g.kb * (x.split + 1) / g.splits);
+        return true;
+      }
+      j -= mine;
+      const int busy = hidden % step, idle = step - busy;  // clusters with one tile more, less
+      const int64_t more = busy && wkb ? (g.kb / g.splits + wkb / 2) / wkb : 0;
+      const int extra = (int)min((int64_t)weight, more * idle);
+      const int at = first - busy, mine2 = first >= busy && extra > at ? (extra - at + idle - 1) / idle : 0;
+      const int i = j < mine2 ? at + j * idle : extra + first + (j - mine2) * step;
+      if (i >= weight) return false;
+      x.weight = true;
+      x.k1 = wkb;
+      place(x, i, wmt, w.mb, w.nt, w.bn);
     }
-    return x;
+    return true;
+  };
+  auto of = [&](const Tile& x) -> const Product& {
+    if constexpr (kEpi == kBack) return x.weight ? w : g;
+    else return g;
   };
   // (kParts) where the part of a tile's n blocks that starts at k ends: the
   // small planes' products, whose roundings are small too, are one part
-  auto part_end = [&](int k, int n) {
-    const int small = n - n / g.pairs;
-    return k < small ? small : min(n, k + g.sums);
+  auto part_end = [&](const Product& p, int k, int n) {
+    const int small = n - n / p.pairs;
+    return k < small ? small : p.sums ? min(n, k + p.sums) : n;
   };
   const bool two = !kSets || g.bufs == 2;  // tiles in flight
-  const int first = blockIdx.x / kCg, step = gridDim.x / kCg;
   bool ok = true;
 
   if (warp >= 4) {
@@ -596,15 +629,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < 32; ++c) row[c] = x;
     };
-    Turn& turn = s_turn[kEpi == kHidden || kEpi == kWeight ? warp - 4 : 0];
-    for (int i = first; i < total; i += step) {
-      const Tile t = tile(i);
-      const int n = (t.k1 - t.k0) * g.pairs;
+    Turn& turn = s_turn[kEpi == kBack ? warp - 4 : 0];
+    Tile t;
+    for (int j = 0; tile(j, t); ++j) {
+      const Product& p = of(t);
+      const int n = (t.k1 - t.k0) * p.pairs;
       const RowData row = row_data<kEpi>(g, t, (int)rank, count);
       float acc[kParts ? 4 : 1][32];
       if constexpr (kParts) {
         if (n == 0) fill(acc, 0.f);
-        for (int k = 0; k < n; k = part_end(k, n)) {
+        for (int k = 0; k < n; k = part_end(p, k, n)) {
           const int buf = it & 1;
           ok = ok && done(buf, it >> 1);
           if (!ok) {
@@ -633,12 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           release(buf);
           ++it;
         }
-        results<kCg, kEpi, true>(g, t, (int)rank, count, 0u, true, !ok, acc, st, turn, s_pair, row);
+        results<kCg, kEpi, true>(p, t, (int)rank, count, 0u, true, !ok, acc, st, turn, s_pair, row);
       } else {
         const int buf = two ? it & 1 : 0;
         if (n > 0) ok = ok && done(buf, two ? it >> 1 : it);
         fence_after();
-        results<kCg, kEpi, false>(g, t, (int)rank, count, lanes + (uint32_t)buf * 256u, n > 0 && ok, !ok,
+        results<kCg, kEpi, false>(p, t, (int)rank, count, lanes + (uint32_t)buf * 256u, n > 0 && ok, !ok,
                                   acc, st, turn, s_pair, row);
         if (n > 0 && ok) release(buf);
         it += n > 0;
@@ -650,42 +684,56 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   } else {
     if constexpr (kParts) registers_down<kFewRegs>();
+    // (dW's A lies across the reduction.  Either product's loop is its own code:
+    // chosen within the loop, maps and descriptors leave the uniform registers,
+    // and the tensor cores wait a fifth of the time.)
+    auto each = [&](auto&& run) {
+      Tile t;
+      for (int j = 0; ok && tile(j, t); ++j) {
+        if constexpr (kEpi == kBack) {
+          if (t.weight) run(t, w, std::true_type{});
+          else run(t, g, std::false_type{});
+        } else {
+          run(t, g, std::false_type{});
+        }
+      }
+    };
+    int st = 0;
+    uint32_t ph = 0;
     if (warp == 0) {
       // ---- operands
       const bool one = elect();
-      int st = 0;
-      uint32_t ph = 0;
-      for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile(i);
+      each([&](const Tile& t, const Product& q, auto amn) {
+        constexpr bool kAmn = decltype(amn)::value;
         const int m = t.m0 + (int)rank * kRows, n = t.n0 + (int)rank * half;
-        for (int p = 0; p < g.pairs && ok; ++p) {
-          const int za = g.pairs == 1 ? 0 : kPairs[p][0], zb = g.pairs == 1 ? 0 : kPairs[p][1];
+        for (int p = 0; p < q.pairs && ok; ++p) {
+          const int za = q.pairs == 1 ? 0 : kPairs[p][0], zb = q.pairs == 1 ? 0 : kPairs[p][1];
           for (int k = t.k0; k < t.k1; ++k) {
             if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
             uint32_t bar = smem_u32(&s_full[st]);
             const uint32_t sa = smem + st * stage_bytes, sb = sa + a_bytes;
-            const int y = (kEpi == kHidden ? g.v0 : 0) + k * kBlk;  // (of rows across the reduction)
             if (one) {
               if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
               if (kCg == 2) bar = map_to(bar, 0);
               if (kAmn) {
                 for (int j = 0; j < kRows; j += 64)
-                  tma_load<kCg>(sa + j * 128u, &g.a, m + j, k * kBlk, za, bar);
+                  tma_load<kCg>(sa + j * 128u, &q.a, m + j, k * kBlk, za, bar);
               } else {
-                tma_load<kCg>(sa, &g.a, k * kBlk, m, za, bar);
+                tma_load<kCg>(sa, &q.a, k * kBlk, m, za, bar);
               }
               if (kBmn) {
+                const int y = (kAmn ? 0 : g.v0) + k * kBlk;
                 for (int j = 0; j < half; j += 64)
-                  tma_load<kCg>(sb + j * 128u, &g.b, n + j, y, zb, bar);
+                  tma_load<kCg>(sb + j * 128u, &q.b, n + j, y, zb, bar);
               } else {
-                tma_load<kCg>(sb, &g.b, k * kBlk, g.v0 + n, zb, bar);
+                tma_load<kCg>(sb, &q.b, k * kBlk, g.v0 + n, zb, bar);
               }
             }
             __syncwarp();
             if (++st == g.stages) st = 0, ph ^= 1u;
           }
         }
-      }
+      });
       // nothing of this CTA's is in flight when it ends: every stage asked for
       // has been taken (or, after a wait that ran out, has at least arrived)
       // (a stage never asked for is in the phase that this wait takes as done)
@@ -697,19 +745,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       // ---- products
       const bool one = elect();
       const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
-      const uint64_t da0 = operand(smem, kAmn), db0 = operand(smem + a_bytes, kBmn);
-      const uint32_t idesc = instruction(kRows * kCg, g.bn, g.fmt, kAmn, kBmn);
-      constexpr uint32_t kStepA = kAmn ? 128u : 2u, kStepB = kBmn ? 128u : 2u;  // 16 elements, in 16 bytes
-      int st = 0;
-      uint32_t ph = 0;
       int it = 0;
-      for (int i = first; i < total && ok; i += step) {
-        const Tile t = tile(i);
-        const int n = (t.k1 - t.k0) * g.pairs;
-        if (n == 0) continue;
+      each([&](const Tile& t, const Product& p, auto amn) {
+        constexpr bool kAmn = decltype(amn)::value;
+        constexpr uint32_t kStepA = kAmn ? 128u : 2u, kStepB = kBmn ? 128u : 2u;  // 16 elements, in 16 bytes
+        const uint64_t da0 = operand(smem, kAmn), db0 = operand(smem + a_bytes, kBmn);
+        const uint32_t idesc = instruction(kRows * kCg, g.bn, g.fmt, kAmn, kBmn);
+        const int n = (t.k1 - t.k0) * p.pairs;
         for (int k = 0; k < n && ok; ++it) {
           // a tile, or (kParts) a part of its reduction, into one of two accumulators
-          const int buf = two ? it & 1 : 0, end = kParts ? part_end(k, n) : n;
+          const int buf = two ? it & 1 : 0, end = kParts ? part_end(p, k, n) : n;
           if (!(ok = mbar_wait_all(smem_u32(&s_free[buf]), ((two ? it >> 1 : it) & 1) ^ 1u))) break;
           fence_after();
           uint32_t d = tmem + (uint32_t)buf * 256u;
@@ -725,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (!here && !(ok = mbar_wait_all(full0 + 8u * st, ph))) break;
             const uint64_t off = (uint64_t)((uint32_t)st * stage_bytes >> 4), da = da0 + off, db = db0 + off;
             if (one) {
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < kBlk / 16; ++j)
                 mma<kCg>(d, da + j * kStepA, db + j * kStepB, idesc, add || j != 0);
               commit<kCg>(empty0 + 8u * st);
@@ -738,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (one) commit<kCg>(smem_u32(&s_done[buf]));
           __syncwarp();
         }
-      }
+      });
     }
   }
   if (!ok && g.status) atomicOr(g.status, (unsigned)GRPO_ERR_TIMEOUT);
@@ -1162,7 +1207,7 @@ int sm_count() {
 }
 
 template <int kCg, int kEpi, bool kParts>
-cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
+cudaError_t launch_product(Product& g, const Product* w, int sms, int tiles, cudaStream_t s) {
   const int half = g.bn / kCg;
   const int stage = g.a_rows * 128 + ((half * 128 + 1023) & ~1023);
   // what the accumulators take has to fit: 512 columns, 256 of each of two tiles
@@ -1171,21 +1216,26 @@ cudaError_t launch_product(Product& g, int sms, int tiles, cudaStream_t s) {
   // rows of A that are not loaded are read from what lies behind: room for the last stage's
   const int more = (kRows - g.a_rows) * 128 + 1024;
   const int fixed = kEpi == kStats ? (int)(kRows * sizeof(Stats))
-                    : kEpi == kHidden || kEpi == kWeight ? (int)(8 * sizeof(Turn)) : 0;
+                    : kEpi == kBack ? (int)(8 * sizeof(Turn)) : 0;
   g.stages = std::min(kMaxStages, (kSmem - fixed - more) / stage);
   const int smem = g.stages * stage + more;
   auto* k = product_kernel<kCg, kEpi, kParts>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch(k, std::max(1, std::min(sms / kCg, tiles)) * kCg, kThreads, kCg, smem, s, g);
+  const int grid = std::max(1, std::min(sms / kCg, tiles)) * kCg;
+  if constexpr (kEpi == kBack) return launch(k, grid, kThreads, kCg, smem, s, g, *w);
+  else return launch(k, grid, kThreads, kCg, smem, s, g, 0);
 }
 
 template <int kEpi>
-cudaError_t launch_product(Product& g, int cg, int sms, int64_t tiles, cudaStream_t s) {
+cudaError_t launch_product(Product& g, int cg, int sms, int64_t tiles, cudaStream_t s,
+                           const Product* w = nullptr) {
   const int n = (int)std::min<int64_t>(tiles, 1 << 20);
-  if (g.sums > 0)
-    return cg == 2 ? launch_product<2, kEpi, true>(g, sms, n, s) : launch_product<1, kEpi, true>(g, sms, n, s);
-  return cg == 2 ? launch_product<2, kEpi, false>(g, sms, n, s) : launch_product<1, kEpi, false>(g, sms, n, s);
+  if (g.sums > 0 || (w && w->sums > 0))
+    return cg == 2 ? launch_product<2, kEpi, true>(g, w, sms, n, s)
+                   : launch_product<1, kEpi, true>(g, w, sms, n, s);
+  return cg == 2 ? launch_product<2, kEpi, false>(g, w, sms, n, s)
+                 : launch_product<1, kEpi, false>(g, w, sms, n, s);
 }
 
 int64_t ceil_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -1242,15 +1292,15 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     l.vc = ceil_to(div_up(whole, pieces), 256);
     l.ldd = l.vc;
     l.d = take((size_t)(2 * l.planes * l.rpad * l.ldd));
-    // parts of dh's reduction, at least eight blocks each: as few as keep the SMs busy
-    const int64_t units = sms / l.cg, tiles = div_up(N, kRows * l.cg) * div_up(K, l.kbn);
-    const int64_t most = std::min<int64_t>(64, l.vc / 64 * (l.planes == 3 ? 6 : 1) / 8);
-    double best = 0;
-    l.splits = 1;
-    for (int64_t n = 1; tiles > 0 && n <= std::max<int64_t>(1, std::min<int64_t>(most, 4 * units / tiles)); ++n) {
-      const double use = (double)(n * tiles) / (double)(div_up(n * tiles, units) * units);
-      if (use > best + 0.03) best = use, l.splits = n;
-    }
+    // Parts of dh's reduction, at least eight blocks each, so that its tiles last
+    // no longer than a third of what a cluster has to do in all (where two of
+    // three tokens take no part, half of it).
+    const int64_t wide = div_up(K, l.kbn), tile = kRows * l.cg, planes = l.planes == 3 ? 6 : 1;
+    const double blocks = (double)(div_up(N, tile) * wide) * (double)(l.vc / 64) +
+                          (double)(div_up(l.vc, tile) * wide) * (double)div_up(N, 64);
+    const double share = std::max(1.0, blocks * l.cg / sms);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, l.vc / 64 * planes / 8));
+    l.splits = std::min<int64_t>(most, (int64_t)(3.0 * (double)(l.vc / 64) / share) + 1);
     l.ldacc = ceil_to(K, 256);
     if (l.splits > 1 || pieces > 1) l.acc = take((size_t)(4 * l.splits * l.rpad * l.ldacc));
   } else {
@@ -1430,43 +1480,36 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
         !encode_weight(&g.b, a, dt, l, g.bn / cg))
       return cudaErrorUnknown;
     if ((e = launch_product<kGrad>(g, cg, sms, mt * g.nt, s)) != cudaSuccess) return e;
-    if (a.dweight) {
-      Product w = g;
-      w.out = a.dweight;
-      w.ost = a.gsv;
-      w.odt = a.wdt;
-      w.add = a.add;
-      w.asv = a.asv;
-      w.bn = l.kbn;
-      w.nt = (int)div_up(a.K, w.bn);
-      w.a_rows = kRows;
-      w.sums = sums_of(dt, div_up(N, 64));
-      if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
-          !encode(&w.b, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, 64))
-        return cudaErrorUnknown;
-      if ((e = launch_product<kWeight>(w, cg, sms, div_up(vp, rows) * w.nt, s)) != cudaSuccess)
-        return e;
-    }
-    if (a.dhidden && N > 0) {
-      Product w = g;
-      w.out = a.dhidden;
-      w.osb = a.gsb;
-      w.ost = a.gst;
-      w.odt = dt;
-      w.bn = l.kbn;
-      w.nt = (int)div_up(a.K, w.bn);
-      w.kb = (vp + 63) / 64;
-      w.splits = (int)l.splits;
-      w.sums = sums_of(dt, div_up(w.kb, w.splits));
-      w.acc = l.acc ? (float*)(a.ws + l.acc) : nullptr;
-      w.ldacc = l.ldacc;
-      w.acc_old = v0 > 0;
-      w.acc_new = v0 + vp < a.V || l.splits > 1;
-      if (!encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, a_rows) ||
-          !encode_weight(&w.b, a, dt, l, 64))
-        return cudaErrorUnknown;
-      if ((e = launch_product<kHidden>(w, cg, sms, mt * w.nt * w.splits, s)) != cudaSuccess) return e;
-    }
+    Product h = g, w = g;
+    h.on = a.dhidden && N > 0;
+    h.out = a.dhidden;
+    h.osb = a.gsb;
+    h.ost = a.gst;
+    h.odt = dt;
+    h.kb = (vp + 63) / 64;
+    h.splits = (int)l.splits;
+    h.sums = sums_of(dt, div_up(h.kb, h.splits));
+    h.acc = l.acc ? (float*)(a.ws + l.acc) : nullptr;
+    h.ldacc = l.ldacc;
+    h.acc_old = v0 > 0;
+    h.acc_new = v0 + vp < a.V || l.splits > 1;
+    w.on = a.dweight != nullptr;
+    w.out = a.dweight;
+    w.ost = a.gsv;
+    w.odt = a.wdt;
+    w.add = a.add;
+    w.asv = a.asv;
+    w.sums = sums_of(dt, div_up(N, 64));
+    h.bn = w.bn = l.kbn;
+    h.nt = w.nt = (int)div_up(a.K, l.kbn);
+    h.a_rows = w.a_rows = kRows;
+    if (!encode(&h.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, kRows) ||
+        !encode_weight(&h.b, a, dt, l, 64) ||
+        !encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
+        !encode(&w.b, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, 64))
+      return cudaErrorUnknown;
+    const int64_t tiles = h.on * mt * h.nt * h.splits + w.on * div_up(vp, rows) * w.nt;
+    if ((e = launch_product<kBack>(h, cg, sms, tiles, s, &w)) != cudaSuccess) return e;
   }
   if (!a.dhidden || N == 0) return cudaSuccess;
   const HiddenRows r{l.splits > 1 ? (const float*)(a.ws + l.acc) : nullptr, (int)l.splits,
