@@ -48,6 +48,7 @@ struct Product {
   int bn, nt;     // columns of a tile, tiles of columns
   int kb;         // blocks of the reduction where it is not over the rows
   int on;         // kBack: this product is wanted
+  int least;      // kBack, dW: what the results of a tile take, in blocks
   int splits;     // kBack, dh: parts of the reduction
   int pairs;      // products of planes: 1, or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
@@ -181,6 +182,12 @@ __device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b)
                : "memory");
 }
 
+__device__ __forceinline__ void store_if(uintptr_t p, unsigned v, bool yes) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.b32 [%0], %1;\n}" ::"l"(p),
+               "r"(v), "r"((unsigned)yes)
+               : "memory");
+}
+
 // 32 results of a row, times `scale` plus `add`'s, in 16- or 32-byte stores.
 template <typename T>
 __device__ __forceinline__ void store_row(T* out, const T* add, const float (&v)[32], float scale) {
@@ -206,9 +213,9 @@ __device__ __forceinline__ void store_row(T* out, const T* add, const float (&v)
 
 // Where the rows of a warp's results start, in elements (-1: no row), and half
 // of the results on their turn.
-struct Turn {
+struct alignas(16) Turn {
   int64_t at[32], add_at[32];
-  float v[16 * kTurn];
+  float v[16 * kTurn];  // (or 32 x 16 words)
 };
 
 // A warp's 32 x 32 results, a row a lane, column `c` of the row on, `n` columns
@@ -224,6 +231,42 @@ __device__ __forceinline__ void store_tile(T* out, const T* add, int c, const fl
   if (n >= 32 && __all_sync(~0u, whole)) {
     if (at >= 0) store_row(out + at + c, add ? add + turn.add_at[lane] + c : nullptr, v, scale);
     return;
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (!add && n >= 32) {
+      // pairs of elements in words, two rows a store; a row that starts in the
+      // middle of a word has its pairs put together anew
+      unsigned* words = reinterpret_cast<unsigned*>(turn.v);
+      auto shuffle = [](int r) { return (r & 6) << 1; };  // (for the banks)
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[i + j] * scale;
+        const uint4 w = Storage<T>::pack(f);
+        *reinterpret_cast<uint4*>(words + lane * 16 + ((i / 2) ^ shuffle(lane))) = w;
+      }
+      __syncwarp();
+      const int l = lane & 15, half = lane >> 4;
+      const uintptr_t base = (uintptr_t)(out + c);
+#pragma unroll 4
+      for (int r0 = 0; r0 < 32; r0 += 2) {
+        const int r = r0 + half;
+        const int64_t row = turn.at[r];
+        const unsigned w = words[r * 16 + (l ^ shuffle(r))], before = words[r * 16 + ((l - (l > 0)) ^ shuffle(r))];
+        const uintptr_t to = base + (uintptr_t)(row * 2);
+        const unsigned odd = (unsigned)to & 2u;
+        store_if(to + 4u * l - odd, __funnelshift_l(before, w, odd * 8u), row >= 0 && l >= (int)(odd >> 1));
+      }
+      // the ends of a shifted row: its first element and its last
+      if (at >= 0 && ((uintptr_t)(out + at + c) & 2)) {
+        Storage<T>::store1(out + at + c, v[0] * scale);
+        Storage<T>::store1(out + at + c + 31, v[31] * scale);
+      }
+      __syncwarp();
+      return;
+    }
   }
 #pragma unroll
   for (int h = 0; h < 32; h += 16) {
@@ -580,7 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       j -= mine;
       const int busy = hidden % step, idle = step - busy;  // clusters with one tile more, less
-      const int64_t more = busy && wkb ? (g.kb / g.splits + wkb / 2) / wkb : 0;
+      const int lasts = max(wkb * w.pairs, w.least);
+      const int64_t more = busy ? (g.kb * g.pairs / g.splits + lasts / 2) / lasts : 0;
       const int extra = (int)min((int64_t)weight, more * idle);
       const int at = first - busy, mine2 = first >= busy && extra > at ? (extra - at + idle - 1) / idle : 0;
       const int i = j < mine2 ? at + j * idle : extra + first + (j - mine2) * step;
@@ -1284,13 +1328,15 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
   if (backward) {
     l.coef = take(16 * l.rpad);
     l.target = take(4 * l.rpad);
-    l.bn = l.cg == 2 ? 256 : V >= 2 * 128 * sms ? 128 : 64;
-    l.kbn = l.cg == 2 ? 256 : K > 64 ? 128 : 64;
+    l.kbn = l.cg == 2 || K > 128 ? 256 : K > 64 ? 128 : 64;
     const int64_t whole = ceil_to(V, 256);
     const int64_t fit = std::max<int64_t>(kPieceBytes / (2 * l.planes * l.rpad) / 256 * 256, 2048);
     const int64_t pieces = div_up(whole, fit);
     l.vc = ceil_to(div_up(whole, pieces), 256);
-    l.ldd = l.vc;
+    // one CTA: columns so that the SMs' shares of a piece are even
+    const int64_t waves = div_up(l.vc, (int64_t)sms * 256);
+    l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(256, ceil_to(div_up(l.vc, sms * waves), 32));
+    l.ldd = ceil_to(div_up(ceil_to(l.vc, 64), l.bn) * l.bn, 64);
     l.d = take((size_t)(2 * l.planes * l.rpad * l.ldd));
     // Parts of dh's reduction, at least eight blocks each, so that its tiles last
     // no longer than a third of what a cluster has to do in all (where two of
@@ -1474,7 +1520,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     g.ldd = l.ldd;
     g.bound = bound;
     g.bn = l.bn;
-    g.nt = (vp + g.bn - 1) / g.bn;
+    g.nt = (int)div_up(ceil_to(vp, 64), g.bn);  // (zeros in what dh's last block reads)
     g.a_rows = a_rows;
     if (!encode(&g.a, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, a_rows) ||
         !encode_weight(&g.b, a, dt, l, g.bn / cg))
@@ -1500,6 +1546,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     w.add = a.add;
     w.asv = a.asv;
     w.sums = sums_of(dt, div_up(N, 64));
+    w.least = a.gsv % 8 == 0 && ((uintptr_t)a.dweight & 15) == 0 ? 16 : 24;
     h.bn = w.bn = l.kbn;
     h.nt = w.nt = (int)div_up(a.K, l.kbn);
     h.a_rows = w.a_rows = kRows;
