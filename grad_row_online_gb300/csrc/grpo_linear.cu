@@ -639,11 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kEpi == kBack) return x.weight ? w : g;
     else return g;
   };
-  // (kParts) where the part of a tile's n blocks that starts at k ends: the
-  // small planes' products, whose roundings are small too, are one part
+  // (kParts) where the part of a tile's n blocks that starts at k ends
   auto part_end = [&](const Product& p, int k, int n) {
-    const int small = n - n / p.pairs;
-    return k < small ? small : p.sums ? min(n, k + p.sums) : n;
+    return p.sums ? min(n, k + p.sums * p.pairs) : n;
   };
   const bool two = !kSets || g.bufs == 2;  // tiles in flight
   bool ok = true;
@@ -750,31 +748,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       each([&](const Tile& t, const Product& q, auto amn) {
         constexpr bool kAmn = decltype(amn)::value;
         const int m = t.m0 + (int)rank * kRows, n = t.n0 + (int)rank * half;
-        for (int p = 0; p < q.pairs && ok; ++p) {
-          const int za = q.pairs == 1 ? 0 : kPairs[p][0], zb = q.pairs == 1 ? 0 : kPairs[p][1];
-          for (int k = t.k0; k < t.k1; ++k) {
-            if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
-            uint32_t bar = smem_u32(&s_full[st]);
-            const uint32_t sa = smem + st * stage_bytes, sb = sa + a_bytes;
-            if (one) {
-              if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
-              if (kCg == 2) bar = map_to(bar, 0);
-              if (kAmn) {
-                for (int j = 0; j < kRows; j += 64)
-                  tma_load<kCg>(sa + j * 128u, &q.a, m + j, k * kBlk, za, bar);
-              } else {
-                tma_load<kCg>(sa, &q.a, k * kBlk, m, za, bar);
+        // parts of `sums` blocks, each with its six products of planes: the tiles
+        // of three planes come from memory once
+        const int part = q.sums ? q.sums : t.k1 - t.k0;
+        for (int k0 = t.k0; k0 < t.k1 && ok; k0 += part) {
+          const int k1 = min(t.k1, k0 + part);
+          for (int p = 0; p < q.pairs && ok; ++p) {
+            const int za = q.pairs == 1 ? 0 : kPairs[p][0], zb = q.pairs == 1 ? 0 : kPairs[p][1];
+            for (int k = k0; k < k1; ++k) {
+              if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
+              uint32_t bar = smem_u32(&s_full[st]);
+              const uint32_t sa = smem + st * stage_bytes, sb = sa + a_bytes;
+              if (one) {
+                if (rank == 0) mbar_expect_tx(bar, (a_bytes + b_bytes) * kCg);
+                if (kCg == 2) bar = map_to(bar, 0);
+                if (kAmn) {
+                  for (int j = 0; j < kRows; j += 64)
+                    tma_load<kCg>(sa + j * 128u, &q.a, m + j, k * kBlk, za, bar);
+                } else {
+                  tma_load<kCg>(sa, &q.a, k * kBlk, m, za, bar);
+                }
+                if (kBmn) {
+                  const int y = (kAmn ? 0 : g.v0) + k * kBlk;
+                  for (int j = 0; j < half; j += 64)
+                    tma_load<kCg>(sb + j * 128u, &q.b, n + j, y, zb, bar);
+                } else {
+                  tma_load<kCg>(sb, &q.b, k * kBlk, g.v0 + n, zb, bar);
+                }
               }
-              if (kBmn) {
-                const int y = (kAmn ? 0 : g.v0) + k * kBlk;
-                for (int j = 0; j < half; j += 64)
-                  tma_load<kCg>(sb + j * 128u, &q.b, n + j, y, zb, bar);
-              } else {
-                tma_load<kCg>(sb, &q.b, k * kBlk, g.v0 + n, zb, bar);
-              }
+              __syncwarp();
+              if (++st == g.stages) st = 0, ph ^= 1u;
             }
-            __syncwarp();
-            if (++st == g.stages) st = 0, ph ^= 1u;
           }
         }
       });
