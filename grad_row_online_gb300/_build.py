@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libgrpo_gb300.so")
 NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["grpo_api.cu", "grpo_prep.cu", "grpo_rows.cu", "grpo_reduce.cu",
            "grpo_logps.cu", "grpo_static.cu", "grpo_vocab.cu", "grpo_token.cu", "grpo_clip.cu",
-           "grpo_linear.cu", "grpo_embed.cu"]
+           "grpo_linear.cu", "grpo_linear_few.cu", "grpo_embed.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 FLAGS = [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

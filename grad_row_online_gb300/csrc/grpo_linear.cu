@@ -1176,11 +1176,11 @@ __global__ void __launch_bounds__(256) hidden_kernel(const HiddenRows a) {
     T* out = (T*)a.out + dst / a.T * a.osb + dst % a.T * a.ost;
     const float scale = a.bound ? 1.f / range_scale(*a.bound) : 1.f;
     // (sums are padded to 256 columns)
-    for (int64_t k = threadIdx.x * 4; k < a.K; k += 1024) {
+    if (const int64_t k = (int64_t)blockIdx.y * 1024 + threadIdx.x * 4; k < a.K) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (packed) {
         const float* p = a.acc + (int64_t)r * a.ldacc + k;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < a.splits; ++i) {
           const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)i * a.rpad * a.ldacc);
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
@@ -1229,10 +1229,10 @@ bool encode(CUtensorMap* m, const void* p, bool bf16, int64_t inner, int64_t out
 }
 
 template <typename... Args>
-cudaError_t launch(void (*k)(Args...), int64_t grid, unsigned block, int cluster, int smem,
+cudaError_t launch(void (*k)(Args...), dim3 grid, unsigned block, int cluster, int smem,
                    cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)grid);
+  c.gridDim = grid;
   c.blockDim = dim3(block);
   c.dynamicSmemBytes = smem;
   c.stream = s;
@@ -1296,6 +1296,7 @@ bool pack_weight(const void* w, grpo_dtype_t dt, int64_t V, int64_t sv) {
 // What a call keeps in its workspace.
 struct Layout {
   bool direct;  // kStats: every row is taken, as it lies
+  int few;      // rows of the form for a handful of tokens; 0: another
   int cg, bn;   // CTAs of a tile, its columns (of the vocabulary)
   int kbn;      // columns of a tile of the width
   int64_t rpad, Kp, planes, nt, vc, splits, ldd, ldacc;
@@ -1327,6 +1328,23 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     return at;
   };
   l.idx = take(4 * l.rpad);
+  l.few = few_rows(dt, N, K);
+  if (l.few) {
+    l.direct = !backward;
+    l.ldacc = ceil_to(K, 256);
+    if (backward) {
+      l.coef = take(16 * l.rpad);
+      l.target = take(4 * l.rpad);
+      l.d = take((size_t)(4 * V * l.few));
+      l.splits = few_parts(V, K, sms);
+      l.acc = take((size_t)(4 * l.splits * l.few * l.ldacc));
+    } else {
+      l.xa = take(4 * l.rpad);
+      l.part = take((size_t)(16 * sms * l.rpad));
+    }
+    l.total = o;
+    return l;
+  }
   l.hidden = take((size_t)(2 * l.planes * l.rpad * l.Kp));
   l.weight = take(pack_weight(weight, dt, V, sv) ? (size_t)(2 * l.planes * ceil_to(V, kPad) * l.Kp) : 0);
   if (backward) {
@@ -1382,6 +1400,18 @@ cudaError_t pack(const LinearArgs& a, grpo_dtype_t dt, const Layout& l, const in
 
 // Parts of a reduction of `kb` blocks: none where one accumulator holds it.
 int sums_of(grpo_dtype_t dt, int64_t kb) { return dt == GRPO_F32 && kb > kSumsF32 ? kSumsF32 : 0; }
+
+FewArgs few(const LinearArgs& a, const Layout& l) {
+  FewArgs f{};
+  f.hidden = a.hidden;
+  f.T = a.T, f.sb = a.sb, f.st = a.st;
+  f.N = (int)(a.B * a.T);
+  f.rows = l.few;
+  f.weight = a.weight;
+  f.V = a.V, f.K = a.K, f.sv = a.sv;
+  f.s2 = a.s2;
+  return f;
+}
 
 Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   Product g{};
@@ -1440,6 +1470,20 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
     p.out_stats = a.stats;
     if ((e = launch(rows_kernel, div_up(N, kPrepRows), 1024, 1, 0, s, p)) != cudaSuccess) return e;
   }
+  auto fold = [&](const float4* part, const float* xa, int parts) {
+    const FoldRows f{part, xa, count, (int)N, parts, (int)l.rpad, (int)N, idx, a.actions,
+                     l.direct ? a.mask : nullptr, a.V, a.inv_t, a.s2, a.logps, a.entropy, a.stats, status};
+    return launch(fold_kernel, div_up(N, 32), 32 * kFoldWarps, 1, 0, s, f);
+  };
+  if (l.few) {
+    FewArgs f = few(a, l);
+    f.actions = a.logps ? a.actions : nullptr;
+    f.part = (float4*)(a.ws + l.part);
+    f.xa = (float*)(a.ws + l.xa);
+    f.rpad = (int)l.rpad;
+    if ((e = launch_few_stats(f, sms, s)) != cudaSuccess) return e;
+    return fold(f.part, f.xa, sms);
+  }
   // rows that tile loads can take where they are
   const int64_t apart = a.T == 1 ? a.sb : a.st;
   const bool in_place = l.direct && dt != GRPO_F32 && ((uintptr_t)a.hidden & 15) == 0 &&
@@ -1473,10 +1517,7 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   if (!mapped || !encode_weight(&g.b, a, dt, l, g.bn / l.cg)) return cudaErrorUnknown;
   const int64_t tiles = div_up(N, kRows * l.cg) * g.nt;
   if ((e = launch_product<kStats>(g, l.cg, sms, tiles, s)) != cudaSuccess) return e;
-  const FoldRows f{g.part, g.xa, count, g.rows, l.direct ? (int)std::min<int64_t>(sms, tiles) : g.nt,
-                   g.rpad, (int)N, idx, a.actions, l.direct ? a.mask : nullptr, a.V, a.inv_t, a.s2,
-                   a.logps, a.entropy, a.stats, status};
-  return launch(fold_kernel, div_up(N, 32), 32 * kFoldWarps, 1, 0, s, f);
+  return fold(g.part, g.xa, l.direct ? (int)std::min<int64_t>(sms, tiles) : g.nt);
 }
 
 cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_t s) {
@@ -1503,6 +1544,36 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
   cudaError_t e = N > 0 ? launch(rows_kernel, div_up(N, kPrepRows), 1024, 1, 0, s, p)
                         : cudaMemsetAsync(h, 0, sizeof(Header), s);
   if (e != cudaSuccess) return e;
+  const bool hidden = a.dhidden && N > 0;
+  // the parts of dh joined, zeros where there is no gradient
+  auto finish = [&](const float* acc, int parts, int64_t rows, const unsigned* bound) {
+    if (!hidden) return cudaSuccess;
+    const HiddenRows r{acc, parts, (int)rows, (int)N, a.K,
+                       l.ldacc, p, idx, &h->count, bound, a.dhidden, std::max<int64_t>(a.T, 1), a.gsb,
+                       a.gst, a.skip_masked};
+    auto* k = dt == GRPO_F32    ? hidden_kernel<float>
+              : dt == GRPO_BF16 ? hidden_kernel<__nv_bfloat16>
+                                : hidden_kernel<__half>;
+    return launch(k, dim3((unsigned)std::min<int64_t>(2 * N, sms * 8), (unsigned)div_up(a.K, 1024)), 256, 1, 0,
+                  s, r);
+  };
+  if (l.few) {
+    FewArgs f = few(a, l);
+    f.idx = idx;
+    f.count = &h->count;
+    f.coef = p.coef;
+    f.target = p.target;
+    f.d = (float*)(a.ws + l.d);
+    f.acc = hidden ? (float*)(a.ws + l.acc) : nullptr;
+    f.ldacc = l.ldacc;
+    f.dweight = a.dweight;
+    f.gsv = a.gsv;
+    f.add = a.add;
+    f.asv = a.asv;
+    if ((e = launch_few_grad(f, sms, s)) != cudaSuccess) return e;
+    if ((e = launch_few_back(f, (int)l.splits, s)) != cudaSuccess) return e;
+    return finish(f.acc, (int)l.splits, l.few, nullptr);
+  }
   if ((e = pack(a, dt, l, idx, &h->count, true, sms, s)) != cudaSuccess) return e;
   const bool bf16 = dt != GRPO_F16;
   const unsigned* bound = dt == GRPO_F16 ? &h->bound : nullptr;
@@ -1562,14 +1633,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     const int64_t tiles = h.on * mt * h.nt * h.splits + w.on * div_up(vp, rows) * w.nt;
     if ((e = launch_product<kBack>(h, cg, sms, tiles, s, &w)) != cudaSuccess) return e;
   }
-  if (!a.dhidden || N == 0) return cudaSuccess;
-  const HiddenRows r{l.splits > 1 ? (const float*)(a.ws + l.acc) : nullptr, (int)l.splits,
-                     (int)l.rpad, (int)N, a.K, l.ldacc, p, idx, &h->count, bound, a.dhidden,
-                     std::max<int64_t>(a.T, 1), a.gsb, a.gst, a.skip_masked};
-  auto* k = dt == GRPO_F32    ? hidden_kernel<float>
-            : dt == GRPO_BF16 ? hidden_kernel<__nv_bfloat16>
-                              : hidden_kernel<__half>;
-  return launch(k, std::min<int64_t>(2 * N, sms * 8), 256, 1, 0, s, r);
+  return finish(l.splits > 1 ? (const float*)(a.ws + l.acc) : nullptr, (int)l.splits, l.rpad, bound);
 }
 
 }  // namespace grpo

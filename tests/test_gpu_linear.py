@@ -325,6 +325,35 @@ def test_the_same_bits_whatever_the_workspace_holds(dtype, N):
         g.grpo_linear_logps_grad(h, W, ids, mask, s["stats"], grad_logps=w, workspace=wb[:-256])
 
 
+@pytest.mark.parametrize("N,K,V", [(2, 4096, 300), (16, 4100, 515), (9, 33, 1000), (16, 1024, 4097),
+                                   (17, 64, 100), (1, 60000, 65), (4, 1, 7), (8, 129, 2051)])
+def test_few_tokens_in_single_precision(N, K, V):
+    """One to sixteen tokens, and just beyond: every form of the gradient."""
+    h, W, ids, mask, w, b = make(N, K, V, "f32", seed=K, pad=K % 3)
+    mask[0], w[0] = True, 0.5
+    s = scores(h, W, ids, mask)
+    check_scores(s, forward(h, W, ids, mask))
+    kw = dict(grad_logps=w, grad_entropy=b, entropy=s["entropy"])
+    call = lambda **more: g.grpo_linear_logps_grad(h, W, ids, mask, s["stats"], **kw, **more)  # noqa: E731
+    full = call()
+    check_gradient(full, gradient(h, W, ids, mask, w, b))
+    assert torch.equal(call(grad_weight=None)["grad_hidden"], full["grad_hidden"])
+    assert torch.equal(call(grad_hidden=False)["grad_weight"], full["grad_weight"])
+    add = torch.randn((V, K), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    r = call(add_weight=add)
+    check_gradient(r, gradient(h, W, ids, mask, w, b, add=add))
+    room = torch.full((V, K + 3), 7.0, device="cuda")
+    room[:, 1:K + 1] = add
+    call(add_weight=room[:, 1:K + 1], grad_weight=room[:, 1:K + 1])
+    assert torch.equal(room[:, 1:K + 1], r["grad_weight"])
+    assert bool((room[:, 0] == 7).all()) and bool((room[:, K + 1:] == 7).all())
+    for fill in (255, 127):
+        ws = torch.full((g.grpo_linear_workspace_size(h, W),), fill, dtype=torch.uint8, device="cuda")
+        wb = torch.full((g.grpo_linear_workspace_size(h, W, True),), fill, dtype=torch.uint8, device="cuda")
+        again = g.grpo_linear_logps(h, W, ids, mask, want_entropy=True, want_stats=True, workspace=ws)
+        assert same((again, call(workspace=wb)), (s, full))
+
+
 def test_outputs_asked_for_alone():
     h, W, ids, mask, _, _ = make(300, 64, 400, "bf16")
     full = scores(h, W, ids, mask)
