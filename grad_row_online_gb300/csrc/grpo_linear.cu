@@ -1299,6 +1299,7 @@ struct Layout {
   int few;      // rows of the form for a handful of tokens; 0: another
   int cg, bn;   // CTAs of a tile, its columns (of the vocabulary)
   int kbn;      // columns of a tile of the width
+  int sets;     // direct: of accumulators that a reduction is cut into
   int64_t rpad, Kp, planes, nt, vc, splits, ldd, ldacc;
   size_t idx, coef, target, xa, part, hidden, weight, d, acc, total;
 };
@@ -1309,7 +1310,8 @@ struct Layout {
 // 4e-6 at 2,048 and 8e-6 at 4,096, where parts of 2,048 make it 2e-6 and cost
 // 8 % (4,096 x 4,096 x 128,256: 2,069 and 2,244 us).  Sums of fp32 operands are
 // as exact as chains of fp32 additions with 8 (and 5e-5 off in the gradients of
-// sharp log-probs without parts).
+// sharp log-probs without parts).  The gradient of 16-bit operands is rounded
+// to 16 bits, 2e-3 of it, and takes one sum.
 static constexpr int kSumsF32 = 8, kSumsWide = 32;
 static constexpr int64_t kPieceBytes = 512ll << 20;  // of the logits' gradient
 
@@ -1373,9 +1375,15 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     if (l.splits > 1 || pieces > 1) l.acc = take((size_t)(4 * l.splits * l.rpad * l.ldacc));
   } else {
     l.direct = N <= kRows;
+    // one CTA: a sum of all products in parts, each with its own
+    // accumulators, for which tensor memory has room here.  Two of them, and
+    // four of 128 columns where a 16-bit width passes 2,048: 64 x 4,096 x 151,936
+    // takes 190 us where two sets of 256 columns take 186, and its entropies are
+    // off by 1.4e-6 where 3.1e-6; 1 x 2,048 x 32,768 33 where 31.
+    l.sets = !l.direct ? 1 : dt != GRPO_F32 && l.Kp > 64 * kSumsWide ? 4 : 2;
     // one CTA: columns so that the SMs' shares of the vocabulary are even
-    const int64_t waves = div_up(V, (int64_t)sms * 256);
-    l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(256, ceil_to(div_up(V, sms * waves), 16));
+    const int64_t wide = l.sets == 4 ? 128 : 256, waves = div_up(V, (int64_t)sms * wide);
+    l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(wide, ceil_to(div_up(V, sms * waves), 16));
     l.nt = div_up(V, l.bn);
     l.xa = take(4 * l.rpad);
     l.part = take((size_t)(16 * (l.direct ? std::min<int64_t>(l.nt, sms) : l.nt) * l.rpad));
@@ -1500,13 +1508,12 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   g.want_entropy = a.entropy != nullptr;
   g.bn = l.bn;
   g.nt = (int)l.nt;
-  if (dt != GRPO_F32 && g.kb > (l.direct ? 2 * kSumsWide : kSumsWide)) g.sums = kSumsWide;
+  if (dt != GRPO_F32 && g.kb > l.sets * kSumsWide) g.sums = kSumsWide;
   if (l.direct) {
     g.run = 1;
     g.a_rows = (int)ceil_to(N, 8);
-    // two sums of half of the products each: an accumulator is rounded towards
-    // zero at every step, and the memory for the second is free here
-    if (!g.sums) g.kc = std::min(2, g.kb * g.pairs);
+    if (!g.sums) g.kc = std::min(l.sets, g.kb * g.pairs);
+    if (l.sets == 4) g.slot = 128;
     g.bufs = g.kc == 1 ? 2 : 1;
   }
   const bool mapped =

@@ -478,19 +478,28 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
  *   weight          : [V,K] of the same dtype, row v at element v stride_v
  *                     (stride_v >= K where V > 1); must not overlap an output.
  *   action_ids, completion_mask, temperature, logps, entropy, stats, status_ws:
- *                     as for grpo_token_logps; a masked token's hidden state is
- *                     not read.
- * Products of bf16 and f16 are exact and summed in fp32; f32 operands are split
- * into three bf16 parts, whose products are formed but for those below 2^-26
- * of |h_k W_vk|.  A row with a NaN or +inf logit, or only -inf, has no
- * distribution: logp, entropy and Z are NaN.  (An infinite f32 operand makes
- * its logits NaN.)  Results are bitwise reproducible.
+ *                     as for grpo_token_logps; a masked token's hidden state,
+ *                     whatever it holds, has no influence (it is read where a
+ *                     call has no more than 128 tokens).
+ * Products of bf16 and f16 are exact and summed in fp32, at most 2,048 of them
+ * in one sum of the tensor cores (which round towards zero at each step of 16).
+ * f32 operands are multiplied in fp32 up to 16 tokens (fewer where K passes
+ * 6,400); beyond, they are split into three bf16 parts, whose products are
+ * formed but for those below 2^-26 of |h_k W_vk| (operands below 1e-33 keep
+ * fewer bits).  A row with a NaN or +inf logit, or only -inf, has no
+ * distribution: logp, entropy and Z are NaN; logits of -inf have p = 0.  (An
+ * infinite f32 operand makes its logits infinite or NaN.)  Results are bitwise
+ * reproducible; those of a token may differ in their last bits between calls
+ * with other numbers of tokens.
  * Sizes: B T and V at most 2^31 - 1025, K at most 2^20, and
  * ceil(B T / 128) ceil(V / 64) < 2^31.
  * ws: grpo_linear_workspace_size(..., 0) bytes, 256-byte aligned, needs no
  * initialisation: the active tokens' hidden states side by side, 16 bytes a
- * token for each 64 to 256 words of the vocabulary, and a copy of the weight
- * where its rows are not 16-byte aligned or f32. */
+ * token for each 256 words of the vocabulary (up to 128 tokens, for each SM at
+ * most), and a copy of the weight where its rows are not 16-byte aligned, or
+ * its three parts where it is f32 (neither with f32 and up to 16 tokens).  For
+ * the gradient also the logits' gradient of a piece of the vocabulary, up to
+ * 512 MB of it, and fp32 sums of grad_hidden. */
 size_t grpo_linear_workspace_size(const void *weight, grpo_dtype_t dt, int64_t B, int64_t T,
                                   int64_t K, int64_t V, int64_t stride_v, int32_t backward);
 
@@ -507,7 +516,8 @@ grpo_status_t grpo_linear_logps(const void *hidden, grpo_dtype_t dt, int64_t B, 
  *   dL/dh_k = sum_v d_v W_vk,   dL/dW_vk = add_vk + sum over tokens of d_v h_k
  * The logits are formed again, and d exists for a piece of the vocabulary at a
  * time, rounded to the operands' dtype for its products (f32: three bf16
- * parts; f16: scaled by a power of two that keeps its values in range).
+ * parts, or fp32 as above; f16: scaled by a power of two that keeps its values
+ * in range).
  *   stats, entropy, grad_logps, grad_entropy, status_ws: as for
  *                     grpo_token_logps_grad.
  *   grad_hidden     : [B,T,K] of dtype `dt`, rows at b grad_stride_b +
@@ -520,9 +530,10 @@ grpo_status_t grpo_linear_logps(const void *hidden, grpo_dtype_t dt, int64_t B, 
  *   add_weight      : [V,K] of grad_weight's type, rows add_stride_v apart,
  *                     NULL = 0; may be grad_weight itself with the same stride
  *                     (accumulation in place), and must not overlap it otherwise.
- * Outputs must not overlap inputs otherwise.  An id outside [0, V) on an active token with dlogp != 0,
- * or a row without a distribution, makes its row of grad_hidden and
- * all of grad_weight NaN (the former sets GRPO_ERR_ACTION_RANGE).
+ * Outputs must not overlap inputs otherwise.  An id outside [0, V) on an active
+ * token with dlogp != 0, or a row without a distribution, makes its row of
+ * grad_hidden and all of grad_weight NaN (the former sets
+ * GRPO_ERR_ACTION_RANGE).
  * ws: grpo_linear_workspace_size(..., 1) bytes. */
 grpo_status_t grpo_linear_logps_grad(
     const void *hidden, grpo_dtype_t dt, int64_t B, int64_t T, int64_t K, int64_t stride_b,
@@ -551,8 +562,8 @@ grpo_status_t grpo_embed_tokens(const void *weight, grpo_dtype_t dt, int64_t V, 
                                 void *stream);
 
 /* Its gradient: grad_weight_v = add_v + scale sum over tokens n with id_n = v
- * of grad_n (n = b T + t).  The tokens are sorted by id, each id's rows summed in fp32 in
- * an order that depends on the ids alone, and rounded once.
+ * of grad_n (n = b T + t).  The tokens are sorted by id, each id's rows summed
+ * in fp32 in an order that depends on the ids alone, and rounded once.
  *   grad            : [B,T,K] of dtype `dt`, row (b, t) at b stride_b +
  *                     t stride_t.
  *   token_ids, token_mask, scale, status_ws: as above; masked tokens and ids
@@ -571,7 +582,8 @@ size_t grpo_embed_workspace_size(int64_t N, int64_t K, int64_t V);
 grpo_status_t grpo_embed_tokens_grad(const void *grad, grpo_dtype_t dt, int64_t B, int64_t T,
                                      int64_t K, int64_t stride_b, int64_t stride_t,
                                      const int64_t *token_ids, const uint8_t *token_mask,
-                                     int64_t V, float scale, const void *add, int64_t add_stride_v, void *grad_weight,
+                                     int64_t V, float scale, const void *add,
+                                     int64_t add_stride_v, void *grad_weight,
                                      grpo_dtype_t grad_weight_dt, int64_t out_stride_v,
                                      void *status_ws, void *ws, size_t ws_bytes, void *stream);
 

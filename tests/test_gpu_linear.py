@@ -62,6 +62,7 @@ SIZES = [  # N, K, V, padding of the rows, temperature
     (1, 128, 1000, 0, 1.0), (64, 256, 777, 0, 0.8), (65, 72, 64, 8, 1.3), (127, 100, 513, 4, 1.0),
     (129, 64, 256, 0, 1.0), (200, 130, 65, 0, 1.0), (256, 512, 2048, 0, 1.0), (300, 65, 5003, 7, 0.7),
     (513, 256, 300, 0, 1.0), (700, 1021, 4999, 0, 1.0), (1030, 320, 6001, 0, 1.0), (40, 2048, 9001, 0, 1.0),
+    (24, 4100, 1111, 0, 0.9), (7, 8320, 333, 0, 1.0),
 ]
 
 
