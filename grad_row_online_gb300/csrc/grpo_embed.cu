@@ -21,7 +21,10 @@ __device__ __forceinline__ void launched_early() {
 }
 
 // A thread takes a vector of `kPer` rows one behind the other, a CTA up to 256
-// vectors of them: the rows' loads are in flight together.
+// vectors of them: the rows' loads are in flight together.  A memory-bound copy
+// (a scale of 1 leaves a row's bits as they are): 65,536 tokens of 2,048 bf16
+// in 61 us, 268 MB written and what of the weight is not in L2 read; 64 tokens
+// 4 us, a launch.
 template <typename T, int kPer>
 __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int slices) {
   constexpr int kVec = Storage<T>::kVec;
@@ -129,7 +132,10 @@ __device__ __forceinline__ void absent_rows(const SumArgs& a, int64_t first) {
 // ---------------------------------------------------------------- sort
 // Stable sort of (id, token) by id, least significant digits first; tokens
 // that take no part get the id V and end behind the others.  A CTA takes a
-// chunk, each of its warps a part of that in order.
+// chunk, each of its warps a part of that in order.  Digits of up to nine bits:
+// two passes for 151,936 words, of two kernels each (one up to 4,096 tokens,
+// whose only CTA keeps the counts), 5 to 9 us a kernel, latency: counts, a scan
+// over the chunks, then a warp's 32 tokens at a time.
 static constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 static constexpr int kMaxDigit = 9;
 static_assert(1 << kMaxDigit <= kSortThreads, "a thread has one digit");
@@ -277,7 +283,10 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs a) {
 // A CTA adds up a chunk of the sorted tokens, its threads a vector of columns
 // each.  An id whose tokens lie in one chunk is done; the parts of one that
 // goes on to other chunks are joined by join_kernel in the chunks' order.
-// Behind those CTAs come the ones that fill the rows of absent ids.
+// Behind those CTAs come the ones that fill the rows of absent ids.  Bound by
+// memory: 38,881 tokens of 2,048 bf16 into 151,936 words, 754 MB, in 117 us
+// (6.4 TB/s).  32 tokens a chunk: a frequent id's tokens are spread over as many
+// CTAs as they fill chunks, and eight rows' loads are in flight a thread.
 static constexpr int kSumChunk = 32;
 
 // kVec elements of what is added to a row, as they lie: one or two vectors
@@ -379,7 +388,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
 
 // Ids that go on from one chunk to others: a CTA looks at a chunk for one that
 // begins there; four warps take a quarter of its parts each, a lane a vector
-// of columns.
+// of columns.  Latency, 19 us for 32,768 tokens: the most frequent id's parts, a
+// quarter of them one behind the other in each warp.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int slices) {
   constexpr int kVec = Storage<T>::kVec;
