@@ -471,7 +471,8 @@ Layout layout(int64_t N, int64_t K, int64_t V) {
   l.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   l.bits = (bits + l.passes - 1) / l.passes;
   // one chunk of up to 4,096 tokens, or up to 256 of at least 2,048
-  l.chunk = (int)((std::max<int64_t>(N <= 4096 ? N : 2048, (N + 255) / 256) + kSortThreads - 1) / kSortThreads * kSortThreads);
+  l.chunk = (int)((std::max<int64_t>(N <= 4096 ? std::max<int64_t>(N, 1) : 2048, (N + 255) / 256) +
+                   kSortThreads - 1) / kSortThreads * kSortThreads);
   l.chunks = (int)((N + l.chunk - 1) / l.chunk);
   l.sums = (int)((N + kSumChunk - 1) / kSumChunk);
   size_t o = 0;

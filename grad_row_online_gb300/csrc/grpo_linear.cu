@@ -1537,7 +1537,7 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   const int64_t apart = a.T == 1 ? a.sb : a.st;
   const bool in_place = l.direct && dt != GRPO_F32 && ((uintptr_t)a.hidden & 15) == 0 &&
                         (a.T == 1 || a.B == 1 || a.sb == a.T * a.st) &&
-                        (N == 1 || (apart % 8 == 0 && apart >= 8));
+                        (N == 1 || (apart % 8 == 0 && apart >= 8 && apart <= (int64_t)1 << 36));
   if ((e = pack(a, dt, l, idx, count, !in_place, sms, s)) != cudaSuccess) return e;
   Product g = base(a, dt, l);
   g.count = count;

@@ -79,6 +79,11 @@ def test_workspace_sizes(lib):  # noqa: F811
     assert lib.grpo_embed_workspace_size(-1, 64, 100) == 0
     assert lib.grpo_embed_workspace_size(10, 64, 0) == 0
     assert lib.grpo_embed_workspace_size(10, 64, 100) % 256 == 0
+    # no tokens: what the calls without any take
+    assert lib.grpo_embed_workspace_size(0, 64, 100) % 256 == 0 < lib.grpo_embed_workspace_size(0, 64, 100)
+    for backward in (0, 1):
+        for dt in (0, 1, 2):
+            assert size(FAKE, dt, 0, 5, 64, 100, 64, backward) > 0 and size(FAKE, dt, 1, 1, 1, 1, 1, backward) > 0
 
 
 def _embed(lib, dt=1, V=100, K=64, sv=64, W=FAKE, ids=FAKE, mask=None, B=2, T=3, scale=1.0, out=2 * FAKE, sb=192,
