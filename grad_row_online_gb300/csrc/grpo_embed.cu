@@ -411,48 +411,34 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   }
 }
 
-// Ids that go on from one chunk to others: a CTA looks at a chunk for one that
-// begins there; four warps take a quarter of its parts each, a lane a vector
-// of columns.  Latency, 19 us for 32,768 tokens: the most frequent id's parts, a
-// quarter of them one behind the other in each warp.
-template <typename T, typename O>
-__global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int slices) {
-  constexpr int kVec = Storage<T>::kVec;
-  __shared__ int s_end;
-  __shared__ float s_sum[kSumThreads / 32][32][kVec];
-  launched_early();
-  const unsigned part = blockIdx.x / (unsigned)slices;
-  const int c = part, slice = blockIdx.x - part * slices;
-  const int64_t next = (int64_t)(c + 1) * kSumChunk;
-  if (next >= a.N) return;
-  // only where the id goes on and did not come from before
+// Ids that go on from one chunk to others, each joined from the chunk c where
+// it begins: of parts 0 (chunk c's) .. n - 1.
+//
+// Most have two parts or three: a warp looks at a chunk for one that begins
+// there, a lane has a vector of columns.  Ids of more than kLong parts are left
+// to the first CTAs, which look for them at kLongChunks chunks each; their four
+// warps take a quarter of the parts.  Latency: 10 us for 38,881 tokens of 2,048
+// bf16, the most frequent id's; 17 with a CTA for every chunk and 256 columns,
+// of which most had little to do and waited for a place.
+static constexpr int kLong = 16, kLongChunks = 64;
+
+// the id that begins in chunk c, or before it in the array, and goes on; -1: none
+__device__ __forceinline__ int goes_on(const SumArgs& a, int64_t c) {
+  const int64_t next = (c + 1) * kSumChunk;
+  if (next >= a.N) return -1;
   const int id = a.sorted[next - 1].x, after = a.sorted[next].x;
-  const int first = c > 0 ? a.sorted[next - kSumChunk - 1].x : -1;
-  if (id >= a.V || after != id || first == id) return;
-  // the chunk in which it ends: the first whose successor starts with another id
-  int last = c + 1;
-  for (;; last += kSumThreads) {
-    const int64_t i = ((int64_t)last + threadIdx.x + 1) * kSumChunk;
-    const bool ends = i >= a.N || a.sorted[i].x != id;
-    if (threadIdx.x == 0) s_end = kSumThreads;
-    __syncthreads();
-    if (ends) atomicMin(&s_end, (int)threadIdx.x);
-    __syncthreads();
-    const int end = s_end;
-    __syncthreads();
-    if (end < kSumThreads) {
-      last += end;
-      break;
-    }
-  }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t k = ((int64_t)slice * 32 + lane) * kVec;
-  const int cols = (int)max((int64_t)0, min((int64_t)kVec, a.K - k));
-  // parts 0 (this chunk's) .. last - c, a quarter of them each, in order
-  const int64_t parts = last - c + 1, from = parts * warp / 4, to = parts * (warp + 1) / 4;
-  float f[kVec];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) f[i] = 0.f;
+  const int before = c > 0 ? a.sorted[next - kSumChunk - 1].x : -1;
+  return id >= a.V || after != id || before == id ? -1 : id;
+}
+// whether it ends in chunk c
+__device__ __forceinline__ bool ends_in(const SumArgs& a, int id, int64_t c) {
+  const int64_t i = (c + 1) * kSumChunk;
+  return i >= a.N || a.sorted[i].x != id;
+}
+
+template <int kVec>
+__device__ __forceinline__ void add_parts(const SumArgs& a, int64_t c, int64_t from, int64_t to, int64_t k,
+                                          int cols, float (&f)[kVec]) {
   if (cols == kVec && (a.K & 3) == 0) {
 #pragma unroll 4
     for (int64_t d = from; d < to; ++d) {
@@ -464,6 +450,7 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int 
       }
     }
   } else {
+#pragma unroll 4
     for (int64_t d = from; d < to; ++d) {
       const float* q = a.parts + ((c + d) * 2 + (d == 0)) * a.K + k;
 #pragma unroll
@@ -471,17 +458,77 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int 
         if (i < cols) f[i] += q[i];
     }
   }
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kSumThreads) join_kernel(const SumArgs a, int slices, int longs) {
+  constexpr int kVec = Storage<T>::kVec, kWarps = kSumThreads / 32;
+  __shared__ int s_end;
+  __shared__ unsigned s_long[kLongChunks / 32];
+  __shared__ float s_sum[kWarps][32][kVec];
+  launched_early();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float f[kVec];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) s_sum[warp][lane][i] = f[i];
-  __syncthreads();
-  if (warp != 0 || cols == 0) return;
-#pragma unroll
-  for (int w = 1; w < kSumThreads / 32; ++w)
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] += s_sum[w][lane][i];
+  for (int i = 0; i < kVec; ++i) f[i] = 0.f;
   Addend<T, O> add;
-  if (a.add) add.load(a, id, k, cols);
-  finish<T, O>(a, id, k, cols, f, add);
+  if ((int)blockIdx.x >= longs) {
+    const int64_t u = ((int64_t)blockIdx.x - longs) * kWarps + warp, c = u / slices;
+    const int id = goes_on(a, c);
+    if (id < 0) return;
+    const unsigned ends = __ballot_sync(~0u, lane >= kLong || ends_in(a, id, c + 1 + lane));
+    const int parts = __ffs(ends) + 1;
+    const int64_t k = ((u - c * slices) * 32 + lane) * kVec;
+    const int cols = (int)min((int64_t)kVec, a.K - k);
+    if (parts > kLong + 1 || cols <= 0) return;
+    if (a.add) add.load(a, id, k, cols);
+    add_parts(a, c, 0, parts, k, cols, f);
+    finish<T, O>(a, id, k, cols, f, add);
+    return;
+  }
+  const int group = blockIdx.x / slices;
+  const int64_t k = ((int64_t)(blockIdx.x - group * slices) * 32 + lane) * kVec;
+  const int cols = (int)max((int64_t)0, min((int64_t)kVec, a.K - k));
+  if (warp < kLongChunks / 32) {
+    const int64_t c = (int64_t)group * kLongChunks + threadIdx.x;
+    const int id = goes_on(a, c);
+    const unsigned found = __ballot_sync(~0u, id >= 0 && !ends_in(a, id, c + kLong));
+    if (lane == 0) s_long[warp] = found;
+  }
+  __syncthreads();
+  for (int w = 0; w < kLongChunks / 32; ++w) {
+    for (unsigned left = s_long[w]; left; left &= left - 1) {
+      const int64_t c = (int64_t)group * kLongChunks + w * 32 + __ffs(left) - 1;
+      const int id = a.sorted[(c + 1) * kSumChunk].x;
+      int64_t last = c + 1 + kLong;
+      for (;; last += kSumThreads) {
+        if (threadIdx.x == 0) s_end = kSumThreads;
+        __syncthreads();
+        if (ends_in(a, id, last + threadIdx.x)) atomicMin(&s_end, (int)threadIdx.x);
+        __syncthreads();
+        const int end = s_end;
+        __syncthreads();
+        if (end < kSumThreads) {
+          last += end;
+          break;
+        }
+      }
+      const int64_t parts = last - c + 1;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) f[i] = 0.f;
+      add_parts(a, c, parts * warp / kWarps, parts * (warp + 1) / kWarps, k, cols, f);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) s_sum[warp][lane][i] = f[i];
+      __syncthreads();
+      if (warp != 0 || cols == 0) continue;
+#pragma unroll
+      for (int v = 1; v < kWarps; ++v)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) f[i] += s_sum[v][lane][i];
+      if (a.add) add.load(a, id, k, cols);
+      finish<T, O>(a, id, k, cols, f, add);
+    }
+  }
 }
 
 struct Layout {
@@ -564,7 +611,10 @@ cudaError_t sorted_sums(SortArgs p, SumArgs a, const Layout& l, char* ws, cudaSt
   e = launch(k, (int64_t)a.sums + absent, kSumThreads, 0, s, a);
   if (e != cudaSuccess || l.sums < 2) return e;
   const int joins = (int)((a.K + kJoin - 1) / kJoin);
-  return launch(join_kernel<T, O>, (int64_t)l.sums * joins, kSumThreads, 0, s, a, joins);
+  // (an id of more than kLong + 1 parts takes as many chunks)
+  const int longs = l.sums > kLong + 1 ? (l.sums + kLongChunks - 1) / kLongChunks * joins : 0;
+  const int64_t shorts = ((int64_t)l.sums * joins + kSumThreads / 32 - 1) / (kSumThreads / 32);
+  return launch(join_kernel<T, O>, longs + shorts, kSumThreads, 0, s, a, joins, longs);
 }
 
 template <typename T>

@@ -117,6 +117,27 @@ def test_layouts(dtype, K):
     assert torch.equal(g.grpo_embed_tokens_grad(row, ids, V, mask), g.grpo_embed_tokens_grad(row.contiguous(), ids, V, mask))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [40, 1021, 264])
+@pytest.mark.parametrize("first", [0, 1, 31])
+def test_ids_over_many_chunks(dtype, K, first):
+    """Runs of an id around 16, 17 and 18 chunks of 32 sorted tokens, and long
+    ones side by side, from each place in a chunk."""
+    runs = [first, 512, 544, 513, 545, 576, 577, 543, 31, 33, 64, 3, 1, 70, 2100, 608, 4500, 640, 5, 1500]
+    V = len(runs) + 1
+    ids = torch.repeat_interleave(torch.arange(len(runs)), torch.tensor(runs))
+    gen = torch.Generator().manual_seed(K)
+    ids = ids[torch.randperm(len(ids), generator=gen)].cuda()
+    grad = torch.randn((len(ids), K), generator=gen).to(DT[dtype]).cuda()
+    d = g.grpo_embed_tokens_grad(grad, ids, V)
+    check_gradient(d, grad, ids, None, V, 1.0)
+    assert torch.equal(g.grpo_embed_tokens_grad(grad, ids, V), d)
+    add = torch.randn((V, K), device="cuda").to(DT[dtype])
+    r = g.grpo_embed_tokens_grad(grad, ids, V, add=add)
+    check_gradient(r, grad, ids, None, V, 1.0, add)
+    assert torch.equal(g.grpo_embed_tokens_grad(grad, ids, V, add=add, out=add), r)
+
+
 @pytest.mark.parametrize("N", [1, 40, 5000, 9000])
 def test_one_id_and_no_id(N):
     """Every token the same word: its rows in every chunk; nothing taking part."""
