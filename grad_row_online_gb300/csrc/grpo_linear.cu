@@ -552,7 +552,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // both products (91 %; the ends of its pieces); 16,384 tokens, 9,209 of them
 // taking part, x 2,048 x 151,936: 2.77 ms, 99.7 %.  Bound by memory up to 128
 // tokens, which take single CTAs with the weight as B: 64 x 4,096 x 32,768 in
-// 50 us, 5.4 TB/s, 64 x 4,096 x 151,936 in 186 us, 6.7 TB/s.  One tensor map
+// 50 us, 5.4 TB/s, 64 x 4,096 x 151,936 in 186 to 190 us, 6.6 TB/s.  One tensor map
 // a load of 64 elements (128 bytes) a row: what the swizzle holds; 6 to 12
 // stages of them in flight.
 //
