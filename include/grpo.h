@@ -519,7 +519,10 @@ grpo_status_t grpo_linear_logps(const void *hidden, grpo_dtype_t dt, int64_t B, 
  * parts, or fp32 as above; f16: scaled by a power of two that keeps its values
  * in range).
  *   stats, entropy, grad_logps, grad_entropy, status_ws: as for
- *                     grpo_token_logps_grad.
+ *                     grpo_token_logps_grad; stats and entropy of
+ *                     grpo_linear_logps for the same tensors (statistics of
+ *                     logits that were rounded otherwise bring their error
+ *                     into every p of a row).
  *   grad_hidden     : [B,T,K] of dtype `dt`, rows at b grad_stride_b +
  *                     t grad_stride_t, not overlapping; nullable.  Rows of
  *                     masked tokens and of tokens without a gradient are set
