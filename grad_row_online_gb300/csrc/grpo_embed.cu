@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "grpo_embed.cuh"
+#include "grpo_index.cuh"
 #include "grpo_vec.cuh"
 
 namespace grpo {
@@ -138,7 +139,6 @@ __device__ __forceinline__ void absent_rows(const SumArgs& a, int64_t first) {
 // Up to 4,096 tokens one CTA does all passes in one kernel: the gradient of
 // 1,000 tokens of 512 bf16 into 32,000 words takes 22.9 us, 24.9 with a kernel
 // a pass.
-static constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 static constexpr int kMaxDigit = 9;
 static_assert(1 << kMaxDigit <= kSortThreads, "a thread has one digit");
 
@@ -191,8 +191,7 @@ __device__ __forceinline__ void count_digits(const SortArgs& a, int (*s)[1 << kM
                                              bool first) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, digits = 1 << a.bits;
   for (int i = threadIdx.x; i < kSortWarps << kMaxDigit; i += kSortThreads) (&s[0][0])[i] = 0;
-  const int part = a.chunk / kSortWarps, from = blockIdx.x * a.chunk + warp * part;
-  const int end = min(from + part, a.N);
+  const auto [from, end] = sort_part(a.chunk, (int)blockIdx.x, warp, a.N);
   int2 key[4];
   sort_keys(a, from + lane, end, first, key);
   __syncthreads();
@@ -257,8 +256,7 @@ __device__ __forceinline__ void place(const SortArgs& a, int (*s)[1 << kMaxDigit
     }
   }
   __syncthreads();
-  const int part = a.chunk / kSortWarps, from = blockIdx.x * a.chunk + warp * part;
-  const int end = min(from + part, a.N);
+  const auto [from, end] = sort_part(a.chunk, (int)blockIdx.x, warp, a.N);
   for (int i = from; i < end; i += 128) {
     int2 key[4];
     sort_keys(a, i + lane, end, false, key);
@@ -542,9 +540,7 @@ Layout layout(int64_t N, int64_t K, int64_t V) {
   while (bits < 31 && (V >> bits) != 0) ++bits;  // ids 0 .. V
   l.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   l.bits = (bits + l.passes - 1) / l.passes;
-  // one chunk of up to 4,096 tokens, or up to 256 of at least 2,048
-  l.chunk = (int)((std::max<int64_t>(N <= 4096 ? std::max<int64_t>(N, 1) : 2048, (N + 255) / 256) +
-                   kSortThreads - 1) / kSortThreads * kSortThreads);
+  l.chunk = (int)sort_chunk(N);
   l.chunks = (int)((N + l.chunk - 1) / l.chunk);
   l.sums = (int)((N + kSumChunk - 1) / kSumChunk);
   size_t o = 0;

@@ -1,0 +1,37 @@
+// grpo_index.cuh -- index arithmetic of the head and the embedding that has to
+// hold up to their largest sizes, where sums of 31-bit numbers pass 2^31.  Plain
+// functions of whole numbers, for the kernels and the host alike.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define GRPO_HD __host__ __device__ __forceinline__
+#else
+#define GRPO_HD inline
+#endif
+
+namespace grpo {
+
+// ---------------------------------------------------------------- sort
+static constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+
+// Tokens a CTA of the sort takes: one chunk of up to 4,096, or up to 256 chunks
+// of at least 2,048, each of whole groups of threads.
+GRPO_HD int64_t sort_chunk(int64_t N) {
+  const int64_t least = N > 4096 ? 2048 : N > 0 ? N : 1, even = (N + 255) / 256;
+  return ((even > least ? even : least) + kSortThreads - 1) / kSortThreads * kSortThreads;
+}
+
+// The tokens [from, end) of N that a warp has of its CTA's chunk; a part that
+// lies behind the last token ends before it begins.  (from + part is formed
+// where it is at most N only: the last chunk may end at 2^31.)
+struct SortPart {
+  int from, end;
+};
+GRPO_HD SortPart sort_part(int chunk, int cta, int warp, int N) {
+  const int part = chunk / kSortWarps, from = cta * chunk + warp * part;
+  return SortPart{from, N - from < part ? N : from + part};
+}
+
+}  // namespace grpo
