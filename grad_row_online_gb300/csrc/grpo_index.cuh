@@ -34,4 +34,23 @@ GRPO_HD SortPart sort_part(int chunk, int cta, int warp, int N) {
   return SortPart{from, N - from < part ? N : from + part};
 }
 
+// ---------------------------------------------------------------- tiles
+// Rows of tiles that are taken together, `row` bytes of operands each: 32 MB of
+// them, so that they stay in L2 while the columns pass, and no more than the mt
+// there are (their product with the columns' tiles is formed in 31 bits).
+GRPO_HD int rows_together(int64_t row, int64_t mt) {
+  const int64_t fit = (32ll << 20) / row, most = mt > 1 ? mt : 1;
+  return (int)(fit < 1 ? 1 : fit < most ? fit : most);
+}
+
+// Tile u of mt x nt: blocks of mb rows of tiles, in which the rows come first.
+struct TilePlace {
+  int row, col;
+};
+GRPO_HD TilePlace tile_place(int u, int mt, int mb, int nt) {
+  const int blk = u / (mb * nt), left = u - blk * mb * nt;
+  const int across = mt - blk * mb < mb ? mt - blk * mb : mb;
+  return TilePlace{blk * mb + left % across, left / across};
+}
+
 }  // namespace grpo

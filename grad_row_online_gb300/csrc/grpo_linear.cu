@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "grpo_index.cuh"
 #include "grpo_linear.cuh"
 #include "grpo_tensor.cuh"
 
@@ -610,10 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tiles: (kBack) parts of the reduction, then blocks of mb rows of tiles, in
   // which the rows' tiles come first
   auto place = [&](Tile& x, int u, int mt, int mb, int nt, int bn) {
-    const int blk = u / (mb * nt), left = u - blk * mb * nt;
-    const int across = min(mb, mt - blk * mb);
-    x.m0 = (blk * mb + left % across) * kTile;
-    x.n0 = left / across * bn;
+    const TilePlace at = tile_place(u, mt, mb, nt);
+    x.m0 = at.row * kTile;
+    x.n0 = at.col * bn;
   };
   // the j-th tile of this cluster: whether there is one, and which
   auto tile = [&](int j, Tile& x) {
@@ -1033,7 +1033,7 @@ __device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step
   const int count = a.count ? *a.count : a.rows;
   const int end = (count + kPad - 1) / kPad * kPad;
   const int lane = threadIdx.x & 31;
-  for (int r = first; r < end; r += step) {
+  for (int64_t r = first; r < end; r += step) {  // (the step behind the last row may pass 2^31)
     const bool live = r < count;
     const int64_t from = live ? (a.idx ? a.idx[r] : r) : 0;
     const T* src = (const T*)a.src + from / a.T * a.sb + from % a.T * a.st;
@@ -1096,7 +1096,7 @@ __device__ __forceinline__ void pack_rows(const PackRows& a, int first, int step
           for (int i = 0; i < 8; ++i) h[i] = k + i < a.K ? __ldg(q + i) : 0u;
           v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
         }
-        *reinterpret_cast<uint4*>((T*)a.dst + (int64_t)r * a.Kp + k) = v;
+        *reinterpret_cast<uint4*>((T*)a.dst + r * a.Kp + k) = v;
       }
     }
   }
@@ -1462,6 +1462,9 @@ FewArgs few(const LinearArgs& a, const Layout& l) {
   return f;
 }
 
+// of a row of tiles, as its operands lie packed
+int64_t row_bytes(const Layout& l) { return 2 * l.planes * kRows * l.cg * l.Kp; }
+
 Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   Product g{};
   g.rows = (int)(a.B * a.T);
@@ -1480,8 +1483,7 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   g.rpad = (int)l.rpad;
   g.T = std::max<int64_t>(a.T, 1);
   g.status = a.hdr ? &a.hdr->status : nullptr;
-  // 32 MB of the rows at a time, so that they stay in L2 while the vocabulary passes
-  g.mb = (int)std::max<int64_t>(1, (32ll << 20) / (2 * l.planes * kRows * l.cg * l.Kp));
+  g.mb = rows_together(row_bytes(l), div_up(a.B * a.T, kRows * l.cg));
   return g;
 }
 
@@ -1673,6 +1675,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     h.bn = w.bn = l.kbn;
     h.nt = w.nt = (int)div_up(a.K, l.kbn);
     h.a_rows = w.a_rows = kRows;
+    w.mb = rows_together(row_bytes(l), div_up(vp, rows));
     if (!encode(&h.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, kRows) ||
         !encode_weight(&h.b, a, dt, l, 64) ||
         !encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
