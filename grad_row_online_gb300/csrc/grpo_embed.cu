@@ -585,7 +585,9 @@ cudaError_t sorted_sums(SortArgs p, SumArgs a, const Layout& l, char* ws, cudaSt
   if (l.chunks == 1) {
     p.out = (int2*)(ws + l.keys[0]);
     const int smem = (int)sizeof(int2) * l.chunk * std::min(l.passes - 1, 2);
-    if ((e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+    // (the limit is the function's, in all threads: never less than any call needs)
+    constexpr int kMost = (int)sizeof(int2) * kSortOne * 2;
+    if ((e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)) != cudaSuccess ||
         (e = launch(sort_kernel, 1, kSortThreads, smem, s, p, l.passes)) != cudaSuccess)
       return e;
     p.in = p.out;

@@ -15,11 +15,12 @@ namespace grpo {
 
 // ---------------------------------------------------------------- sort
 static constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+static constexpr int kSortOne = 4096;  // tokens that one CTA sorts
 
-// Tokens a CTA of the sort takes: one chunk of up to 4,096, or up to 256 chunks
-// of at least 2,048, each of whole groups of threads.
+// Tokens a CTA of the sort takes: one chunk of up to kSortOne, or up to 256
+// chunks of at least 2,048, each of whole groups of threads.
 GRPO_HD int64_t sort_chunk(int64_t N) {
-  const int64_t least = N > 4096 ? 2048 : N > 0 ? N : 1, even = (N + 255) / 256;
+  const int64_t least = N > kSortOne ? 2048 : N > 0 ? N : 1, even = (N + 255) / 256;
   return ((even > least ? even : least) + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 

@@ -1306,10 +1306,12 @@ cudaError_t launch_product(Product& g, const Product* w, int sms, int tiles, cud
   const int more = (kRows - g.a_rows) * 128 + 1024;
   const int fixed = kEpi == kStats ? (int)(kRows * sizeof(Stats))
                     : kEpi == kBack ? (int)(8 * sizeof(Turn)) : 0;
-  g.stages = std::min(kMaxStages, (kSmem - fixed - more) / stage);
+  const int most = kSmem - fixed;
+  g.stages = std::min(kMaxStages, (most - more) / stage);
   const int smem = g.stages * stage + more;
   auto* k = product_kernel<kCg, kEpi, kParts>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the function's, in all threads: never less than any call needs)
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   const int grid = std::max(1, std::min(sms / kCg, tiles)) * kCg;
   if constexpr (kEpi == kBack) return launch(k, grid, kThreads, kCg, smem, s, g, *w);

@@ -241,7 +241,8 @@ template <int kRows, bool kGrad>
 cudaError_t logits(const FewArgs& a, int ctas, cudaStream_t s) {
   auto* k = few_logits_kernel<kRows, kGrad>;
   const int smem = (int)hidden_bytes(a.K, kRows);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the function's, in all threads: never less than any call needs)
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kHiddenBytes);
   return e != cudaSuccess ? e : launch(k, dim3((unsigned)ctas), kThreads, smem, s, a);
 }
 
