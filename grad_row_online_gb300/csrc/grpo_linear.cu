@@ -54,7 +54,7 @@ struct Product {
   int pairs;      // products of planes: 1, or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
   int sums;       // kParts: blocks that one accumulator sums up
-  int kc;         // kStats, kCg 1: sets of accumulators that the reduction is cut into, in order
+  int kc;         // logits, kCg 1: sets of accumulators that the reduction is cut into, in order
   int slot, bufs; // columns of a set; tiles that are in flight, 1 or 2
   int want_entropy; // kStats: D is wanted; kGrad: c1 is not 0
   int run;        // kStats: one record of a CTA's tiles, which are of the same rows
@@ -370,7 +370,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
         if (have) {
           tmem_ld32(tm + c, v);
           tmem_wait(v);
-          if constexpr (kCg == 1 && kEpi == kStats) {
+          if constexpr (kCg == 1 && kEpi != kBack) {
             for (int j = 1; j < g.kc; ++j) {
               float w[32];
               tmem_ld32(tm + j * g.slot + c, w);
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Turn s_turn[kEpi == kBack ? 8 : 1];
   __shared__ Stats s_pair[kEpi == kStats ? kRows : 1];
   constexpr bool kBmn = kEpi == kBack;
-  constexpr bool kSets = kCg == 1 && kEpi == kStats && !kParts;
+  constexpr bool kSets = kCg == 1 && kEpi != kBack && !kParts;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kCg == 2 ? cluster_rank() : 0u;
@@ -1342,7 +1342,7 @@ struct Layout {
   int few;      // rows of the form for a handful of tokens; 0: another
   int cg, bn;   // CTAs of a tile, its columns (of the vocabulary)
   int kbn;      // columns of a tile of the width
-  int sets;     // direct: of accumulators that a reduction is cut into
+  int sets;     // logits of one CTA: of accumulators that a reduction is cut into
   int64_t rpad, Kp, planes, nt, vc, splits, ldd, ldacc;
   size_t idx, coef, target, xa, part, hidden, weight, d, acc, total;
 };
@@ -1390,6 +1390,13 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     l.total = o;
     return l;
   }
+  // One CTA: a logit's sum in parts, each with its own accumulators, for which
+  // tensor memory has room here.  Two of them, and four of 128 columns where a
+  // 16-bit width passes 2,048: 64 x 4,096 x 151,936 takes 190 us where two sets
+  // of 256 columns take 186, and its entropies are off by 1.4e-6 where 3.1e-6;
+  // 1 x 2,048 x 32,768 33 where 31.  The gradient of fp32 operands forms its
+  // logits in the same order, so that its p are those of the statistics.
+  l.sets = l.cg == 2 || (backward && dt != GRPO_F32) ? 1 : dt != GRPO_F32 && l.Kp > 64 * kSumsWide ? 4 : 2;
   l.hidden = take((size_t)(2 * l.planes * l.rpad * l.Kp));
   l.weight = take(pack_weight(weight, dt, V, sv) ? (size_t)(2 * l.planes * ceil_to(V, kPad) * l.Kp) : 0);
   if (backward) {
@@ -1418,12 +1425,6 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     if (l.splits > 1 || pieces > 1) l.acc = take((size_t)(4 * l.splits * l.rpad * l.ldacc));
   } else {
     l.direct = N <= kRows;
-    // one CTA: a sum of all products in parts, each with its own
-    // accumulators, for which tensor memory has room here.  Two of them, and
-    // four of 128 columns where a 16-bit width passes 2,048: 64 x 4,096 x 151,936
-    // takes 190 us where two sets of 256 columns take 186, and its entropies are
-    // off by 1.4e-6 where 3.1e-6; 1 x 2,048 x 32,768 33 where 31.
-    l.sets = !l.direct ? 1 : dt != GRPO_F32 && l.Kp > 64 * kSumsWide ? 4 : 2;
     // one CTA: columns so that the SMs' shares of the vocabulary are even
     const int64_t wide = l.sets == 4 ? 128 : 256, waves = div_up(V, (int64_t)sms * wide);
     l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(wide, ceil_to(div_up(V, sms * waves), 16));
@@ -1487,6 +1488,15 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   g.status = a.hdr ? &a.hdr->status : nullptr;
   g.mb = rows_together(row_bytes(l), div_up(a.B * a.T, kRows * l.cg));
   return g;
+}
+
+// The order of a logit's sum: forward pass, and the gradient of fp32 operands.
+void order(Product& g, grpo_dtype_t dt, const Layout& l) {
+  if (dt != GRPO_F32 && g.kb > l.sets * kSumsWide) g.sums = kSumsWide;
+  if (l.cg == 2) return;
+  if (!g.sums) g.kc = std::min(l.sets, g.kb * g.pairs);
+  if (l.sets == 4) g.slot = 128;
+  g.bufs = g.kc == 1 ? 2 : 1;
 }
 
 bool encode_weight(CUtensorMap* m, const LinearArgs& a, grpo_dtype_t dt, const Layout& l, int box) {
@@ -1553,13 +1563,10 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
   g.want_entropy = a.entropy != nullptr;
   g.bn = l.bn;
   g.nt = (int)l.nt;
-  if (dt != GRPO_F32 && g.kb > l.sets * kSumsWide) g.sums = kSumsWide;
+  order(g, dt, l);
   if (l.direct) {
     g.run = 1;
     g.a_rows = (int)ceil_to(N, 8);
-    if (!g.sums) g.kc = std::min(l.sets, g.kb * g.pairs);
-    if (l.sets == 4) g.slot = 128;
-    g.bufs = g.kc == 1 ? 2 : 1;
   }
   const bool mapped =
       in_place ? encode(&g.a, a.hidden, dt != GRPO_F16, a.K, N, 1, N == 1 ? ceil_to(a.K, 8) : apart,
@@ -1652,7 +1659,9 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     if (!encode(&g.a, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, a_rows) ||
         !encode_weight(&g.b, a, dt, l, g.bn / cg))
       return cudaErrorUnknown;
-    if ((e = launch_product<kGrad>(g, cg, sms, mt * g.nt, s)) != cudaSuccess) return e;
+    Product x = g;
+    if (dt == GRPO_F32) order(x, dt, l);
+    if ((e = launch_product<kGrad>(x, cg, sms, mt * g.nt, s)) != cudaSuccess) return e;
     Product h = g, w = g;
     h.on = a.dhidden && N > 0;
     h.out = a.dhidden;
