@@ -758,7 +758,8 @@ def grpo_linear_logps_grad(hidden: torch.Tensor, weight: torch.Tensor,
 
     ``grad_hidden`` / ``grad_weight``: True (a new tensor), a tensor to write
     into, or None / False (not wanted).  grad_weight has weight's dtype or is
-    f32; ``add_weight`` (of grad_weight's dtype; may be grad_weight itself) is
+    f32 (of 16-bit tensors: more exact than a rounding of the logits' gradient
+    to their dtype allows, for a product more); ``add_weight`` (of grad_weight's dtype; may be grad_weight itself) is
     added to it: a gradient accumulated over batches, or the embedding's part
     of a tied weight.  Returns a dict of ``grad_hidden`` and ``grad_weight``.
     A tensor written into counts as modified in place."""

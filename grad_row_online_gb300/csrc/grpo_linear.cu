@@ -51,7 +51,7 @@ struct Product {
   int on;         // kBack: this product is wanted
   int least;      // kBack, dW: what the results of a tile take, in blocks
   int splits;     // kBack, dh: parts of the reduction
-  int pairs;      // products of planes: 1, or 6 of three planes each
+  int pairs;      // products of planes: 1, 2 (of A's two), or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
   int sums;       // kParts: blocks that one accumulator sums up
   int kc;         // logits, kCg 1: sets of accumulators that the reduction is cut into, in order
@@ -72,6 +72,7 @@ struct Product {
   const float4* coef;    // [rpad] of (m, c0, c1, s dlogp)
   const int* target;     // [rpad]
   __nv_bfloat16* d;      // [planes][rpad][ldd]
+  int planes;
   int64_t ldd;
   const unsigned* bound; // f16: largest |d|, as bits; nullptr: no scaling
   // kBack.  dh: fp32 sums, or results
@@ -98,6 +99,11 @@ struct Stats {
 // Products of planes, the small ones first: x = x0 + x1 + x2 in bf16, and what
 // is left out is below 2^-26 of |x| |w|.
 __device__ __constant__ signed char kPairs[6][2] = {{0, 2}, {2, 0}, {1, 1}, {0, 1}, {1, 0}, {0, 0}};
+
+// the planes of product p of a block
+__device__ __forceinline__ int2 planes_of(int pairs, int p) {
+  return pairs == 6 ? make_int2(kPairs[p][0], kPairs[p][1]) : make_int2(pairs - 1 - p, 0);
+}
 
 // 2^e with the largest |d| times it in [2^14, 2^15): fp16 has no range of its
 // own to spare, and 2^-28 of the largest value is still a normal number.
@@ -453,7 +459,6 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
     const float c0 = -q.y * scale, c1 = -q.z * scale;
     const float2 s2 = make_float2(g.s2, g.s2), r2 = make_float2(-q.x, -q.x);
     const float2 c02 = make_float2(c0, c0), c12 = make_float2(c1, c1);
-    const int planes = g.pairs == 1 ? 1 : 3;
     __nv_bfloat16* dst = g.d + (int64_t)r * g.ldd + t.n0;
     blocks(g.bn, [&](int c, float(&v)[32]) {
       // (far below the others, -inf among them: 0, not 0 x inf)
@@ -479,20 +484,21 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = live && c + i < n ? (failed ? bad : v[i]) : 0.f;
       }
-      if (g.fmt == 0) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 16)
-          store32(dst + c + i, Storage<__half>::pack(v + i), Storage<__half>::pack(v + i + 8));
-      } else {
-        for (int p = 0; p < planes; ++p) {
+      for (int p = 0; p < g.planes; ++p) {
+        __nv_bfloat16* to = dst + (int64_t)p * g.rpad * g.ldd + c;
+        if (g.fmt == 0) {
 #pragma unroll
           for (int i = 0; i < 32; i += 16)
-            store32(dst + (int64_t)p * g.rpad * g.ldd + c + i, Storage<__nv_bfloat16>::pack(v + i),
-                    Storage<__nv_bfloat16>::pack(v + i + 8));
-          if (planes > 1) {
+            store32(to + i, Storage<__half>::pack(v + i), Storage<__half>::pack(v + i + 8));
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
-          }
+          for (int i = 0; i < 32; i += 16)
+            store32(to + i, Storage<__nv_bfloat16>::pack(v + i), Storage<__nv_bfloat16>::pack(v + i + 8));
+        }
+        if (p + 1 < g.planes) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] -= g.fmt == 0 ? __half2float(__float2half_rn(v[i])) : __bfloat162float(__float2bfloat16_rn(v[i]));
         }
       }
     });
@@ -561,6 +567,9 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // the tensor cores take 16-bit operands, and two planes of d would double the
 // work of two of three products.  It adds half a step of the type to each
 // term, 1.7e-3 to 2.4e-3 in norm for bf16 (1.7e-3 is the results' own rounding).
+// Where dW leaves in fp32, that rounding would be all of its error, and dW takes
+// a second plane of d with what the first one lacks: 1.6e-3 becomes 1e-6 to
+// 5e-6, and 4,608 x 2,048 x 151,936 bf16 takes 7.40 ms where it took 5.16.
 template <int kCg, int kEpi, bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product g,
@@ -772,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k0 = t.k0; k0 < t.k1 && ok; k0 += part) {
           const int k1 = min(t.k1, k0 + part);
           for (int p = 0; p < q.pairs && ok; ++p) {
-            const int za = q.pairs == 1 ? 0 : kPairs[p][0], zb = q.pairs == 1 ? 0 : kPairs[p][1];
+            const int2 z = planes_of(q.pairs, p);
             for (int k = k0; k < k1; ++k) {
               if (!(ok = mbar_wait_all(smem_u32(&s_empty[st]), ph ^ 1u))) break;
               uint32_t bar = smem_u32(&s_full[st]);
@@ -782,16 +791,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kCg == 2) bar = map_to(bar, 0);
                 if (kAmn) {
                   for (int j = 0; j < kRows; j += 64)
-                    tma_load<kCg>(sa + j * 128u, &q.a, m + j, k * kBlk, za, bar);
+                    tma_load<kCg>(sa + j * 128u, &q.a, m + j, k * kBlk, z.x, bar);
                 } else {
-                  tma_load<kCg>(sa, &q.a, k * kBlk, m, za, bar);
+                  tma_load<kCg>(sa, &q.a, k * kBlk, m, z.x, bar);
                 }
                 if (kBmn) {
                   const int y = (kAmn ? 0 : g.v0) + k * kBlk;
                   for (int j = 0; j < half; j += 64)
-                    tma_load<kCg>(sb + j * 128u, &q.b, n + j, y, zb, bar);
+                    tma_load<kCg>(sb + j * 128u, &q.b, n + j, y, z.y, bar);
                 } else {
-                  tma_load<kCg>(sb, &q.b, k * kBlk, g.v0 + n, zb, bar);
+                  tma_load<kCg>(sb, &q.b, k * kBlk, g.v0 + n, z.y, bar);
                 }
               }
               __syncwarp();
@@ -1343,7 +1352,7 @@ struct Layout {
   int cg, bn;   // CTAs of a tile, its columns (of the vocabulary)
   int kbn;      // columns of a tile of the width
   int sets;     // logits of one CTA: of accumulators that a reduction is cut into
-  int64_t rpad, Kp, planes, nt, vc, splits, ldd, ldacc;
+  int64_t rpad, Kp, planes, dplanes, nt, vc, splits, ldd, ldacc;
   size_t idx, coef, target, xa, part, hidden, weight, d, acc, total;
 };
 
@@ -1354,17 +1363,22 @@ struct Layout {
 // 8 % (4,096 x 4,096 x 128,256: 2,069 and 2,244 us).  Sums of fp32 operands are
 // as exact as chains of fp32 additions with 8 (and 5e-5 off in the gradients of
 // sharp log-probs without parts).  The gradient of 16-bit operands is rounded
-// to 16 bits, 2e-3 of it, and takes one sum.
-static constexpr int kSumsF32 = 8, kSumsWide = 32;
+// to 16 bits, 2e-3 of it, and takes one sum; dW in fp32 sums up to 4,096 tokens:
+// 8,192 tokens and more are off by 5.5e-6 at most (9.9e-6 and, 20,000, 2.3e-5 in
+// one sum; 3.4e-6 in sums of 2,048), and 4,608 x 2,048 x 151,936 takes 7.40 ms
+// (7.17 in one sum, 7.56 in sums of 2,048).
+static constexpr int kSumsF32 = 8, kSumsWide = 32, kSumsTokens = 64;
 static constexpr int64_t kPieceBytes = 512ll << 20;  // of the logits' gradient
 
+// `exact`: dW in fp32 of 16-bit operands.
 Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t V, int64_t sv,
-              bool backward) {
+              bool backward, bool exact) {
   Layout l{};
   const int sms = sm_count();
   l.rpad = ceil_to(std::max<int64_t>(N, 1), kPad);
   l.Kp = ceil_to(K, 64);
   l.planes = dt == GRPO_F32 ? 3 : 1;
+  l.dplanes = exact ? 2 : l.planes;
   l.cg = N > kRows ? 2 : 1;
   size_t o = 256;
   auto take = [&](size_t bytes) {
@@ -1394,9 +1408,10 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
   // tensor memory has room here.  Two of them, and four of 128 columns where a
   // 16-bit width passes 2,048: 64 x 4,096 x 151,936 takes 190 us where two sets
   // of 256 columns take 186, and its entropies are off by 1.4e-6 where 3.1e-6;
-  // 1 x 2,048 x 32,768 33 where 31.  The gradient of fp32 operands forms its
-  // logits in the same order, so that its p are those of the statistics.
-  l.sets = l.cg == 2 || (backward && dt != GRPO_F32) ? 1 : dt != GRPO_F32 && l.Kp > 64 * kSumsWide ? 4 : 2;
+  // 1 x 2,048 x 32,768 33 where 31.  The gradient forms its logits in the same
+  // order where its results have more than 16 bits.
+  const bool wide_sums = l.cg == 1 && (!backward || exact || dt == GRPO_F32);
+  l.sets = !wide_sums ? 1 : dt != GRPO_F32 && l.Kp > 64 * kSumsWide ? 4 : 2;
   l.hidden = take((size_t)(2 * l.planes * l.rpad * l.Kp));
   l.weight = take(pack_weight(weight, dt, V, sv) ? (size_t)(2 * l.planes * ceil_to(V, kPad) * l.Kp) : 0);
   if (backward) {
@@ -1404,14 +1419,14 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     l.target = take(4 * l.rpad);
     l.kbn = l.cg == 2 || K > 128 ? 256 : K > 64 ? 128 : 64;
     const int64_t whole = ceil_to(V, 256);
-    const int64_t fit = std::max<int64_t>(kPieceBytes / (2 * l.planes * l.rpad) / 256 * 256, 2048);
+    const int64_t fit = std::max<int64_t>(kPieceBytes / (2 * l.dplanes * l.rpad) / 256 * 256, 2048);
     const int64_t pieces = div_up(whole, fit);
     l.vc = ceil_to(div_up(whole, pieces), 256);
     // one CTA: columns so that the SMs' shares of a piece are even
-    const int64_t waves = div_up(l.vc, (int64_t)sms * 256);
-    l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(256, ceil_to(div_up(l.vc, sms * waves), 32));
+    const int64_t most = l.sets == 4 ? 128 : 256, waves = div_up(l.vc, (int64_t)sms * most);
+    l.bn = l.cg == 2 ? 256 : (int)std::min<int64_t>(most, ceil_to(div_up(l.vc, sms * waves), 32));
     l.ldd = ceil_to(div_up(ceil_to(l.vc, 64), l.bn) * l.bn, 64);
-    l.d = take((size_t)(2 * l.planes * l.rpad * l.ldd));
+    l.d = take((size_t)(2 * l.dplanes * l.rpad * l.ldd));
     // Parts of dh's reduction, at least eight blocks each, so that its tiles last
     // no longer than a third of what a cluster has to do in all (where two of
     // three tokens take no part, half of it).
@@ -1419,8 +1434,8 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     const double blocks = (double)(div_up(N, tile) * wide) * (double)(l.vc / 64) +
                           (double)(div_up(l.vc, tile) * wide) * (double)div_up(N, 64);
     const double share = std::max(1.0, blocks * l.cg / sms);
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, l.vc / 64 * planes / 8));
-    l.splits = std::min<int64_t>(most, (int64_t)(3.0 * (double)(l.vc / 64) / share) + 1);
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(64, l.vc / 64 * planes / 8));
+    l.splits = std::min<int64_t>(parts, (int64_t)(3.0 * (double)(l.vc / 64) / share) + 1);
     l.ldacc = ceil_to(K, 256);
     if (l.splits > 1 || pieces > 1) l.acc = take((size_t)(4 * l.splits * l.rpad * l.ldacc));
   } else {
@@ -1452,6 +1467,8 @@ cudaError_t pack(const LinearArgs& a, grpo_dtype_t dt, const Layout& l, const in
 
 // Parts of a reduction of `kb` blocks: none where one accumulator holds it.
 int sums_of(grpo_dtype_t dt, int64_t kb) { return dt == GRPO_F32 && kb > kSumsF32 ? kSumsF32 : 0; }
+// of 16-bit operands, for fp32 results
+int sums_wide(int64_t kb) { return kb > kSumsWide ? kSumsWide : 0; }
 
 FewArgs few(const LinearArgs& a, const Layout& l) {
   FewArgs f{};
@@ -1490,9 +1507,9 @@ Product base(const LinearArgs& a, grpo_dtype_t dt, const Layout& l) {
   return g;
 }
 
-// The order of a logit's sum: forward pass, and the gradient of fp32 operands.
+// The order of a logit's sum: forward pass, and gradients of more than 16 bits.
 void order(Product& g, grpo_dtype_t dt, const Layout& l) {
-  if (dt != GRPO_F32 && g.kb > l.sets * kSumsWide) g.sums = kSumsWide;
+  if (dt != GRPO_F32) g.sums = sums_wide(div_up(g.kb, l.sets));
   if (l.cg == 2) return;
   if (!g.sums) g.kc = std::min(l.sets, g.kb * g.pairs);
   if (l.sets == 4) g.slot = 128;
@@ -1510,13 +1527,15 @@ bool encode_weight(CUtensorMap* m, const LinearArgs& a, grpo_dtype_t dt, const L
 
 size_t linear_ws(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t V, int64_t sv,
                  bool backward) {
-  return layout(weight, dt, N, K, V, sv, backward).total;
+  const size_t need = layout(weight, dt, N, K, V, sv, backward, false).total;
+  if (!backward || dt == GRPO_F32) return need;
+  return std::max(need, layout(weight, dt, N, K, V, sv, true, true).total);
 }
 
 cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream_t s) {
   const int64_t N = a.B * a.T;
   const int sms = sm_count();
-  const Layout l = layout(a.weight, dt, N, a.K, a.V, a.sv, false);
+  const Layout l = layout(a.weight, dt, N, a.K, a.V, a.sv, false, false);
   Header* h = (Header*)a.ws;
   int* idx = l.direct ? nullptr : (int*)(a.ws + l.idx);
   const int* count = l.direct ? nullptr : &h->count;
@@ -1582,7 +1601,8 @@ cudaError_t launch_linear_logps(const LinearArgs& a, grpo_dtype_t dt, cudaStream
 cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_t s) {
   const int64_t N = a.B * a.T;
   const int sms = sm_count();
-  const Layout l = layout(a.weight, dt, N, a.K, a.V, a.sv, true);
+  const bool exact = a.dweight && a.wdt == GRPO_F32 && dt != GRPO_F32;
+  const Layout l = layout(a.weight, dt, N, a.K, a.V, a.sv, true, exact);
   Header* h = (Header*)a.ws;
   int* idx = (int*)(a.ws + l.idx);
   PrepRows p{};
@@ -1651,6 +1671,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     g.target = p.target;
     g.want_entropy = a.dent != nullptr;
     g.d = (__nv_bfloat16*)(a.ws + l.d);
+    g.planes = (int)l.dplanes;
     g.ldd = l.ldd;
     g.bound = bound;
     g.bn = l.bn;
@@ -1660,7 +1681,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
         !encode_weight(&g.b, a, dt, l, g.bn / cg))
       return cudaErrorUnknown;
     Product x = g;
-    if (dt == GRPO_F32) order(x, dt, l);
+    if (exact || dt == GRPO_F32) order(x, dt, l);
     if ((e = launch_product<kGrad>(x, cg, sms, mt * g.nt, s)) != cudaSuccess) return e;
     Product h = g, w = g;
     h.on = a.dhidden && N > 0;
@@ -1681,15 +1702,16 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     w.odt = a.wdt;
     w.add = a.add;
     w.asv = a.asv;
-    w.sums = sums_of(dt, div_up(N, 64));
+    if (exact) w.pairs = 2;
+    w.sums = exact ? (div_up(N, 64) > kSumsTokens ? kSumsTokens : 0) : sums_of(dt, div_up(N, 64));
     w.least = a.gsv % 8 == 0 && ((uintptr_t)a.dweight & 15) == 0 ? 16 : 24;
     h.bn = w.bn = l.kbn;
     h.nt = w.nt = (int)div_up(a.K, l.kbn);
     h.a_rows = w.a_rows = kRows;
     w.mb = rows_together(row_bytes(l), div_up(vp, rows));
-    if (!encode(&h.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, kRows) ||
+    if (!encode(&h.a, g.d, bf16, l.ldd, l.rpad, l.dplanes, l.ldd, l.rpad * l.ldd, kRows) ||
         !encode_weight(&h.b, a, dt, l, 64) ||
-        !encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.planes, l.ldd, l.rpad * l.ldd, 64) ||
+        !encode(&w.a, g.d, bf16, l.ldd, l.rpad, l.dplanes, l.ldd, l.rpad * l.ldd, 64) ||
         !encode(&w.b, a.ws + l.hidden, bf16, l.Kp, l.rpad, l.planes, l.Kp, l.rpad * l.Kp, 64))
       return cudaErrorUnknown;
     const int64_t tiles = h.on * mt * h.nt * h.splits + w.on * div_up(vp, rows) * w.nt;

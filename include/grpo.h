@@ -517,7 +517,9 @@ grpo_status_t grpo_linear_logps(const void *hidden, grpo_dtype_t dt, int64_t B, 
  * The logits are formed again, and d exists for a piece of the vocabulary at a
  * time, rounded to the operands' dtype for its products (f32: three bf16
  * parts, or fp32 as above; f16: scaled by a power of two that keeps its values
- * in range).
+ * in range).  That rounding is as large as the one of 16-bit results; a
+ * grad_weight in f32 of 16-bit operands takes d in two parts, off by 2^-17 of
+ * it, which costs a fourth product beside the other three.
  *   stats, entropy, grad_logps, grad_entropy, status_ws: as for
  *                     grpo_token_logps_grad; stats and entropy of
  *                     grpo_linear_logps for the same tensors (statistics of

@@ -60,3 +60,15 @@ def logp_bound(x, blocks, s=1.0 / TEMPERATURE):
     of one sum, and by as much as ten blocks for the fp32 arithmetic behind them.
     That is a figure in norm; the largest of 500 normal deviates is 3.1 of them."""
     return 3.1 * 2 * s * (2e-8 * blocks + 2e-7) * x.abs().amax(-1)
+
+
+def rounded(dtype):
+    """Gradients in 16 bits: the rounding of d to that type for its products, and
+    the result's own, each eps / 2 times 0.43 in norm (uniform over a step, the
+    steps' sizes over a binade); together 0.61."""
+    return torch.finfo(dtype).eps / 2 * 0.77
+
+
+# - fp32 grad_weight of 16-bit operands: d in two parts, off by 2^-17 of it, beside
+#   the logits' error above.
+TWO_PARTS = 1e-5

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import grad_row_online_gb300 as g
-from accuracy_cases import F32, SHORT, TEMPERATURE, WIDE, exact, exact_d, logp_bound, make, off
+from accuracy_cases import F32, SHORT, TEMPERATURE, TWO_PARTS, WIDE, exact, exact_d, logp_bound, make, off, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -63,6 +63,27 @@ def test_scores_of_16_bits(dtype, N, K, V):
         far = (s[n].double() - want).abs() / logp_bound(x, blocks)
         print(n, float(far.max()))
         assert float(far.max()) <= 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("N,K,V", [(20, 512, 9000), (128, 2048, 5000), (700, 1024, 9000), (5000, 256, 3000)])
+def test_gradients_of_16_bits(dtype, N, K, V):
+    """grad_weight of the operands' type and, more exactly, in fp32; added to what is there."""
+    h, W, ids, w, b = make(N, K, V, DT[dtype], "cuda", N + K)
+    s = scores(h, W, ids)
+    d = exact_d(h.double() @ W.double().t(), ids, w, b)
+    gh, gw = d @ W.double(), d.t() @ h.double()
+    r = gradient(h, W, ids, s, w, b)
+    wide = gradient(h, W, ids, s, w, b, grad_weight=torch.empty(W.shape, device="cuda"))
+    found = {"grad_hidden": off(r["grad_hidden"], gh), "grad_weight": off(r["grad_weight"], gw),
+             "grad_hidden beside fp32": off(wide["grad_hidden"], gh)}
+    exactly = off(wide["grad_weight"], gw)
+    print(dtype, N, K, V, found, exactly)
+    assert max(found.values()) <= rounded(DT[dtype]), found
+    assert exactly <= TWO_PARTS
+    add = torch.randn(W.shape, device="cuda")
+    more = gradient(h, W, ids, s, w, b, add_weight=add, grad_hidden=None)
+    assert off(more["grad_weight"], gw + add.double()) <= TWO_PARTS
 
 
 @pytest.mark.parametrize("N,K", [(17, 512), (64, 256), (128, 512), (128, 100), (128, 2048), (300, 512)])
