@@ -487,10 +487,12 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
  * 6,400); beyond, they are split into three bf16 parts, whose products are
  * formed but for those below 2^-26 of |h_k W_vk| (operands below 1e-33 keep
  * fewer bits).  A row with a NaN or +inf logit, or only -inf, has no
- * distribution: logp, entropy and Z are NaN; logits of -inf have p = 0.  (An
- * infinite f32 operand makes its logits infinite or NaN.)  Results are bitwise
- * reproducible; those of a token may differ in their last bits between calls
- * with other numbers of tokens.
+ * distribution: logp, entropy and Z are NaN; logits of -inf have p = 0.  (Beyond
+ * 16 tokens an infinite f32 operand, and finite ones whose product passes fp32's
+ * largest value, make a logit infinite or NaN: the products of their parts
+ * overflow with signs of their own.)  Results are bitwise reproducible; those of
+ * a token may differ in their last bits between calls with other numbers of
+ * tokens.
  * Sizes: B T and V at most 2^31 - 1025, K at most 2^20, and
  * ceil(B T / 128) ceil(V / 64) < 2^31.
  * ws: grpo_linear_workspace_size(..., 0) bytes, 256-byte aligned, needs no
