@@ -1368,7 +1368,9 @@ struct Layout {
 // one sum; 3.4e-6 in sums of 2,048), and 4,608 x 2,048 x 151,936 takes 7.40 ms
 // (7.17 in one sum, 7.56 in sums of 2,048).
 static constexpr int kSumsF32 = 8, kSumsWide = 32, kSumsTokens = 64;
-static constexpr int64_t kPieceBytes = 512ll << 20;  // of the logits' gradient
+// Of the logits' gradient: pieces of 512 MB, but of 2,048 words at least, since
+// each piece reads and writes the sums of dh.
+static constexpr int64_t kPieceBytes = 512ll << 20, kPieceWords = 2048;
 
 // `exact`: dW in fp32 of 16-bit operands.
 Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t V, int64_t sv,
@@ -1419,7 +1421,7 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
     l.target = take(4 * l.rpad);
     l.kbn = l.cg == 2 || K > 128 ? 256 : K > 64 ? 128 : 64;
     const int64_t whole = ceil_to(V, 256);
-    const int64_t fit = std::max<int64_t>(kPieceBytes / (2 * l.dplanes * l.rpad) / 256 * 256, 2048);
+    const int64_t fit = std::max<int64_t>(kPieceBytes / (2 * l.dplanes * l.rpad) / 256 * 256, kPieceWords);
     const int64_t pieces = div_up(whole, fit);
     l.vc = ceil_to(div_up(whole, pieces), 256);
     // one CTA: columns so that the SMs' shares of a piece are even

@@ -500,8 +500,10 @@ grpo_status_t grpo_token_logps_grad(const void *logits, grpo_dtype_t dt, int64_t
  * token for each 256 words of the vocabulary (up to 128 tokens, for each SM at
  * most), and a copy of the weight where its rows are not 16-byte aligned, or
  * its three parts where it is f32 (neither with f32 and up to 16 tokens).  For
- * the gradient also the logits' gradient of a piece of the vocabulary, up to
- * 512 MB of it, and fp32 sums of grad_hidden. */
+ * the gradient also the logits' gradient of a piece of the vocabulary, of 512 MB
+ * or of 2,048 words, whichever is more (a word and token take 6 bytes with f32
+ * operands and up to 4 with others; tokens count in multiples of 256), and fp32
+ * sums of grad_hidden. */
 size_t grpo_linear_workspace_size(const void *weight, grpo_dtype_t dt, int64_t B, int64_t T,
                                   int64_t K, int64_t V, int64_t stride_v, int32_t backward);
 
