@@ -51,7 +51,7 @@ F32 = 3e-6
 #   Sums of up to 32 blocks: 4e-6 (twice that at a width of 4,096 in one sum).
 WIDE = 6e-6
 # - up to 128 tokens: sums of half that length.
-SHORT = 4e-6
+SHORT = WIDE / 2
 
 
 def logp_bound(x, blocks, s=1.0 / TEMPERATURE):
