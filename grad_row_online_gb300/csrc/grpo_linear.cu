@@ -54,7 +54,7 @@ struct Product {
   int pairs;      // products of planes: 1, 2 (of A's two), or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
   int sums;       // kParts: blocks that one accumulator sums up
-  int kc;         // logits, kCg 1: sets of accumulators that the reduction is cut into, in order
+  int kc;         // kSets: of accumulators that a logit's reduction is cut into, in order
   int slot, bufs; // columns of a set; tiles that are in flight, 1 or 2
   int want_entropy; // kStats: D is wanted; kGrad: c1 is not 0
   int run;        // kStats: one record of a CTA's tiles, which are of the same rows
@@ -354,7 +354,7 @@ __device__ __forceinline__ RowData row_data(const Product& g, const Tile& t, int
 // ---- results of a tile: a thread has one row; two warps share 32 rows and take
 // blocks of 32 columns in turn, from tensor memory at `tm` or (kParts) added
 // up in `acc`
-template <int kCg, int kEpi, bool kParts>
+template <int kCg, int kEpi, bool kParts, bool kSets>
 __device__ __forceinline__ void results(const Product& g, const Tile& t, int rank, int count,
                                         uint32_t tm, bool have, bool failed,
                                         float (&acc)[kParts ? 4 : 1][32], Stats& st, Turn& turn,
@@ -376,7 +376,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
         if (have) {
           tmem_ld32(tm + c, v);
           tmem_wait(v);
-          if constexpr (kCg == 1 && kEpi != kBack) {
+          if constexpr (kSets) {
             for (int j = 1; j < g.kc; ++j) {
               float w[32];
               tmem_ld32(tm + j * g.slot + c, w);
@@ -548,7 +548,8 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // An accumulator is rounded towards zero at every step, 16 products long, so
 // a sum's error grows with its length and has its sign.  kParts: sums of `sums`
 // blocks each are added up in registers, rounded to nearest (fp32 operands,
-// and widths whose logits would be off by more than fp32 log-probs are).
+// and widths whose logits would be off by more than fp32 log-probs are).  kSets:
+// a logit's parts have accumulators of their own instead, one tile at a time.
 //
 // Bound by the tensor cores where tokens are many: a tile is 256 x 256, the most
 // that two sets of accumulators leave room for, so that an operand's element
@@ -570,7 +571,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // Where dW leaves in fp32, that rounding would be all of its error, and dW takes
 // a second plane of d with what the first one lacks: 1.6e-3 becomes 1e-6 to
 // 5e-6, and 4,608 x 2,048 x 151,936 bf16 takes 7.40 ms where it took 5.16.
-template <int kCg, int kEpi, bool kParts>
+template <int kCg, int kEpi, bool kParts, bool kSets>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Product g,
                    const __grid_constant__ std::conditional_t<kEpi == kBack, Product, int> w) {
@@ -580,7 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Turn s_turn[kEpi == kBack ? 8 : 1];
   __shared__ Stats s_pair[kEpi == kStats ? kRows : 1];
   constexpr bool kBmn = kEpi == kBack;
-  constexpr bool kSets = kCg == 1 && kEpi != kBack && !kParts;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kCg == 2 ? cluster_rank() : 0u;
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto part_end = [&](const Product& p, int k, int n) {
     return p.sums ? min(n, k + p.sums * p.pairs) : n;
   };
-  const bool two = !kSets || g.bufs == 2;  // tiles in flight
+  constexpr bool two = !kSets;  // tiles in flight
   bool ok = true;
 
   if (warp >= 4) {
@@ -736,12 +736,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(buf);
           ++it;
         }
-        results<kCg, kEpi, true>(p, t, (int)rank, count, 0u, true, !ok, acc, st, turn, s_pair, row);
+        results<kCg, kEpi, true, false>(p, t, (int)rank, count, 0u, true, !ok, acc, st, turn, s_pair, row);
       } else {
         const int buf = two ? it & 1 : 0;
         if (n > 0) ok = ok && done(buf, two ? it >> 1 : it);
         fence_after();
-        results<kCg, kEpi, false>(p, t, (int)rank, count, lanes + (uint32_t)buf * 256u, n > 0 && ok, !ok,
+        results<kCg, kEpi, false, kSets>(p, t, (int)rank, count, lanes + (uint32_t)buf * 256u, n > 0 && ok, !ok,
                                   acc, st, turn, s_pair, row);
         if (n > 0 && ok) release(buf);
         it += n > 0;
@@ -1304,7 +1304,7 @@ int sm_count() {
   return n > 0 ? n : 152;
 }
 
-template <int kCg, int kEpi, bool kParts>
+template <int kCg, int kEpi, bool kParts, bool kSets>
 cudaError_t launch_product(Product& g, const Product* w, int sms, int tiles, cudaStream_t s) {
   const int half = g.bn / kCg;
   const int stage = g.a_rows * 128 + ((half * 128 + 1023) & ~1023);
@@ -1318,7 +1318,7 @@ cudaError_t launch_product(Product& g, const Product* w, int sms, int tiles, cud
   const int most = kSmem - fixed;
   g.stages = std::min(kMaxStages, (most - more) / stage);
   const int smem = g.stages * stage + more;
-  auto* k = product_kernel<kCg, kEpi, kParts>;
+  auto* k = product_kernel<kCg, kEpi, kParts, kSets>;
   // (the limit is the function's, in all threads: never less than any call needs)
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
@@ -1332,10 +1332,13 @@ cudaError_t launch_product(Product& g, int cg, int sms, int64_t tiles, cudaStrea
                            const Product* w = nullptr) {
   const int n = (int)std::min<int64_t>(tiles, 1 << 20);
   if (g.sums > 0 || (w && w->sums > 0))
-    return cg == 2 ? launch_product<2, kEpi, true>(g, w, sms, n, s)
-                   : launch_product<1, kEpi, true>(g, w, sms, n, s);
-  return cg == 2 ? launch_product<2, kEpi, false>(g, w, sms, n, s)
-                 : launch_product<1, kEpi, false>(g, w, sms, n, s);
+    return cg == 2 ? launch_product<2, kEpi, true, false>(g, w, sms, n, s)
+                   : launch_product<1, kEpi, true, false>(g, w, sms, n, s);
+  if constexpr (kEpi != kBack) {
+    if (g.bufs == 1) return launch_product<1, kEpi, false, true>(g, w, sms, n, s);
+  }
+  return cg == 2 ? launch_product<2, kEpi, false, false>(g, w, sms, n, s)
+                 : launch_product<1, kEpi, false, false>(g, w, sms, n, s);
 }
 
 int64_t ceil_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
