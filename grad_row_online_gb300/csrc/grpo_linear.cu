@@ -662,9 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  auto of = [&](const Tile& x) -> const Product& {
-    if constexpr (kEpi == kBack) return x.weight ? w : g;
-    else return g;
+  auto of = [&](const Tile& x) -> const Product* {
+    if constexpr (kEpi == kBack) return x.weight ? &w : &g;
+    else return &g;
   };
   // (kParts) where the part of a tile's n blocks that starts at k ends
   auto part_end = [&](const Product& p, int k, int n) {
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Turn& turn = s_turn[kEpi == kBack ? warp - 4 : 0];
     Tile t;
     for (int j = 0; tile(j, t); ++j) {
-      const Product& p = of(t);
+      const Product& p = *of(t);
       const int n = (t.k1 - t.k0) * p.pairs;
       const RowData row = row_data<kEpi>(g, t, (int)rank, count);
       float acc[kParts ? 4 : 1][32];
