@@ -620,8 +620,12 @@ cudaError_t embed(EmbedArgs a, cudaStream_t s) {
   constexpr int kCols = 256 * Storage<T>::kVec;
   const int slices = (int)((a.K + kCols - 1) / kCols);
   if (a.sb == a.T * a.st) a.T = a.N;  // rows evenly apart
-  // rows together where there are enough of them for every SM
-  if (a.N * slices >= 152 * 16) return launch(embed_kernel<T, 4>, (a.N + 3) / 4 * slices, 256, 0, s, a, slices);
+  // Rows together where there are enough of them: 2,048 bf16 a row, one a thread
+  // and four take 3.8 and 4.4 us for 1,024 tokens, 5.4 and 5.3 for 2,048, 15.1 and
+  // 12.4 for 8,192, 104 and 78 for 65,536; 1,021 fp32, 5.5 and 7.6 for 2,048, 8.9
+  // and 9.1 for 4,096.
+  constexpr int64_t kMany = 2432;
+  if (a.N * slices >= kMany) return launch(embed_kernel<T, 4>, (a.N + 3) / 4 * slices, 256, 0, s, a, slices);
   return launch(embed_kernel<T, 1>, a.N * slices, 256, 0, s, a, slices);
 }
 

@@ -38,7 +38,10 @@ GRPO_HD SortPart sort_part(int chunk, int cta, int warp, int N) {
 // ---------------------------------------------------------------- tiles
 // Rows of tiles that are taken together, `row` bytes of operands each: 32 MB of
 // them, so that they stay in L2 while the columns pass, and no more than the mt
-// there are (their product with the columns' tiles is formed in 31 bits).
+// there are (their product with the columns' tiles is formed in 31 bits).  8,192 x
+// 4,096 x 65,536 bf16 takes 2.52 ms, with 16 MB 2.57, with 64 or all 2.68; 16,384 x
+// 2,048 x 65,536 2.36, 2.34 and 2.40; the gradient of 8,192 x 2,048 x 65,536 3.91,
+// 3.81 and 4.06.
 GRPO_HD int rows_together(int64_t row, int64_t mt) {
   const int64_t fit = (32ll << 20) / row, most = mt > 1 ? mt : 1;
   return (int)(fit < 1 ? 1 : fit < most ? fit : most);

@@ -49,7 +49,7 @@ struct Product {
   int bn, nt;     // columns of a tile, tiles of columns
   int kb;         // blocks of the reduction where it is not over the rows
   int on;         // kBack: this product is wanted
-  int least;      // kBack, dW: what the results of a tile take, in blocks
+  int least;      // kBack, dW: what a tile takes at least, for its results, in blocks
   int splits;     // kBack, dh: parts of the reduction
   int pairs;      // products of planes: 1, 2 (of A's two), or 6 of three planes each
   int a_rows;     // rows of A that are loaded (kCg 1; the others' results are not used)
@@ -875,8 +875,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   d_v = s dlogp 1[v = a] - 2^u (c0 + c1 u),   u = (x_v - m) s log2 e,
 //   c0 = s / Z (dlogp + dH (H - ln Z)),  c1 = s ln 2 / Z dH
 // A CTA takes 1,024 tokens and counts those before them itself, so no CTA waits
-// for another: latency, 5 us for 2,048 tokens and 9 for 16,384, where the
-// products that masked tokens would cost take milliseconds.
+// for another: latency, 3.5 us for 16,384 tokens (gradient: 5.2) and 9.4 (18) for
+// 131,072, where the products that masked tokens would cost take milliseconds.
+// The reads grow with the square of the tokens: 0.14 ms (0.28) for 2^20, 1.8
+// (3.6) for 2^22, a hundredth of such a batch's products.
 static constexpr int kPrepRows = 1024;
 
 struct Header {  // the first 256 bytes of the workspace
@@ -1188,7 +1190,9 @@ __global__ void __launch_bounds__(32 * kFoldWarps) fold_kernel(const FoldRows a)
 // The parts of the reduction of dh joined (in a fixed order), rows without a
 // gradient set to zero.  Where parts are many, rows are few, and
 // eight groups of threads take an eighth each: the gradient of 1 x 1,024 x
-// 32,768 in fp32, 304 parts, takes 95 us, 151 with one group.
+// 32,768 in fp32, 304 parts, takes 91 us, 139 with one group, 8 x 2,048 x 32,768
+// in bf16, 64 parts, 118 and 133.  With sixteen parts or fewer one group is
+// as fast or faster: 300 x 2,048 x 32,768 takes 162 us, 173 with eight.
 struct HiddenRows {
   const float* acc;  // nullptr: only the rows without a gradient
   int splits, rpad, N;
@@ -1348,6 +1352,10 @@ bool pack_weight(const void* w, grpo_dtype_t dt, int64_t V, int64_t sv) {
   return dt == GRPO_F32 || ((uintptr_t)w & 15) != 0 || (V > 1 && sv % 8 != 0);
 }
 
+// What a tile of dW takes at least, in blocks of its products: 8 to 32 give the
+// same times but for 2 %, with rows on 16 bytes and without (256 to 2,048 tokens).
+static constexpr int kLeast = 16;
+
 // What a call keeps in its workspace.
 struct Layout {
   bool direct;  // kStats: every row is taken, as it lies
@@ -1412,8 +1420,8 @@ Layout layout(const void* weight, grpo_dtype_t dt, int64_t N, int64_t K, int64_t
   // One CTA: a logit's sum in parts, each with its own accumulators, for which
   // tensor memory has room here.  Two of them, and four of 128 columns where a
   // 16-bit width passes 2,048: 64 x 4,096 x 151,936 takes 190 us where two sets
-  // of 256 columns take 186, and its entropies are off by 1.4e-6 where 3.1e-6;
-  // 1 x 2,048 x 32,768 33 where 31.  The gradient forms its logits in the same
+  // of 256 columns take 183, and its entropies are off by 1.4e-6 where 3.1e-6;
+  // 1 x 2,048 x 32,768 would take 32 where 30.  The gradient forms its logits in the same
   // order where its results have more than 16 bits.
   const bool wide_sums = l.cg == 1 && (!backward || exact || dt == GRPO_F32);
   l.sets = !wide_sums ? 1 : dt != GRPO_F32 && l.Kp > 64 * kSumsWide ? 4 : 2;
@@ -1709,7 +1717,7 @@ cudaError_t launch_linear_grad(const LinearArgs& a, grpo_dtype_t dt, cudaStream_
     w.asv = a.asv;
     if (exact) w.pairs = 2;
     w.sums = exact ? (div_up(N, 64) > kSumsTokens ? kSumsTokens : 0) : sums_of(dt, div_up(N, 64));
-    w.least = a.gsv % 8 == 0 && ((uintptr_t)a.dweight & 15) == 0 ? 16 : 24;
+    w.least = kLeast;
     h.bn = w.bn = l.kbn;
     h.nt = w.nt = (int)div_up(a.K, l.kbn);
     h.a_rows = w.a_rows = kRows;

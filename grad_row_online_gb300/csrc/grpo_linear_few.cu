@@ -12,7 +12,9 @@
 // 1 token 419 us, 4 447, 8 541, 16 1,076 : 1,710 at any; 128256 x 4096 and its
 // gradient (2.1 GB read twice, written once), 1 token 1,015 us, 8 1,526,
 // 16 2,304 : 3,300; 32768 x 1024 and its gradient, 1 token 95 us, 8 149,
-// 16 208 : 240.  Beyond sixteen the planes are the faster form.
+// 16 208 : 240.  Beyond sixteen the planes are the faster form of the two; from 17
+// to about 60 tokens of such wide weights neither is as fast as a product of the
+// library's (24 tokens of 151936 x 4096: planes 1,716, a form on it 1,412).
 #include <algorithm>
 
 #include "grpo_linear.cuh"
