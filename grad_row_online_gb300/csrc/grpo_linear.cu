@@ -1370,7 +1370,7 @@ struct Layout {
 // Blocks of a reduction, 64 elements each, that one accumulator sums up.  A
 // logit of 16-bit operands is off by about 2e-8 of its size for each block:
 // sharp log-probs (temperature 0.6, deviation 3) by 2.2e-6 at a width of 1,024,
-// 4e-6 at 2,048 and 8e-6 at 4,096, where parts of 2,048 make it 2e-6 and cost
+// 4e-6 at 2,048 and 8e-6 at 4,096, where parts of 2,048 make it 4e-6 and cost
 // 8 % (4,096 x 4,096 x 128,256: 2,069 and 2,244 us).  Sums of fp32 operands are
 // as exact as chains of fp32 additions with 8 (and 5e-5 off in the gradients of
 // sharp log-probs without parts).  The gradient of 16-bit operands is rounded

@@ -66,7 +66,8 @@ def test_scores_of_16_bits(dtype, N, K, V):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("N,K,V", [(20, 512, 9000), (128, 2048, 5000), (700, 1024, 9000), (5000, 256, 3000), (14000, 128, 2000)])
+@pytest.mark.parametrize("N,K,V", [(20, 512, 9000), (128, 2048, 5000), (700, 1024, 9000), (5000, 256, 3000), (14000, 128, 2000),
+                                   (1, 64, 700), (100, 4096, 3000), (60, 8320, 1500), (300, 4096, 3000)])
 def test_gradients_of_16_bits(dtype, N, K, V):
     """grad_weight of the operands' type and, more exactly, in fp32; added to what is there."""
     h, W, ids, w, b = make(N, K, V, DT[dtype], "cuda", N + K)
