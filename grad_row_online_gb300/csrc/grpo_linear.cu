@@ -550,6 +550,9 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // blocks each are added up in registers, rounded to nearest (fp32 operands,
 // and widths whose logits would be off by more than fp32 log-probs are).  kSets:
 // a logit's parts have accumulators of their own instead, one tile at a time.
+// (kParts spills: 128 sums and 32 operands a thread in the 168 registers that the
+// compiler has, 0.9 to 1.5 KB of stores in the code; the tensor pipe is busy 73 to
+// 86 % of the time, 91 to 95 without parts.)
 //
 // Bound by the tensor cores where tokens are many: a tile is 256 x 256, the most
 // that two sets of accumulators leave room for, so that an operand's element
@@ -560,7 +563,7 @@ __device__ __forceinline__ void results(const Product& g, const Tile& t, int ran
 // both products (91 %; the ends of its pieces); 16,384 tokens, 9,209 of them
 // taking part, x 2,048 x 151,936: 2.77 ms, 99.7 %.  Bound by memory up to 128
 // tokens, which take single CTAs with the weight as B: 64 x 4,096 x 32,768 in
-// 50 us, 5.4 TB/s, 64 x 4,096 x 151,936 in 186 to 190 us, 6.6 TB/s.  One tensor map
+// 50 us, 5.4 TB/s, 64 x 4,096 x 151,936 in 190 us, 6.6 TB/s.  One tensor map
 // a load of 64 elements (128 bytes) a row: what the swizzle holds; 6 to 12
 // stages of them in flight.
 //
